@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from typing import NamedTuple
 
 import torch
 
@@ -28,9 +29,11 @@ NOALLOC_SCRATCH_BYTES = 32 << 20
 DEV_SUM_CLAMPED, DEV_NEGATIVE_SIZE = 1, 2
 E4M3, E5M2 = 0, 1
 (OP_FWD, OP_SILU, OP_DLHS, OP_TGMM, OP_BF16_FWD, OP_BF16_DLHS, OP_FFN_FWD, OP_FFN_BWD, OP_FWD_VARIANT,
- OP_TGMM_DENSE) = range(10)
+ OP_TGMM_DENSE, OP_ROUTE, OP_MXFP4) = range(12)
 LHS_SCALE_BF16, ACC_BF16, RHS_SCALE_FIRST = 1, 2, 4
 GRAD_DTYPES = {"e4m3": E4M3, "e5m2": E5M2}
+F32, BF16 = 0, 1
+LOGIT_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 class Fp8GmmError(RuntimeError):
@@ -65,6 +68,16 @@ _SIGNATURES = {
     "gmm_bf16_fwd": [_P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _P],
     "gmm_bf16_silu": [_P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _P],
     "gmm_bf16_dlhs": [_P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _P],
+    "moe_route": [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P],
+    "moe_route_bwd": [_P, _P, _I32, _P, _P, _I64, _I32, _I32, _I32, _P, _P],
+    "moe_permute": [_P, _P, _I64, _I32, _I64, _I64, _P, _P],
+    "moe_permute_fp8": [_P, _P, _I64, _I32, _I64, _I64, _P, _P, _P],
+    "moe_combine": [_P, _P, _P, _I64, _I32, _I64, _I64, _P, _P],
+    "moe_combine_bwd": [_P, _P, _P, _P, _I64, _I32, _I64, _I64, _P, _P, _P],
+    "quantize_mxfp4_weights": [_P, _I64, _I64, _I32, _P, _P, _P],
+    "dequantize_mxfp4": [_P, _P, _I64, _I64, _I32, _P, _P],
+    "gmm_mxfp4_fwd": [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, _I32, _P, _P, _SZ, _P, _P],
+    "gmm_silu_mxfp4": [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, _I32, _P, _P, _SZ, _P, _P],
 }
 
 _lib = None
@@ -559,3 +572,211 @@ def gmm_bf16_dlhs(dout, w, group_sizes, *, out=None):
     with torch.cuda.device(dev):
         _call("gmm_bf16_dlhs", _ptr(dout), _ptr(w), _ptr(group_sizes), M, K, N, G, _ptr(out), None, _stream(dev))
     return out
+
+
+# --------------------------------------------------------------------------- routing, dispatch, combine
+
+class MoeRouting(NamedTuple):
+    """What moe_route returns; a slot is one of a token's k choices."""
+    ids: torch.Tensor          # int32 [T, k], -1 for a choice that found only masked logits
+    weights: torch.Tensor      # float32 [T, k]
+    group_sizes: torch.Tensor  # int32 [E]
+    row_of_slot: torch.Tensor  # int32 [T, k], -1 where ids is
+    slot_of_row: torch.Tensor  # int32 [T * k], -1 past the last slot's row
+
+
+def _req_logits(logits):
+    if isinstance(logits, torch.Tensor) and logits.dtype not in LOGIT_DTYPES:
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    _req(logits, "logits", getattr(logits, "dtype", None), 2)
+
+
+def _req_slots(t, name, dtype, T=None, k=None):
+    _req(t, name, dtype, 2)
+    if T is not None and tuple(t.shape) != (T, k):
+        raise ValueError(f"{name} must be [{T}, {k}], got {tuple(t.shape)}")
+
+
+def moe_route(logits, k, *, renormalize=True, workspace=None):
+    """The k largest of each token's router logits [T, E] (float32 or bfloat16;
+    -inf masks an expert), their softmax weights (over the chosen experts, or
+    over all without ``renormalize``) and the slots' stable sort by expert:
+    a MoeRouting."""
+    _req_logits(logits)
+    dev = logits.device
+    T, E = logits.shape
+    k = int(k)
+    if not 1 <= k <= E:
+        raise ValueError(f"k must be between 1 and the {E} experts, got {k}")
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    group_sizes = torch.empty((E,), dtype=torch.int32, device=dev)
+    row_of_slot = torch.empty((T, k), dtype=torch.int32, device=dev)
+    slot_of_row = torch.empty((T * k,), dtype=torch.int32, device=dev)
+    ws, need = _workspace(OP_ROUTE, T, E, k, 1, dev, tile_m=0, workspace=workspace)
+    with torch.cuda.device(dev):
+        _call("moe_route", _ptr(logits), LOGIT_DTYPES[logits.dtype], T, E, k, bool(renormalize), _ptr(ids),
+              _ptr(weights), _ptr(group_sizes), _ptr(row_of_slot), _ptr(slot_of_row), _ptr(ws), need, _stream(dev))
+    return MoeRouting(ids, weights, group_sizes, row_of_slot, slot_of_row)
+
+
+def moe_route_bwd(dweights, logits, ids, weights, *, renormalize=True, out=None):
+    """The gradient of moe_route's weights by its logits, in the logits' type
+    [T, E], from dweights [T, k] and the call's logits, ids and weights."""
+    _req_logits(logits)
+    T, E = logits.shape
+    _req_slots(ids, "ids", torch.int32)
+    k = ids.shape[1]
+    _req_slots(ids, "ids", torch.int32, T, k)
+    _req_slots(weights, "weights", torch.float32, T, k)
+    _req_slots(dweights, "dweights", torch.float32, T, k)
+    dev = _same_device(dweights, logits, ids, weights)
+    out = _out(out, (T, E), logits.dtype, dev, "out")
+    with torch.cuda.device(dev):
+        _call("moe_route_bwd", _ptr(dweights), _ptr(logits), LOGIT_DTYPES[logits.dtype], _ptr(ids), _ptr(weights), T,
+              E, k, bool(renormalize), _ptr(out), _stream(dev))
+    return out
+
+
+def _slots(x, name, row_of_slot, rows):
+    _req(x, name, torch.bfloat16, 2)
+    _req_slots(row_of_slot, "row_of_slot", torch.int32)
+    T, k = row_of_slot.shape
+    if rows is not None and x.shape[0] != T:
+        raise ValueError(f"{name} must have the {T} rows of row_of_slot, got {tuple(x.shape)}")
+    return _same_device(x, row_of_slot), T, k, x.shape[1]
+
+
+def moe_permute(x, row_of_slot, *, out=None):
+    """bf16 [R, H]: row row_of_slot[t, j] is x[t] (R = T * k, or the rows of
+    ``out``); rows that no slot names are left as they are."""
+    dev, T, k, H = _slots(x, "x", row_of_slot, True)
+    if out is None:
+        out = torch.empty((T * k, H), dtype=torch.bfloat16, device=dev)
+    _req(out, "out", torch.bfloat16, 2)
+    if out.shape[1] != H or out.device != dev:
+        raise ValueError(f"out must be [R, {H}] on {dev}, got {tuple(out.shape)} on {out.device}")
+    with torch.cuda.device(dev):
+        _call("moe_permute", _ptr(x), _ptr(row_of_slot), T, k, out.shape[0], H, _ptr(out), _stream(dev))
+    return out
+
+
+def moe_permute_fp8(x, row_of_slot, *, codes=None, scales=None):
+    """e4m3 codes [R, H] and f32 row scales [R] of moe_permute's rows, as
+    quantize_rows_fp8 gives them: the operands of gmm_fp8_fwd_q and
+    gmm_silu_fp8_q."""
+    dev, T, k, H = _slots(x, "x", row_of_slot, True)
+    R = T * k if codes is None else codes.shape[0]
+    codes = _out(codes, (R, H), torch.uint8, dev, "codes")
+    scales = _out(scales, (R,), torch.float32, dev, "scales")
+    _same_device(x, codes, scales)
+    with torch.cuda.device(dev):
+        _call("moe_permute_fp8", _ptr(x), _ptr(row_of_slot), T, k, R, H, _ptr(codes), _ptr(scales), _stream(dev))
+    return codes, scales
+
+
+def moe_combine(y, row_of_slot, weights=None, *, out=None):
+    """bf16 [T, H]: the sum of each token's rows of y [R, H] with its weights
+    [T, k]; without weights the plain sum, moe_permute's gradient."""
+    dev, T, k, H = _slots(y, "y", row_of_slot, None)
+    if weights is not None:
+        _req_slots(weights, "weights", torch.float32, T, k)
+    out = _out(out, (T, H), torch.bfloat16, dev, "out")
+    _same_device(y, weights, out)
+    with torch.cuda.device(dev):
+        _call("moe_combine", _ptr(y), _ptr(row_of_slot), _ptr(weights), T, k, y.shape[0], H, _ptr(out), _stream(dev))
+    return out
+
+
+def moe_combine_bwd(dout, y, row_of_slot, weights, *, dy=None, dweights=None):
+    """moe_combine's gradients from dout [T, H]: (dy bf16 [R, H], dweights f32
+    [T, k]).  Rows of dy that no slot names are left as they are."""
+    dev, T, k, H = _slots(dout, "dout", row_of_slot, True)
+    _req(y, "y", torch.bfloat16, 2)
+    if y.shape[1] != H:
+        raise ValueError(f"y must be [R, {H}], got {tuple(y.shape)}")
+    _req_slots(weights, "weights", torch.float32, T, k)
+    dy = _out(dy, tuple(y.shape), torch.bfloat16, dev, "dy")
+    dweights = _out(dweights, (T, k), torch.float32, dev, "dweights")
+    _same_device(dout, y, weights, dy, dweights)
+    with torch.cuda.device(dev):
+        _call("moe_combine_bwd", _ptr(dout), _ptr(y), _ptr(row_of_slot), _ptr(weights), T, k, y.shape[0], H, _ptr(dy),
+              _ptr(dweights), _stream(dev))
+    return dy, dweights
+
+
+# --------------------------------------------------------------------------- MXFP4
+
+def quantize_mxfp4_weights(w, *, codes=None, scales=None):
+    """MXFP4 codes u8 [G, N, K/2] and scales u8 [G, K/128, N, 4] of weights
+    w bf16 [G, K, N], in blocks of 32 along K."""
+    _req(w, "w", torch.bfloat16, 3)
+    G, K, N = w.shape
+    dev = w.device
+    codes = _out(codes, (G, N, K // 2), torch.uint8, dev, "codes")
+    scales = _out(scales, (G, K // 128, N, 4), torch.uint8, dev, "scales")
+    _same_device(w, codes, scales)
+    with torch.cuda.device(dev):
+        _call("quantize_mxfp4_weights", _ptr(w), K, N, G, _ptr(codes), _ptr(scales), _stream(dev))
+    return codes, scales
+
+
+def _mxfp4_shapes(codes, scales):
+    _req(codes, "codes", torch.uint8, 3)
+    _req(scales, "scales", torch.uint8, 4)
+    G, N, half = codes.shape
+    K = 2 * half
+    if tuple(scales.shape) != (G, K // 128, N, 4):
+        raise ValueError(f"scales must be [{G}, {K // 128}, {N}, 4] for codes {tuple(codes.shape)}, "
+                         f"got {tuple(scales.shape)}")
+    return G, K, N
+
+
+def dequantize_mxfp4(codes, scales, *, out=None):
+    """The values bf16 [G, N, K] of MXFP4 codes [G, N, K/2] and scales
+    [G, K/128, N, 4]."""
+    G, K, N = _mxfp4_shapes(codes, scales)
+    dev = _same_device(codes, scales)
+    out = _out(out, (G, N, K), torch.bfloat16, dev, "out")
+    _same_device(codes, out)
+    with torch.cuda.device(dev):
+        _call("dequantize_mxfp4", _ptr(codes), _ptr(scales), K, N, G, _ptr(out), _stream(dev))
+    return out
+
+
+def _mxfp4_product(name, x, codes, scales, group_sizes, slot_of_row, topk, out, dev_status, workspace, swiglu):
+    _req(x, "x", torch.bfloat16, 2)
+    G, K, N = _mxfp4_shapes(codes, scales)
+    _req(group_sizes, "group_sizes", torch.int32, 1)
+    T = x.shape[0]
+    M = T
+    if slot_of_row is not None:
+        _req(slot_of_row, "slot_of_row", torch.int32, 1)
+        M = slot_of_row.shape[0]
+    if x.shape[1] != K or group_sizes.shape[0] != G:
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)} codes {tuple(codes.shape)} "
+                         f"group_sizes {tuple(group_sizes.shape)}")
+    dev = _same_device(x, codes, scales, group_sizes, slot_of_row)
+    out = _out(out, (M, N // 2 if swiglu else N), torch.bfloat16, dev, "out")
+    _same_device(x, out)
+    ws, need = _workspace(OP_MXFP4, T, K, N, G, dev, tile_m=0, workspace=workspace)
+    with torch.cuda.device(dev):
+        _call(name, _ptr(x), _ptr(codes), _ptr(scales), _ptr(group_sizes), _ptr(slot_of_row), int(topk), T, M, K, N, G,
+              _ptr(out), _ptr(ws), need, _ptr(dev_status), _stream(dev))
+    return out
+
+
+def gmm_mxfp4_fwd(x, codes, scales, group_sizes, *, slot_of_row=None, topk=1, out=None, dev_status=None,
+                  workspace=None):
+    """Grouped product on 4-bit operands: x bf16 [T, K] is quantized to MXFP4 a
+    token, row r reads token slot_of_row[r] // topk (row r without slot_of_row);
+    bf16 [M, N]."""
+    return _mxfp4_product("gmm_mxfp4_fwd", x, codes, scales, group_sizes, slot_of_row, topk, out, dev_status,
+                          workspace, False)
+
+
+def gmm_silu_mxfp4(x, codes, scales, group_sizes, *, slot_of_row=None, topk=1, out=None, dev_status=None,
+                   workspace=None):
+    """gmm_mxfp4_fwd with SwiGLU over the columns [gate | up]; bf16 [M, N/2]."""
+    return _mxfp4_product("gmm_silu_mxfp4", x, codes, scales, group_sizes, slot_of_row, topk, out, dev_status,
+                          workspace, True)

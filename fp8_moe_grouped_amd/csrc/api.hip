@@ -411,9 +411,185 @@ int moe_ffn_fp8_bwd(const void* x, const void* h, const void* preact, const void
   return FP8GMM_OK;
 }
 
+static int check_route(int64_t T, int64_t E, int64_t k) {
+  if (T < 0 || E <= 0 || k <= 0 || k > E || T > kMaxRows / k) return FP8GMM_ERR_SHAPE;
+  if (E > kMaxGroups || k > kMaxTopk) return FP8GMM_ERR_UNSUPPORTED;
+  return FP8GMM_OK;
+}
+
+int moe_route(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t renormalize, int32_t* ids,
+              float* weights, int32_t* group_sizes, int32_t* row_of_slot, int32_t* slot_of_row, void* ws,
+              size_t ws_bytes, void* stream) {
+  if (!group_sizes) return FP8GMM_ERR_NULL;
+  int st = check_route(T, E, k);
+  if (st != FP8GMM_OK) return st;
+  if (T > 0 && (!logits || !ids || !weights || !row_of_slot || !slot_of_row)) return FP8GMM_ERR_NULL;
+  if (dtype != FP8GMM_F32 && dtype != FP8GMM_BF16) return FP8GMM_ERR_UNSUPPORTED;
+  if (!aligned16(logits) || !aligned16(ws)) return FP8GMM_ERR_ALIGN;
+  const size_t need = route_workspace_bytes((int)T, E);
+  if (need > 0 && (!ws || ws_bytes < need)) return FP8GMM_ERR_WORKSPACE;
+  if (launch_route(logits, dtype == FP8GMM_BF16, (int)T, E, k, renormalize != 0, ids, weights, group_sizes,
+                   row_of_slot, slot_of_row, ws, reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+int moe_route_bwd(const float* dweights, const void* logits, int32_t dtype, const int32_t* ids, const float* weights,
+                  int64_t T, int32_t E, int32_t k, int32_t renormalize, void* dlogits, void* stream) {
+  int st = check_route(T, E, k);
+  if (st != FP8GMM_OK) return st;
+  if (T > 0 && (!dweights || (!logits && !renormalize) || !ids || !weights || !dlogits)) return FP8GMM_ERR_NULL;
+  if (dtype != FP8GMM_F32 && dtype != FP8GMM_BF16) return FP8GMM_ERR_UNSUPPORTED;
+  if (!aligned16(logits) || !aligned16(dlogits)) return FP8GMM_ERR_ALIGN;
+  if (launch_route_bwd(dweights, logits, dtype == FP8GMM_BF16, ids, weights, (int)T, E, k, renormalize != 0, dlogits,
+                       reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+// T tokens of width H with k choices each, R buffer rows.
+static int check_slots(int64_t T, int64_t k, int64_t R, int64_t H) {
+  if (T < 0 || k <= 0 || R < 0 || R > kMaxRows || H <= 0 || T > kMaxRows / k) return FP8GMM_ERR_SHAPE;
+  if (k > kMaxTopk || H % 128 != 0 || H > kMaxK) return FP8GMM_ERR_UNSUPPORTED;
+  return FP8GMM_OK;
+}
+
+int moe_permute(const void* x, const int32_t* row_of_slot, int64_t T, int32_t k, int64_t R, int64_t H, void* out,
+                void* stream) {
+  int st = check_slots(T, k, R, H);
+  if (st != FP8GMM_OK) return st;
+  if (T > 0 && (!x || !row_of_slot || (R > 0 && !out))) return FP8GMM_ERR_NULL;
+  if (!aligned16(x) || !aligned16(out)) return FP8GMM_ERR_ALIGN;
+  if (T == 0 || R == 0) return FP8GMM_OK;
+  if (launch_permute(static_cast<const uint16_t*>(x), row_of_slot, (int)T, k, (int)R, (int)H,
+                     static_cast<uint16_t*>(out), reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+int moe_permute_fp8(const void* x, const int32_t* row_of_slot, int64_t T, int32_t k, int64_t R, int64_t H,
+                    uint8_t* codes_out, float* scale_out, void* stream) {
+  int st = check_slots(T, k, R, H);
+  if (st != FP8GMM_OK) return st;
+  if (T > 0 && (!x || !row_of_slot || (R > 0 && (!codes_out || !scale_out)))) return FP8GMM_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes_out)) return FP8GMM_ERR_ALIGN;
+  if (T == 0 || R == 0) return FP8GMM_OK;
+  if (launch_permute_fp8(static_cast<const uint16_t*>(x), row_of_slot, (int)T, k, (int)R, (int)H, codes_out,
+                         scale_out, reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+int moe_combine(const void* y, const int32_t* row_of_slot, const float* weights, int64_t T, int32_t k, int64_t R,
+                int64_t H, void* out, void* stream) {
+  int st = check_slots(T, k, R, H);
+  if (st != FP8GMM_OK) return st;
+  if (T > 0 && ((R > 0 && !y) || !row_of_slot || !out)) return FP8GMM_ERR_NULL;
+  if (!aligned16(y) || !aligned16(out)) return FP8GMM_ERR_ALIGN;
+  if (T == 0) return FP8GMM_OK;
+  if (launch_combine(static_cast<const uint16_t*>(y), row_of_slot, weights, (int)T, k, (int)R, (int)H,
+                     static_cast<uint16_t*>(out), reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+int moe_combine_bwd(const void* dout, const void* y, const int32_t* row_of_slot, const float* weights, int64_t T,
+                    int32_t k, int64_t R, int64_t H, void* dy, float* dweights, void* stream) {
+  int st = check_slots(T, k, R, H);
+  if (st != FP8GMM_OK) return st;
+  if (T > 0 && (!dout || (R > 0 && (!y || !dy)) || !row_of_slot || !weights || !dweights)) return FP8GMM_ERR_NULL;
+  if (!aligned16(dout) || !aligned16(y) || !aligned16(dy)) return FP8GMM_ERR_ALIGN;
+  if (T == 0) return FP8GMM_OK;
+  if (launch_combine_bwd(static_cast<const uint16_t*>(dout), static_cast<const uint16_t*>(y), row_of_slot, weights,
+                         (int)T, k, (int)R, (int)H, static_cast<uint16_t*>(dy), dweights,
+                         reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+int quantize_mxfp4_weights(const void* w, int64_t K, int64_t N, int32_t G, uint8_t* codes_out, uint8_t* scale_out,
+                           void* stream) {
+  int st = check_common(0, K, N, G);   // sizes first: a K below 128 leaves a caller without scales
+  if (st != FP8GMM_OK) return st;
+  if (K > kMaxK) return FP8GMM_ERR_UNSUPPORTED;
+  if (!w || !codes_out || !scale_out) return FP8GMM_ERR_NULL;
+  if (!aligned16(w) || !aligned16(codes_out) || !aligned16(scale_out)) return FP8GMM_ERR_ALIGN;
+  if (launch_quant_weights_mxfp4(static_cast<const uint16_t*>(w), G, (int)K, (int)N, codes_out, scale_out,
+                                 reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+int dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale, int64_t K, int64_t N, int32_t G, void* out,
+                     void* stream) {
+  if (!codes || !scale || !out) return FP8GMM_ERR_NULL;
+  int st = check_common(0, K, N, G);
+  if (st != FP8GMM_OK) return st;
+  if (K > kMaxK || N > kMaxMxfp4N) return FP8GMM_ERR_UNSUPPORTED;
+  if (!aligned16(codes) || !aligned16(scale) || !aligned16(out)) return FP8GMM_ERR_ALIGN;
+  if (launch_dequant_mxfp4(codes, scale, G, (int)N, (int)K, static_cast<uint16_t*>(out),
+                           reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+// MXFP4 product's workspace: the tokens' codes [T + 1, K/2], then their scales [T + 1, K/32].
+static size_t mxfp4_ws(int64_t T, int64_t K) {
+  return align_up((size_t)(T + 1) * (K / 2)) + align_up((size_t)(T + 1) * (K / 32));
+}
+
+static int check_mxfp4(int64_t T, int64_t M, int64_t K, int64_t N, int32_t G) {
+  int st = check_common(M, K, N, G);
+  if (st != FP8GMM_OK) return st;
+  if (T < 0 || T > kMaxRows) return FP8GMM_ERR_SHAPE;
+  if (K > kMaxK || N > kMaxMxfp4N) return FP8GMM_ERR_UNSUPPORTED;
+  return FP8GMM_OK;
+}
+
+static int mxfp4_common(const void* x, const uint8_t* codes, const uint8_t* scale, const int32_t* group_sizes,
+                        const int32_t* slot_of_row, int32_t topk, int64_t T, int64_t M, int64_t K, int64_t N,
+                        int32_t G, void* out, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream,
+                        bool swiglu) {
+  if (!codes || !scale || !group_sizes) return FP8GMM_ERR_NULL;
+  int st = check_mxfp4(T, M, K, N, G);
+  if (st != FP8GMM_OK) return st;
+  if (topk <= 0 || (!slot_of_row && T != M)) return FP8GMM_ERR_SHAPE;
+  if (M > 0 && ((T > 0 && !x) || !out)) return FP8GMM_ERR_NULL;
+  if (swiglu && ((N / 2) % 128 != 0)) return FP8GMM_ERR_UNSUPPORTED;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scale) || !aligned16(out) || !aligned16(ws))
+    return FP8GMM_ERR_ALIGN;
+  if (M > 0 && (!ws || ws_bytes < mxfp4_ws(T, K))) return FP8GMM_ERR_WORKSPACE;
+  if (M == 0) return FP8GMM_OK;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  uint8_t* aq = static_cast<uint8_t*>(ws);
+  uint8_t* as = aq + align_up((size_t)(T + 1) * (K / 2));
+  if (launch_quant_rows_mxfp4(static_cast<const uint16_t*>(x), (int)T, (int)K, aq, as, s) != hipSuccess ||
+      launch_gmm_mxfp4(aq, as, codes, scale, group_sizes, slot_of_row, topk, (int)T, G, (int)M, (int)K, (int)N, swiglu,
+                       static_cast<uint16_t*>(out), dev_status, s) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+int gmm_mxfp4_fwd(const void* x, const uint8_t* codes, const uint8_t* scale, const int32_t* group_sizes,
+                  const int32_t* slot_of_row, int32_t topk, int64_t T, int64_t M, int64_t K, int64_t N, int32_t G,
+                  void* out, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  return mxfp4_common(x, codes, scale, group_sizes, slot_of_row, topk, T, M, K, N, G, out, ws, ws_bytes, dev_status,
+                      stream, false);
+}
+
+int gmm_silu_mxfp4(const void* x, const uint8_t* codes, const uint8_t* scale, const int32_t* group_sizes,
+                   const int32_t* slot_of_row, int32_t topk, int64_t T, int64_t M, int64_t K, int64_t N, int32_t G,
+                   void* out, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  return mxfp4_common(x, codes, scale, group_sizes, slot_of_row, topk, T, M, K, N, G, out, ws, ws_bytes, dev_status,
+                      stream, true);
+}
+
 size_t fp8gmm_workspace_bytes(int32_t op, int64_t M, int64_t K, int64_t N, int32_t G, int32_t tile_m) {
+  if (op == FP8GMM_OP_ROUTE) return check_route(M, K, N) == FP8GMM_OK ? route_workspace_bytes((int)M, (int)K) : 0;
   if (check_common(M, K, N, G) != FP8GMM_OK) return 0;
   switch (op) {
+    case FP8GMM_OP_MXFP4:
+      return check_mxfp4(M, M, K, N, G) == FP8GMM_OK ? mxfp4_ws(M, K) : 0;
     case FP8GMM_OP_FWD:
     case FP8GMM_OP_SILU:
       return fwd_ws(M, K);

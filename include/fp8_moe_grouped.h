@@ -6,7 +6,9 @@
  *   "MoE: native FP8 QAT for routed-expert GMMs" (maxtext PR #5969), with its
  *   conversation page, and "MoE fp8 backward: in-kernel drhs operand
  *   quantization + configurable gradient dtype" (maxtext PR #4971).
- * Each declaration names the page and the section it follows.
+ * Each declaration names the page and the section it follows.  The calls around
+ * that path (moe_route to moe_combine_bwd, and the MXFP4 calls) are defined by
+ * their formulas alone.
  *
  * Common conventions
  * ------------------
@@ -72,6 +74,12 @@ extern "C" {
 #define FP8GMM_OP_FFN_BWD 7   /* moe_ffn_fp8_bwd: pass K = H, N = I, tile_m = 512 */
 #define FP8GMM_OP_FWD_VARIANT 8 /* gmm_fp8_fwd_variant: pass lhs_block as tile_m */
 #define FP8GMM_OP_TGMM_DENSE 9  /* tgmm_dense_quant */
+#define FP8GMM_OP_ROUTE 10      /* moe_route: pass M = T, K = E, N = k, G = 1 */
+#define FP8GMM_OP_MXFP4 11      /* gmm_mxfp4_fwd, gmm_silu_mxfp4: pass M = T (rows of x) */
+
+/* types of the router's logits */
+#define FP8GMM_F32 0
+#define FP8GMM_BF16 1
 
 /* flags of gmm_fp8_fwd_variant */
 #define FP8GMM_LHS_SCALE_BF16 1   /* round each activation scale to bf16 */
@@ -330,6 +338,103 @@ int moe_ffn_fp8_bwd(const void* x, const void* h, const void* preact, const void
                     const int32_t* group_sizes, int64_t M, int64_t H, int64_t I, int32_t G, int32_t grad_dtype,
                     void* d_preact, void* dx, float* dwi, float* dwo, void* ws, size_t ws_bytes,
                     int32_t* dev_status, void* stream);
+
+/*
+ * Routing.  A slot is one of a token's k choices: slot t*k + j is choice j of
+ * token t.  1 <= k <= min(E, 32), E <= 1024, T*k < 2^24.
+ *
+ * moe_route -- the k largest of each token's E logits, their softmax weights,
+ * and the stable sort of all slots by expert:
+ *   ids[t, j]      the j-th largest logit's expert (ties: the lower expert first;
+ *                  NaN is above every number); -inf is masked and never chosen:
+ *                  a choice that finds nothing else has id -1 and weight 0
+ *   weights[t, j]  exp(x[t, ids] - m) / sum exp(x[t, e] - m), the sum over the
+ *                  chosen e (renormalize != 0) or over all e; NaN if the token
+ *                  has a NaN or +inf among them
+ *   group_sizes[e] number of slots of expert e: the sizes the grouped matmuls take
+ *   row_of_slot    [T, k]: the slot's row of the ragged buffer, experts in order,
+ *                  the slots of an expert in theirs; -1 for an id of -1
+ *   slot_of_row    [T*k]: the inverse; -1 at rows past the last slot's
+ * logits f32 or bf16 (dtype FP8GMM_F32 / FP8GMM_BF16) [T, E]; ids, row_of_slot
+ * i32 [T, k]; weights f32 [T, k]; group_sizes i32 [E]; slot_of_row i32 [T*k].
+ * ws: fp8gmm_workspace_bytes(FP8GMM_OP_ROUTE, T, E, k, 1, 0) bytes (0 for few tokens).
+ *
+ * moe_route_bwd -- the logits' gradient from dweights f32 [T, k] and the call's
+ * inputs and outputs, with s = sum_j weights * dweights over the chosen:
+ *   renormalize: dlogits[t, ids[t,j]] = weights (dweights - s), 0 elsewhere
+ *   otherwise:   dlogits[t, e] = [e = ids[t,j]] weights dweights - softmax(x[t])[e] * s
+ * A choice with id -1 adds nothing and its dweights is not read; a token whose
+ * logits are all -inf gets zeros.  Sums in f32, rounded once to the logits'
+ * type.  logits may be NULL with renormalize.  dlogits [T, E].
+ */
+int moe_route(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t renormalize, int32_t* ids,
+              float* weights, int32_t* group_sizes, int32_t* row_of_slot, int32_t* slot_of_row, void* ws,
+              size_t ws_bytes, void* stream);
+int moe_route_bwd(const float* dweights, const void* logits, int32_t dtype, const int32_t* ids, const float* weights,
+                  int64_t T, int32_t E, int32_t k, int32_t renormalize, void* dlogits, void* stream);
+
+/*
+ * Tokens [T, H] to the R rows of a ragged buffer and back, by row_of_slot
+ * i32 [T, k] (from moe_route, or any map that gives no row twice).  A row
+ * outside [0, R) is neither read nor written and counts as zero.  Buffer rows
+ * that no slot names are not written.  H a multiple of 128, at most 16384;
+ * k <= 32, T*k < 2^24, R < 2^24.
+ *
+ * moe_permute:     out[row_of_slot[t,j], :] = x[t, :]                   bf16 [R, H]
+ * moe_permute_fp8: codes_out u8 [R, H] and scale_out f32 [R] of the same rows,
+ *   quantized as quantize_rows_fp8 does (bit for bit): the FP8 forward's
+ *   operands (gmm_fp8_fwd_q, gmm_silu_fp8_q) without a bf16 buffer between
+ * moe_combine:     out[t, :] = bf16( sum_j weights[t,j] * y[row_of_slot[t,j], :] ),
+ *   f32, j ascending; without weights (NULL) the plain sum, which is also
+ *   moe_permute's gradient.  y bf16 [R, H], weights f32 [T, k], out bf16 [T, H]
+ * moe_combine_bwd: dy[row_of_slot[t,j], :] = bf16( weights[t,j] * dout[t, :] ),
+ *   dweights[t,j] = sum_h dout[t,h] * y[row_of_slot[t,j], h] (f32; 0 for a row
+ *   outside the buffer).  The gradient without weights is moe_permute(dout).
+ */
+int moe_permute(const void* x, const int32_t* row_of_slot, int64_t T, int32_t k, int64_t R, int64_t H, void* out,
+                void* stream);
+int moe_permute_fp8(const void* x, const int32_t* row_of_slot, int64_t T, int32_t k, int64_t R, int64_t H,
+                    uint8_t* codes_out, float* scale_out, void* stream);
+int moe_combine(const void* y, const int32_t* row_of_slot, const float* weights, int64_t T, int32_t k, int64_t R,
+                int64_t H, void* out, void* stream);
+int moe_combine_bwd(const void* dout, const void* y, const int32_t* row_of_slot, const float* weights, int64_t T,
+                    int32_t k, int64_t R, int64_t H, void* dy, float* dweights, void* stream);
+
+/*
+ * MXFP4: 4-bit e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) in
+ * blocks of 32 along K that share an E8M0 scale byte b, the power 2^(b - 127):
+ *   b    = max(floor(log2 max|x|) - 2, -127) + 127 (0 for a block of zeros; 255,
+ *          which makes every value NaN, if the block holds an Inf or a NaN)
+ *   code = e2m1(x / 2^(b - 127)), nearest even, saturating at 6, zeros signed
+ * Weight codes are u8 [G, N, K/2], the even k of a pair in the low half byte;
+ * scales u8 [G, K/128, N, 4], the four blocks of 128 k of a column together.
+ * K and N multiples of 128, K <= 16384, N <= 65536 for the product and the values.
+ *
+ * quantize_mxfp4_weights: codes and scales of w bf16 [G, K, N] (K contracted, as
+ *   the bf16 arm's weights).
+ * dequantize_mxfp4: their values bf16 [G, N, K] (exact).
+ *
+ * gmm_mxfp4_fwd -- grouped product on 4-bit operands, gathering its rows: row r
+ * of expert g (group_sizes as everywhere) is token slot_of_row[r] / topk of
+ * x bf16 [T, K], or row r itself when slot_of_row is NULL (then T = M).  With
+ * q(.) the MXFP4 values of x's blocks and w the weights' values:
+ *   out[r, n] = bf16( sum_k q(x)[token, k] * w[g, n, k] )      f32 accumulation
+ * out bf16 [M, N]; rows >= sum(group_sizes) are neither read nor written.  A
+ * slot outside [0, T*topk) gives a row of zeros.
+ * gmm_silu_mxfp4: N = 2I columns [gate | up]; out bf16 [M, I] =
+ *   bf16( silu(y[r, i]) * y[r, I + i] ) of the f32 products y.  I % 128 == 0.
+ * ws: fp8gmm_workspace_bytes(FP8GMM_OP_MXFP4, T, K, N, G, 0) bytes.
+ */
+int quantize_mxfp4_weights(const void* w, int64_t K, int64_t N, int32_t G, uint8_t* codes_out, uint8_t* scale_out,
+                           void* stream);
+int dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale, int64_t K, int64_t N, int32_t G, void* out,
+                     void* stream);
+int gmm_mxfp4_fwd(const void* x, const uint8_t* codes, const uint8_t* scale, const int32_t* group_sizes,
+                  const int32_t* slot_of_row, int32_t topk, int64_t T, int64_t M, int64_t K, int64_t N, int32_t G,
+                  void* out, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+int gmm_silu_mxfp4(const void* x, const uint8_t* codes, const uint8_t* scale, const int32_t* group_sizes,
+                   const int32_t* slot_of_row, int32_t topk, int64_t T, int64_t M, int64_t K, int64_t N, int32_t G,
+                   void* out, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /*
  * fp8gmm_workspace_bytes -- device workspace the call `op` needs for these

@@ -1,0 +1,253 @@
+"""GPU tests of the MXFP4 calls: codes, scales and values bit for bit; products
+within f32 accumulation and half a bf16 step of the plain 64-bit definition."""
+import math
+
+import pytest
+import torch
+
+from tests import plain_moe as P
+
+pytestmark = pytest.mark.gpu
+
+
+def special(w):
+    """Blocks of zeros, signed zeros, ties, subnormals, the largest values."""
+    flat = w.view(-1, w.shape[-1])                   # [.., N]: columns are channels
+    flat[:32, 0] = 0
+    flat[:32, 1] = -0.0
+    flat[:16, 2] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, 6, -0.25, -0.75, -1.25, -1.75, -2.5, -3.5, -5, -7.9])
+    flat[16:32, 2] = 0
+    flat[:32, 3] = 2.0 ** -133
+    flat[:32, 4] = 3.38e38
+    flat[:32, 5] = torch.linspace(-2.0 ** -124, 2.0 ** -125, 32)
+    return w
+
+
+@pytest.mark.parametrize("G_,K,N", [(1, 128, 128), (3, 384, 256), (2, 640, 384), (1, 7168, 128), (5, 256, 640)])
+def test_weights(G_, K, N):
+    import fp8_moe_grouped_amd as G
+    w = torch.randn((G_, K, N), generator=torch.Generator().manual_seed(K)) * 0.02
+    w = special(w).to(torch.bfloat16)
+    code, byte = P.mxfp4(w.transpose(1, 2))
+    want_c, want_s = P.pack_weights(code, byte)
+    codes, scales = G.quantize_mxfp4_weights(w.cuda())
+    assert torch.equal(codes.cpu(), want_c) and torch.equal(scales.cpu(), want_s)
+    values = G.dequantize_mxfp4(codes, scales).cpu()
+    want = P.mxfp4_values(code, byte).to(torch.bfloat16)
+    assert torch.equal(values.view(torch.int16), want.view(torch.int16))
+
+
+def test_weights_not_finite():
+    import fp8_moe_grouped_amd as G
+    w = torch.ones((1, 128, 128), dtype=torch.bfloat16)
+    w[0, 3, 0], w[0, 40, 1], w[0, 127, 2] = math.nan, math.inf, -math.inf
+    codes, scales = G.quantize_mxfp4_weights(w.cuda())
+    s = scales.cpu()[0, 0]
+    assert s[0].tolist() == [255, 125, 125, 125] and s[1].tolist() == [125, 255, 125, 125]
+    assert s[2].tolist() == [125, 125, 125, 255]
+    nan = torch.isnan(G.dequantize_mxfp4(codes, scales)).cpu()[0]
+    assert nan[0, :32].all() and nan[1, 32:64].all() and nan[2, 96:].all() and int(nan.sum()) == 96
+
+
+def activations(T, K, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((T, K), generator=g)
+    return torch.where(torch.rand((T, K), generator=g) < 0.01, 50 * x, x).to(torch.bfloat16)
+
+
+def weights(G_, N, K, seed):
+    g = torch.Generator().manual_seed(seed)
+    code = torch.randint(0, 16, (G_, N, K), generator=g, dtype=torch.uint8)
+    byte = torch.randint(118, 124, (G_, N, K // 32), generator=g, dtype=torch.uint8)
+    return code, byte
+
+
+def product(x, code, byte, sizes, tokens):
+    """(sum, sum of magnitudes) in float64 of the valid rows."""
+    a = P.mxfp4_values(*P.mxfp4(x))
+    y, mag, at = [], [], 0
+    for g, n in enumerate(sizes):
+        w = P.mxfp4_values(code[g], byte[g])
+        rows = torch.where((tokens[at:at + n] >= 0).unsqueeze(1), a[tokens[at:at + n].clamp(min=0)], 0.0)
+        y.append(rows @ w.t())
+        mag.append(rows.abs() @ w.abs().t())
+        at += n
+    return torch.cat(y), torch.cat(mag)
+
+
+def check(out, y, mag, K, swiglu):
+    # each instruction adds the sums of four blocks to f32: four roundings of at most the magnitudes'
+    # sum, twice over for an adder that cuts off; a few more where partial sums are joined
+    e = mag * 2.0 ** -23 * (4 * K / 128 + 16)
+    if swiglu:
+        I = y.shape[1] // 2
+        g, u, eg, eu = y[:, :I], y[:, I:], e[:, :I], e[:, I:]
+        sig = torch.sigmoid(g)
+        silu, slope = g * sig, (sig * (1 + g * (1 - sig))).abs()
+        # first order, the second order of the small errors, and the f32 evaluation (exp's argument, reciprocal)
+        e = slope * u.abs() * eg + silu.abs() * eu + eg * eu * 1.1 + 0.5 * eg * eg * u.abs() \
+            + 2.0 ** -20 * (4 + g.abs()) * (silu * u).abs()
+        y = silu * u
+    got = out.cpu().double()
+    tol = e + y.abs() * 2.0 ** -8 + 2.0 ** -126
+    bad = (got - y).abs() > tol
+    assert not bool(bad.any()), (int(bad.sum()), float(((got - y).abs() / tol).max()))
+
+
+def sizes_of(M, G_, seed, empty=True):
+    g = torch.Generator().manual_seed(seed)
+    p = torch.rand(G_, generator=g) ** 2
+    if empty and G_ > 2:
+        p[1] = 0
+    n = (p / p.sum() * M).floor().int()
+    n[-1] += M - int(n.sum())
+    return n
+
+
+GEMM = [(1, 1, 1, 128, 256), (1, 8, 8, 7168, 256), (3, 2, 5, 384, 512), (17, 1, 2, 256, 256), (33, 4, 4, 640, 768),
+        (100, 3, 7, 1152, 512), (257, 1, 1, 512, 256), (300, 4, 6, 896, 1280), (64, 2, 32, 128, 256),
+        (1500, 2, 3, 256, 512), (2100, 1, 2, 768, 1024)]
+
+
+@pytest.mark.parametrize("T,k,G_,K,N", GEMM)
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_product(T, k, G_, K, N, swiglu):
+    """Gathered rows, ragged and empty groups, rows past the valid prefix, slots without a token."""
+    import fp8_moe_grouped_amd as G
+    M = T * k
+    g = torch.Generator().manual_seed(T)
+    tail = M // 10
+    sizes = sizes_of(M - tail, G_, K)
+    slots = torch.randperm(M, generator=g).int()
+    if M > 4:
+        slots[1], slots[3] = -1, M + 5               # no token: zeros
+    x = activations(T, K, T)
+    code, byte = weights(G_, N, K, N)
+    codes, scales = P.pack_weights(code, byte)
+    tokens = torch.where((slots >= 0) & (slots < M), slots // k, -1).long()
+    n = M - tail
+    slots[n:] = torch.iinfo(torch.int32).max
+    out = torch.full((M, N // 2 if swiglu else N), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    f = G.gmm_silu_mxfp4 if swiglu else G.gmm_mxfp4_fwd
+    f(x.cuda(), codes.cuda(), scales.cuda(), sizes.cuda(), slot_of_row=slots.cuda(), topk=k, out=out, dev_status=status)
+    y, mag = product(x, code, byte, sizes.tolist(), tokens)
+    assert int(status) == 0 and bool((out[n:] == 7.0).all())
+    check(out[:n], y, mag, K, swiglu)
+
+
+@pytest.mark.parametrize("M,N", [(9, 128), (70, 384), (900, 640)])
+def test_product_plain_rows(M, N):
+    """Without a map, and N a multiple of 128 only."""
+    import fp8_moe_grouped_amd as G
+    K = 512
+    x = activations(M, K, 1)
+    code, byte = weights(3, N, K, 2)
+    codes, scales = P.pack_weights(code, byte)
+    sizes = sizes_of(M, 3, 5)
+    out = G.gmm_mxfp4_fwd(x.cuda(), codes.cuda(), scales.cuda(), sizes.cuda())
+    check(out, *product(x, code, byte, sizes.tolist(), torch.arange(M)), K, False)
+
+
+def test_product_not_finite():
+    """An Inf or NaN activation makes its own rows NaN, a NaN scale its own column."""
+    import fp8_moe_grouped_amd as G
+    x = activations(40, 256, 1)
+    x[3, 7], x[20, 200] = math.inf, math.nan
+    code, byte = weights(2, 256, 256, 2)
+    code = code & 7 | 1                              # no zero codes
+    byte[1, 5, 2] = 255
+    codes, scales = P.pack_weights(code, byte)
+    sizes = torch.tensor([15, 25], dtype=torch.int32)
+    out = G.gmm_mxfp4_fwd(x.cuda(), codes.cuda(), scales.cuda(), sizes.cuda()).cpu()
+    nan = torch.isnan(out)
+    want = torch.zeros_like(nan)
+    want[3] = want[20] = True
+    want[15:, 5] = True
+    assert torch.equal(nan, want) and bool(torch.isfinite(out[~want]).all())
+
+
+def test_product_repairs_sizes():
+    import fp8_moe_grouped_amd as G
+    x = activations(20, 256, 1)
+    code, byte = weights(3, 256, 256, 2)
+    codes, scales = P.pack_weights(code, byte)
+    for sizes, fixed, flags in (([-4, 8, 30], [0, 8, 12], G.DEV_NEGATIVE_SIZE | G.DEV_SUM_CLAMPED), ([0, 0, 0], [0, 0, 0], 0),
+                                ([3, 2, 1], [3, 2, 1], 0)):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full((20, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+        G.gmm_mxfp4_fwd(x.cuda(), codes.cuda(), scales.cuda(), torch.tensor(sizes, dtype=torch.int32).cuda(), out=out,
+                        dev_status=st)
+        n = sum(fixed)
+        assert int(st) == flags and bool((out[n:] == 7.0).all())
+        if n:
+            check(out[:n], *product(x, code, byte, fixed, torch.arange(20)), 256, False)
+
+
+def test_product_agrees_with_values():
+    """gmm_bf16_fwd on the dequantized weights and activations gives the same product."""
+    import fp8_moe_grouped_amd as G
+    M, K, N, G_ = 500, 1024, 512, 4
+    x = activations(M, K, 1)
+    w = (0.02 * torch.randn((G_, K, N), generator=torch.Generator().manual_seed(2))).to(torch.bfloat16)
+    sizes = sizes_of(M, G_, 3).cuda()
+    codes, scales = G.quantize_mxfp4_weights(w.cuda())
+    got = G.gmm_mxfp4_fwd(x.cuda(), codes, scales, sizes).float()
+    xv = P.mxfp4_values(*P.mxfp4(x)).to(torch.bfloat16).cuda()
+    wv = G.dequantize_mxfp4(codes, scales).transpose(1, 2).contiguous()
+    ref = G.gmm_bf16_fwd(xv, wv, sizes).float()
+    assert float((got - ref).norm() / ref.norm()) < 2.0 ** -8
+
+
+def test_product_graph_and_stream():
+    import fp8_moe_grouped_amd as G
+    M, K, N, G_ = 96, 768, 512, 5
+    code, byte = weights(G_, N, K, 2)
+    codes, scales = (t.cuda() for t in P.pack_weights(code, byte))
+    xs = [activations(M, K, s).cuda() for s in range(3)]
+    sz = [sizes_of(M, G_, s).cuda() for s in range(3)]
+    eager = [G.gmm_silu_mxfp4(x, codes, scales, s) for x, s in zip(xs, sz)]
+    x, s = xs[0].clone(), sz[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = G.gmm_silu_mxfp4(x, codes, scales, s)
+    for i in (0, 1, 2, 1):
+        x.copy_(xs[i])
+        s.copy_(sz[i])
+        graph.replay()
+        G.gmm_silu_mxfp4(xs[(i + 1) % 3], codes, scales, sz[0])
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager[i])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out = G.gmm_silu_mxfp4(xs[2], codes, scales, sz[2])
+    side.synchronize()
+    assert torch.equal(out, eager[2])
+
+
+def test_refusals():
+    import fp8_moe_grouped_amd as G
+    w = torch.zeros((2, 256, 256), dtype=torch.bfloat16, device="cuda")
+    codes, scales = G.quantize_mxfp4_weights(w)
+    x = torch.zeros((8, 256), dtype=torch.bfloat16, device="cuda")
+    sizes = torch.tensor([4, 4], dtype=torch.int32, device="cuda")
+    for call in (lambda: G.quantize_mxfp4_weights(w[:, :, :128]), lambda: G.dequantize_mxfp4(codes, scales[:1]),
+                 lambda: G.gmm_mxfp4_fwd(x[:, :128].contiguous(), codes, scales, sizes),
+                 lambda: G.gmm_mxfp4_fwd(x, codes, scales, sizes[:1]),
+                 lambda: G.gmm_mxfp4_fwd(x, codes, scales, sizes, out=x[:4]),
+                 lambda: G.gmm_mxfp4_fwd(x, codes, scales, sizes, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        G.quantize_mxfp4_weights(w.float())
+    with pytest.raises(TypeError):
+        G.gmm_mxfp4_fwd(x, codes, scales, sizes, slot_of_row=sizes.long())
+    with pytest.raises(G.Fp8GmmError) as e:
+        G.quantize_mxfp4_weights(torch.zeros((1, 96, 128), dtype=torch.bfloat16, device="cuda"))
+    assert e.value.status == G.ERR_UNSUPPORTED
+    with pytest.raises(G.Fp8GmmError) as e:
+        G.gmm_mxfp4_fwd(x, codes, scales, sizes, topk=0)
+    assert e.value.status == G.ERR_SHAPE
+    assert G.gmm_mxfp4_fwd(x[:0], codes, scales, sizes).shape == (0, 256)
