@@ -533,9 +533,10 @@ int dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale, int64_t K, int6
   return FP8GMM_OK;
 }
 
-// MXFP4 product's workspace: the tokens' codes [T + 1, K/2], then their scales [T + 1, K/32].
+// MXFP4 product's workspace: the tokens' codes [T + 1, K/2], then their scales [T + 1, K/32],
+// a row padded to 16 bytes.
 static size_t mxfp4_ws(int64_t T, int64_t K) {
-  return align_up((size_t)(T + 1) * (K / 2)) + align_up((size_t)(T + 1) * (K / 32));
+  return align_up((size_t)(T + 1) * (K / 2)) + align_up((size_t)(T + 1) * ((K + 511) / 512 * 16));
 }
 
 static int check_mxfp4(int64_t T, int64_t M, int64_t K, int64_t N, int32_t G) {

@@ -18,6 +18,7 @@
 #include "launch.hpp"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace fp8gmm {
 namespace {
@@ -65,7 +66,7 @@ __global__ __launch_bounds__(64 * kWaves) void gmm_mxfp4_split_kernel(
       token = slot < 0 ? T : min(slot / topk, T);   // row T of the quantized activations is zero
     }
     ap[i] = aq + (size_t)token * (K / 2) + 16 * q;
-    as[i] = ascale + (size_t)token * kw;
+    as[i] = ascale + (size_t)token * ((kw + 3) & ~3);
   }
   int col[2];
 #pragma unroll
@@ -139,17 +140,275 @@ __global__ __launch_bounds__(64 * kWaves) void gmm_mxfp4_split_kernel(
   }
 }
 
+// ---------------------------------------------------------------- large tiles
+
+// Many rows: a block owns up to 256 rows x 256 columns (SwiGLU: 128 gate and the
+// matching 128 up) of one expert.  Four waves, one per SIMD, 2 x 2: with 128 x 128
+// a wave the operands read from LDS stay below its bandwidth (64 KB a stage of 128
+// k against 1024 cycles of matrix instructions; eight waves of 64 x 128 would read
+// 96 KB beside the 32 KB that arrive).  An expert's rows are cut into tiles of
+// nearly equal counts of 64 rows, and a wave's instructions follow the tile's
+// count (MI fragments of 32 rows), so a short tile takes proportionally less time.
+//
+// The contraction advances 128 k (64 bytes a row) a stage through a ring of four
+// stages in LDS, filled by buffer loads with the LDS destination.  While a stage's
+// matrix instructions issue from one register set, the next stage's operands are
+// read into the other, and the copies of the stage four ahead go to the slot that
+// was just read.  Scale words (four blocks of 32 k) arrive four stages at a time.
+constexpr int BM = 256, BN = 256, BK = 64;          // BK in bytes: 128 k
+constexpr int kStages = 4;
+constexpr int kRingBytes = kStages * (BM + BN) * BK;
+constexpr int kScaleSlot = BM * 16 + 4 * BN * 4;    // four stages' scale words, rows then columns
+constexpr int kTileLds = kRingBytes + 2 * kScaleSlot;
+static_assert(kTileLds + sizeof(int) * (3 * kMaxGroups + 1) <= 160 * 1024, "ring, scales and expert table fit the LDS");
+
+__device__ __forceinline__ int swz(int row, int chunk) { return row * BK + ((chunk ^ ((row >> 2) & 3)) << 4); }
+
+template <int SEL>
+__device__ __forceinline__ v16f mfma_mxfp4_32(const v4i& a, const v4i& b, const v16f& c, int sa, int sb) {
+  const v8i a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, SEL, sa, SEL, sb);
+}
+
+template <bool SWIGLU>
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(1, 1)))
+void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __restrict__ ascale,
+                           const uint8_t* __restrict__ codes, const uint8_t* __restrict__ wscale,
+                           const int* __restrict__ group_sizes, const int* __restrict__ slot_of_row, int topk, int T,
+                           int G, int M, int K, int N, uint16_t* __restrict__ out, int* status) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  int* const t_start = reinterpret_cast<int*>(smem + kTileLds);
+  int* const t_end = t_start + G;
+  int* const t_pre = t_end + G;
+  build_group_table(group_sizes, G, M, BM, GroupTable{t_start, t_end, t_pre}, status);
+  __syncthreads();
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int half = N >> 1;
+  const int n_tiles = SWIGLU ? half / (BN / 2) : (N + BN - 1) / BN;
+  const int tiles = t_pre[G];
+  if ((int)blockIdx.x >= tiles * n_tiles) return;
+  int mt, nt;
+  raster_tile<8>(blockIdx.x, tiles, n_tiles, mt, nt);
+  nt = __builtin_amdgcn_readfirstlane(nt);
+  const int g = __builtin_amdgcn_readfirstlane(find_group(t_pre, G, mt));
+  // this tile's share of the expert's units of 64 rows
+  const int g0 = t_start[g], g1 = t_end[g], part = mt - t_pre[g];
+  const int parts = (g1 - g0 + BM - 1) / BM, units = (g1 - g0 + 63) / 64;
+  const int u0 = units * part / parts, u1 = units * (part + 1) / parts;
+  const int row0 = __builtin_amdgcn_readfirstlane(g0 + 64 * u0);
+  const int rows = __builtin_amdgcn_readfirstlane(min(64 * (u1 - u0), g1 - row0));
+
+  const int kw = K / 128, nk = kw;
+  const uint32_t abytes = (uint32_t)K / 2, sbytes = (uint32_t)((kw + 3) / 4) * 16;
+  const BufRsrc ra = make_rsrc(aq, (uint32_t)(T + 1) * abytes);      // below 2^32 (the launcher's rule)
+  const BufRsrc rsa = make_rsrc(ascale, (uint32_t)(T + 1) * sbytes);
+  const BufRsrc rb = make_rsrc(codes + (size_t)g * N * abytes, (uint32_t)N * abytes);
+  const BufRsrc rsb = make_rsrc(wscale + (size_t)g * kw * N * 4, (uint32_t)kw * (uint32_t)N * 4u);
+  auto token_of = [&](int r) {                      // rows past the tile's end repeat its last
+    const int row = row0 + min(r, rows - 1);
+    if (!slot_of_row) return row;
+    const int slot = slot_of_row[row];
+    return slot < 0 ? T : min(slot / topk, T);
+  };
+  auto column = [&](int c) {                        // column of tile column c (past N: past the buffer's end)
+    return SWIGLU ? (c < BN / 2 ? nt * (BN / 2) + c : half + nt * (BN / 2) + c - BN / 2) : nt * BN + c;
+  };
+
+  auto run = [&](auto mi_c) __attribute__((always_inline)) {
+    constexpr int MI = decltype(mi_c)::value;       // the tile has up to 64 * MI rows, a wave 32 * MI
+    constexpr int kLoads = MI + 4;                  // a wave's copies of a stage, without the scales
+    uint32_t va[MI], vb[4], vsa, vsb;
+#pragma unroll
+    for (int j = 0; j < MI; ++j) {
+      const int r = (MI * wave + j) * 16 + (lane >> 2);
+      va[j] = (uint32_t)token_of(r) * abytes + (uint32_t)(((lane & 3) ^ ((r >> 2) & 3)) << 4);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = (4 * wave + j) * 16 + (lane >> 2);
+      vb[j] = (uint32_t)column(c) * abytes + (uint32_t)(((lane & 3) ^ ((c >> 2) & 3)) << 4);
+    }
+    vsa = (uint32_t)token_of(64 * wave + lane) * sbytes;
+    vsb = ((uint32_t)wave * (uint32_t)N + (uint32_t)column(4 * lane)) * 4u;
+    auto slot_at = [&](int u) { return smem + u * (BM + BN) * BK; };
+    auto copy = [&](int ks, int u, int q) __attribute__((always_inline)) {   // copy q of stage ks into ring slot u
+      if (q < MI) dma16(ra, slot_at(u) + (MI * wave + q) * 1024, va[q], (uint32_t)ks * BK);
+      else dma16(rb, slot_at(u) + BM * BK + (4 * wave + q - MI) * 1024, vb[q - MI], (uint32_t)ks * BK);
+    };
+    auto copy_scales = [&](int ks) __attribute__((always_inline)) {          // of stages ks .. ks + 3, ks a multiple of 4
+      uint8_t* const s = smem + kRingBytes + ((ks >> 2) & 1) * kScaleSlot;
+      dma16(rsa, s + wave * 1024, vsa, (uint32_t)ks * 4u);
+      dma16(rsb, s + BM * 16 + wave * 1024, vsb, (uint32_t)ks * (uint32_t)N * 4u);
+    };
+
+    const int h = lane >> 5, r32 = lane & 31;
+    int arow[MI], bcol[4];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) arow[i] = wm * 32 * MI + 32 * i + r32;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      bcol[j] = (SWIGLU ? (j < 2 ? wn * 64 + 32 * j : 128 + wn * 64 + 32 * (j - 2)) : wn * 128 + 32 * j) + r32;
+    v4i a[2][MI][2], b[2][4][2];
+    int sa[2][MI], sb[2][4];
+    auto read_a = [&](auto set_c, int u, int ks, int i) __attribute__((always_inline)) {
+      constexpr int S = decltype(set_c)::value;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) a[S][i][s] = *reinterpret_cast<const v4i*>(slot_at(u) + swz(arow[i], 2 * s + h));
+      const uint8_t* sc = smem + kRingBytes + ((ks >> 2) & 1) * kScaleSlot;
+      sa[S][i] = *reinterpret_cast<const int*>(sc + arow[i] * 16 + 4 * u);
+    };
+    auto read_b = [&](auto set_c, int u, int ks, int j) __attribute__((always_inline)) {
+      constexpr int S = decltype(set_c)::value;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        b[S][j][s] = *reinterpret_cast<const v4i*>(slot_at(u) + BM * BK + swz(bcol[j], 2 * s + h));
+      const uint8_t* sc = smem + kRingBytes + ((ks >> 2) & 1) * kScaleSlot + BM * 16;
+      sb[S][j] = *reinterpret_cast<const int*>(sc + (u * BN + bcol[j]) * 4);
+    };
+
+    v16f acc[MI][4];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+    // ---- prologue: stages 0..3 in flight, stage 0 in registers
+    copy_scales(0);
+    const int pre = min(nk, kStages);
+    for (int s = 0; s < pre; ++s)
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) copy(s, s, q);
+    if (pre == 4) wait_vmem_lds<3 * kLoads>();
+    else wait_vmem_lds<0>();
+    barrier_only();
+#pragma unroll
+    for (int i = 0; i < MI; ++i) read_a(std::integral_constant<int, 0>{}, 0, 0, i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) read_b(std::integral_constant<int, 0>{}, 0, 0, j);
+
+    // One stage, ks % 4 = U: its operands are in register set U & 1.  MAIN: four more stages follow.
+    // The scale words are shifted to the lane's blocks (h, 2 + h) where they are used, so that
+    // nothing waits for the reads of the next stage.
+    auto step = [&](int ks, auto u_c, auto main_c) __attribute__((always_inline)) {
+      constexpr int U = decltype(u_c)::value, S = U & 1, NU = (U + 1) & 3;
+      constexpr bool MAIN = decltype(main_c)::value;
+      using Next = std::integral_constant<int, 1 - S>;
+      const bool more = MAIN || ks + 1 < nk, ahead = MAIN || ks + 4 < nk;
+      if (more) {
+        // stage ks + 1 has landed when only the copies of stages ks + 2 and ks + 3 are left
+        // (and the scales that came with one of them)
+        if (MAIN || ks + 3 < nk) wait_vmem_lds<2 * kLoads + (U == 1 || U == 2 ? 2 : 0)>();
+        else wait_vmem_lds<0>();
+        barrier_only();
+      }
+      int xa[MI];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) xa[i] = sa[S][i] >> (8 * h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (ahead) {
+          if (U == 0 && j == 0) copy_scales(ks + 4);
+#pragma unroll
+          for (int q = j * kLoads / 4; q < (j + 1) * kLoads / 4; ++q) copy(ks + 4, U, q);
+        }
+        if (more) {
+          read_b(Next{}, NU, ks + 1, j);
+#pragma unroll
+          for (int i = j * MI / 4; i < (j + 1) * MI / 4; ++i) read_a(Next{}, NU, ks + 1, i);
+        }
+        const int xb = sb[S][j] >> (8 * h);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) acc[i][j] = mfma_mxfp4_32<0>(b[S][j][0], a[S][i][0], acc[i][j], xb, xa[i]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) acc[i][j] = mfma_mxfp4_32<2>(b[S][j][1], a[S][i][1], acc[i][j], xb, xa[i]);
+        sched_fence();
+      }
+    };
+    using U0 = std::integral_constant<int, 0>;
+    using U1 = std::integral_constant<int, 1>;
+    using U2 = std::integral_constant<int, 2>;
+    using U3 = std::integral_constant<int, 3>;
+    int ks = 0;
+    for (; ks + 7 < nk; ks += 4) {
+      step(ks, U0{}, std::true_type{});
+      step(ks + 1, U1{}, std::true_type{});
+      step(ks + 2, U2{}, std::true_type{});
+      step(ks + 3, U3{}, std::true_type{});
+    }
+    for (; ks < nk; ks += 4) {                      // the last one to seven stages
+      step(ks, U0{}, std::false_type{});
+      if (ks + 1 < nk) step(ks + 1, U1{}, std::false_type{});
+      if (ks + 2 < nk) step(ks + 2, U2{}, std::false_type{});
+      if (ks + 3 < nk) step(ks + 3, U3{}, std::false_type{});
+    }
+
+    // ---- epilogue: a lane holds row arow[i], columns 8q + 4h + 0..3 of each fragment.  Lanes l and
+    // l + 32 hold the same row and trade 8-byte groups, so that every store is 16 bytes.
+    auto store_frag = [&](uint16_t* rowp, const v2i* pq) __attribute__((always_inline)) {
+      const v2i s0 = h ? pq[0] : pq[1], s1 = h ? pq[2] : pq[3];
+      const int r00 = __shfl_xor(s0[0], 32), r01 = __shfl_xor(s0[1], 32);
+      const int r10 = __shfl_xor(s1[0], 32), r11 = __shfl_xor(s1[1], 32);
+      const v4i x0 = h ? (v4i){r00, r01, pq[1][0], pq[1][1]} : (v4i){pq[0][0], pq[0][1], r00, r01};
+      const v4i x1 = h ? (v4i){r10, r11, pq[3][0], pq[3][1]} : (v4i){pq[2][0], pq[2][1], r10, r11};
+      *reinterpret_cast<v4i*>(rowp + 8 * h) = x0;
+      *reinterpret_cast<v4i*>(rowp + 16 + 8 * h) = x1;
+    };
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      if (arow[i] >= rows) continue;
+      const size_t row = (size_t)row0 + arow[i];
+#pragma unroll
+      for (int j = 0; j < (SWIGLU ? 2 : 4); ++j) {
+        v2i pq[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = acc[i][j][4 * q + e];
+            // hardware reciprocal: the product is rounded to bf16 right after
+            v[e] = SWIGLU ? y * __builtin_amdgcn_rcpf(1.0f + __expf(-y)) * acc[i][(j + 2) & 3][4 * q + e] : y;
+          }
+          pq[q] = (v2i){(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
+        }
+        if (SWIGLU) store_frag(out + row * half + nt * (BN / 2) + wn * 64 + 32 * j, pq);
+        else if (nt * BN + wn * 128 + 32 * j < N) store_frag(out + row * N + nt * BN + wn * 128 + 32 * j, pq);
+      }
+    }
+  };
+  if (rows > 192) run(std::integral_constant<int, 4>{});
+  else if (rows > 128) run(std::integral_constant<int, 3>{});
+  else if (rows > 64) run(std::integral_constant<int, 2>{});
+  else run(std::integral_constant<int, 1>{});
+}
+
 }  // namespace
 
 hipError_t launch_gmm_mxfp4(const uint8_t* aq, const uint8_t* ascale, const uint8_t* codes, const uint8_t* wscale,
                             const int* group_sizes, const int* slot_of_row, int topk, int T, int G, int M, int K,
                             int N, bool swiglu, uint16_t* out, int* status, hipStream_t stream) {
+  const uint32_t* as = reinterpret_cast<const uint32_t*>(ascale);
+  const uint32_t* bs = reinterpret_cast<const uint32_t*>(wscale);
+  if ((long long)(T + 1) * (K / 2) < (1LL << 32) && M >= 64 * G) {
+    const long long tiles = std::min<long long>(M, ((long long)M + BM - 1) / BM + G);
+    const size_t lds = kTileLds + sizeof(int) * (3 * (size_t)G + 1);
+    if (swiglu)
+      hipLaunchKernelGGL(gmm_mxfp4_tile_kernel<true>, dim3((unsigned)(tiles * (N / 256))), dim3(256), lds, stream, aq,
+                         ascale, codes, wscale, group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
+    else
+      hipLaunchKernelGGL(gmm_mxfp4_tile_kernel<false>, dim3((unsigned)(tiles * ((N + 255) / 256))), dim3(256), lds,
+                         stream, aq, ascale, codes, wscale, group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
+    return hipGetLastError();
+  }
   constexpr int MA = 4;
   const long long tiles = std::min<long long>(M, ((long long)M + 16 * MA - 1) / (16 * MA) + G);
   const dim3 grid((unsigned)(tiles * (N / 32)));
   const size_t lds = sizeof(float) * 4 * kWaves * MA * 2 * 64 + sizeof(int) * (3 * (size_t)G + 1);
-  const uint32_t* as = reinterpret_cast<const uint32_t*>(ascale);
-  const uint32_t* bs = reinterpret_cast<const uint32_t*>(wscale);
   if (swiglu)
     hipLaunchKernelGGL((gmm_mxfp4_split_kernel<MA, true>), grid, dim3(64 * kWaves), lds, stream, aq, as, codes, bs,
                        group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);

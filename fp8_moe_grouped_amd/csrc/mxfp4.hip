@@ -43,7 +43,8 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
 }
 
 // Activations: one 16-byte chunk (8 values) per lane, four lanes a block.  Row T
-// is written as zeros: the product reads it for rows without a token.
+// is written as zeros: the product reads it for rows without a token.  Scale rows
+// are padded to 16 bytes.
 __global__ __launch_bounds__(256) void quant_rows_mxfp4_kernel(const v4i* __restrict__ x, int T, int nch,
                                                               uint32_t* __restrict__ codes,
                                                               uint8_t* __restrict__ scales) {
@@ -61,7 +62,10 @@ __global__ __launch_bounds__(256) void quant_rows_mxfp4_kernel(const v4i* __rest
   am = quad_max<0x4E>(am);                          // lanes 2 3 0 1
   const uint32_t b = scale_byte(am);
   codes[i] = cvt_fp4x8(v[0], v[1], v[2], v[3], b);
-  if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)b;
+  if ((threadIdx.x & 3) == 0) {
+    const int t = (int)(i / nch), c = (int)(i % nch);
+    scales[(size_t)t * ((nch + 63) / 64 * 16) + (c >> 2)] = (uint8_t)b;
+  }
 }
 
 // Weights: a block turns a tile of 256 k x 128 n.  A lane owns two adjacent
