@@ -30,6 +30,71 @@ __device__ __forceinline__ v4f mfma_mxfp4(const v4i& a, const v4i& b, const v4f&
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, sa, 0, sb);
 }
 
+// ---------------------------------------------------------------- schedule
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {     // lanes without a source add 0
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+// Inclusive prefix sum across the wave without LDS.
+__device__ __forceinline__ int wave_scan_dpp(int v) {
+  v = dpp_add<0x111, 0xF>(v);                       // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);                       // row_bcast 15 into rows 1 and 3
+  return dpp_add<0x143, 0xC>(v);                    // row_bcast 31 into rows 2 and 3
+}
+
+// The experts' rows and tiles of BM rows, 64 experts at a time, one a lane.  Every
+// wave finds its own tile in registers: the LDS table of build_group_table (one
+// wave's shuffles, a barrier, a binary search) took 9400 cycles from the block's
+// start to its tile's first address, this takes 3900.
+template <int BM>
+struct TileMap {
+  int start, end, first, tiles;                     // the lane's expert: rows, first tile, tiles
+  int total;                                        // tiles of all experts
+
+  __device__ __forceinline__ void scan64(const int* __restrict__ group_sizes, int G, int M, int base, int& rows,
+                                         int& before, int& flags) {
+    const int g = base + (int)(threadIdx.x & 63);
+    const int raw = g < G ? group_sizes[g] : 0;
+    if (raw < 0) flags |= kDevNegativeSize;
+    const int sz = min(max(raw, 0), M);             // M < 2^24: no overflow below
+    const int last = rows + wave_scan_dpp(sz);
+    if (raw > M || (last > M && sz > 0)) flags |= kDevSumClamped;
+    start = min(last - sz, M);
+    end = min(last, M);
+    tiles = (end - start + BM - 1) / BM;
+    const int upto = before + wave_scan_dpp(tiles);
+    first = upto - tiles;
+    rows = min(__builtin_amdgcn_readlane(last, 63), M);
+    before = __builtin_amdgcn_readlane(upto, 63);
+  }
+  __device__ __forceinline__ void scan(const int* __restrict__ group_sizes, int G, int M, int* status) {
+    int rows = 0, before = 0, flags = 0;
+    for (int base = 0; base < G; base += 64) scan64(group_sizes, G, M, base, rows, before, flags);
+    total = before;
+    if (status != nullptr && blockIdx.x == 0 && threadIdx.x < 64 && flags) atomicOr(status, flags);
+  }
+  // expert and place of tile mt < total: its expert's rows and its index among the expert's tiles
+  __device__ __forceinline__ void locate(const int* __restrict__ group_sizes, int G, int M, int mt, int& g, int& g0,
+                                         int& g1, int& part) {
+    int rows = 0, before = 0, flags = 0;
+    for (int base = 0; base < G; base += 64) {
+      if (G > 64) scan64(group_sizes, G, M, base, rows, before, flags);   // scan left the last 64
+      const uint64_t hit = __ballot(first <= mt && mt < first + tiles);
+      if (hit == 0) continue;
+      const int at = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+      g = base + at;
+      g0 = __builtin_amdgcn_readlane(start, at);
+      g1 = __builtin_amdgcn_readlane(end, at);
+      part = mt - __builtin_amdgcn_readlane(first, at);
+      return;
+    }
+  }
+};
+
 template <int MA, bool SWIGLU>
 __global__ __launch_bounds__(64 * kWaves) void gmm_mxfp4_split_kernel(
     const uint8_t* __restrict__ aq, const uint32_t* __restrict__ ascale, const uint8_t* __restrict__ codes,
@@ -38,20 +103,16 @@ __global__ __launch_bounds__(64 * kWaves) void gmm_mxfp4_split_kernel(
   constexpr int BM = 16 * MA;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   v4f* const part = reinterpret_cast<v4f*>(smem);   // [kWaves][MA * 2][64]
-  int* const t_start = reinterpret_cast<int*>(part + kWaves * MA * 2 * 64);
-  int* const t_end = t_start + G;
-  int* const t_pre = t_end + G;
-  build_group_table(group_sizes, G, M, BM, GroupTable{t_start, t_end, t_pre}, status);
-  __syncthreads();
-
+  TileMap<BM> map;
+  map.scan(group_sizes, G, M, status);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tiles = t_pre[G], half = N >> 1;
+  const int tiles = map.total, half = N >> 1;
   const int n_tiles = N / 32;
   if ((int)blockIdx.x >= tiles * n_tiles) return;
-  const int mt = __builtin_amdgcn_readfirstlane(blockIdx.x % tiles), nt = blockIdx.x / tiles;
-  const int g = __builtin_amdgcn_readfirstlane(find_group(t_pre, G, mt));
-  const int row0 = __builtin_amdgcn_readfirstlane(t_start[g] + (mt - t_pre[g]) * BM);
-  const int rows = __builtin_amdgcn_readfirstlane(min(BM, t_end[g] - row0));
+  const int mt = blockIdx.x % tiles, nt = blockIdx.x / tiles;
+  int g = 0, g0 = 0, g1 = 0, tile = 0;
+  map.locate(group_sizes, G, M, mt, g, g0, g1, tile);
+  const int row0 = g0 + tile * BM, rows = min(BM, g1 - row0);
 
   const int q = lane >> 4, r16 = lane & 15;
   const int kw = K / 128;                           // scale words of a row
@@ -150,19 +211,20 @@ __global__ __launch_bounds__(64 * kWaves) void gmm_mxfp4_split_kernel(
 // nearly equal counts of 64 rows, and a wave's instructions follow the tile's
 // count (MI fragments of 32 rows), so a short tile takes proportionally less time.
 //
-// The contraction advances 128 k (64 bytes a row) a stage through a ring of four
-// stages in LDS, filled by buffer loads with the LDS destination.  While a stage's
-// matrix instructions issue from one register set, the next stage's operands are
-// read into the other, and the copies of the stage four ahead go to the slot that
-// was just read.  Scale words (four blocks of 32 k) arrive four stages at a time.
-constexpr int BM = 256, BN = 256, BK = 64;          // BK in bytes: 128 k
-constexpr int kStages = 4;
-constexpr int kRingBytes = kStages * (BM + BN) * BK;
+// The contraction advances 128 k a stage; buffer loads with the LDS destination
+// bring two stages (a pair: 128 bytes, one cache line, a row) at a time into one of
+// two slots.  While a stage's matrix instructions issue from one register set, the
+// next stage's operands are read into the other, and the copies of the pair two
+// ahead go to the slot that was just read.  Scale words (four blocks of 32 k)
+// arrive two pairs at a time.
+constexpr int BM = 256, BN = 256, BK = 128;         // BK in bytes: the 256 k of a pair
+constexpr int kSlotBytes = (BM + BN) * BK;
+constexpr int kRingBytes = 2 * kSlotBytes;
 constexpr int kScaleSlot = BM * 16 + 4 * BN * 4;    // four stages' scale words, rows then columns
 constexpr int kTileLds = kRingBytes + 2 * kScaleSlot;
-static_assert(kTileLds + sizeof(int) * (3 * kMaxGroups + 1) <= 160 * 1024, "ring, scales and expert table fit the LDS");
+static_assert(kTileLds <= 160 * 1024, "ring and scales fit the LDS");
 
-__device__ __forceinline__ int swz(int row, int chunk) { return row * BK + ((chunk ^ ((row >> 2) & 3)) << 4); }
+__device__ __forceinline__ int swz(int row, int chunk) { return row * BK + ((chunk ^ ((row >> 1) & 7)) << 4); }
 
 template <int SEL>
 __device__ __forceinline__ v16f mfma_mxfp4_32(const v4i& a, const v4i& b, const v16f& c, int sa, int sb) {
@@ -177,29 +239,23 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
                            const int* __restrict__ group_sizes, const int* __restrict__ slot_of_row, int topk, int T,
                            int G, int M, int K, int N, uint16_t* __restrict__ out, int* status) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  int* const t_start = reinterpret_cast<int*>(smem + kTileLds);
-  int* const t_end = t_start + G;
-  int* const t_pre = t_end + G;
-  build_group_table(group_sizes, G, M, BM, GroupTable{t_start, t_end, t_pre}, status);
-  __syncthreads();
-
+  TileMap<BM> map;
+  map.scan(group_sizes, G, M, status);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int half = N >> 1;
   const int n_tiles = SWIGLU ? half / (BN / 2) : (N + BN - 1) / BN;
-  const int tiles = t_pre[G];
+  const int tiles = map.total;
   if ((int)blockIdx.x >= tiles * n_tiles) return;
   int mt, nt;
-  raster_tile<8>(blockIdx.x, tiles, n_tiles, mt, nt);
-  nt = __builtin_amdgcn_readfirstlane(nt);
-  const int g = __builtin_amdgcn_readfirstlane(find_group(t_pre, G, mt));
+  raster_tile<4>(blockIdx.x, tiles, n_tiles, mt, nt);   // 389 us against 395 with groups of 8 and 401 with 16
+  int g = 0, g0 = 0, g1 = 0, part = 0;
+  map.locate(group_sizes, G, M, mt, g, g0, g1, part);
   // this tile's share of the expert's units of 64 rows
-  const int g0 = t_start[g], g1 = t_end[g], part = mt - t_pre[g];
   const int parts = (g1 - g0 + BM - 1) / BM, units = (g1 - g0 + 63) / 64;
   const int u0 = units * part / parts, u1 = units * (part + 1) / parts;
-  const int row0 = __builtin_amdgcn_readfirstlane(g0 + 64 * u0);
-  const int rows = __builtin_amdgcn_readfirstlane(min(64 * (u1 - u0), g1 - row0));
+  const int row0 = g0 + 64 * u0, rows = min(64 * (u1 - u0), g1 - row0);
 
   const int kw = K / 128, nk = kw;
   const uint32_t abytes = (uint32_t)K / 2, sbytes = (uint32_t)((kw + 3) / 4) * 16;
@@ -219,24 +275,25 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
 
   auto run = [&](auto mi_c) __attribute__((always_inline)) {
     constexpr int MI = decltype(mi_c)::value;       // the tile has up to 64 * MI rows, a wave 32 * MI
-    constexpr int kLoads = MI + 4;                  // a wave's copies of a stage, without the scales
-    uint32_t va[MI], vb[4], vsa, vsb;
+    constexpr int kLoads = 2 * MI + 8;              // a wave's copies of a pair, without the scales
+    uint32_t va[2 * MI], vb[8], vsa, vsb;
+    const int mine = token_of(16 * MI * wave + min(lane, 16 * MI - 1));      // a lane has a row's token
 #pragma unroll
-    for (int j = 0; j < MI; ++j) {
-      const int r = (MI * wave + j) * 16 + (lane >> 2);
-      va[j] = (uint32_t)token_of(r) * abytes + (uint32_t)(((lane & 3) ^ ((r >> 2) & 3)) << 4);
+    for (int j = 0; j < 2 * MI; ++j) {
+      const int r = (2 * MI * wave + j) * 8 + (lane >> 3);
+      va[j] = (uint32_t)__shfl(mine, 8 * j + (lane >> 3)) * abytes + (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) << 4);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = (4 * wave + j) * 16 + (lane >> 2);
-      vb[j] = (uint32_t)column(c) * abytes + (uint32_t)(((lane & 3) ^ ((c >> 2) & 3)) << 4);
+    for (int j = 0; j < 8; ++j) {
+      const int c = (8 * wave + j) * 8 + (lane >> 3);
+      vb[j] = (uint32_t)column(c) * abytes + (uint32_t)(((lane & 7) ^ ((c >> 1) & 7)) << 4);
     }
     vsa = (uint32_t)token_of(64 * wave + lane) * sbytes;
     vsb = ((uint32_t)wave * (uint32_t)N + (uint32_t)column(4 * lane)) * 4u;
-    auto slot_at = [&](int u) { return smem + u * (BM + BN) * BK; };
-    auto copy = [&](int ks, int u, int q) __attribute__((always_inline)) {   // copy q of stage ks into ring slot u
-      if (q < MI) dma16(ra, slot_at(u) + (MI * wave + q) * 1024, va[q], (uint32_t)ks * BK);
-      else dma16(rb, slot_at(u) + BM * BK + (4 * wave + q - MI) * 1024, vb[q - MI], (uint32_t)ks * BK);
+    auto copy = [&](int p, int u, int q) __attribute__((always_inline)) {    // copy q of pair p into slot u
+      uint8_t* const s = smem + u * kSlotBytes;
+      if (q < 2 * MI) dma16(ra, s + (2 * MI * wave + q) * 1024, va[q], (uint32_t)p * BK);
+      else dma16(rb, s + BM * BK + (8 * wave + q - 2 * MI) * 1024, vb[q - 2 * MI], (uint32_t)p * BK);
     };
     auto copy_scales = [&](int ks) __attribute__((always_inline)) {          // of stages ks .. ks + 3, ks a multiple of 4
       uint8_t* const s = smem + kRingBytes + ((ks >> 2) & 1) * kScaleSlot;
@@ -253,20 +310,20 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
       bcol[j] = (SWIGLU ? (j < 2 ? wn * 64 + 32 * j : 128 + wn * 64 + 32 * (j - 2)) : wn * 128 + 32 * j) + r32;
     v4i a[2][MI][2], b[2][4][2];
     int sa[2][MI], sb[2][4];
-    auto read_a = [&](auto set_c, int u, int ks, int i) __attribute__((always_inline)) {
-      constexpr int S = decltype(set_c)::value;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) a[S][i][s] = *reinterpret_cast<const v4i*>(slot_at(u) + swz(arow[i], 2 * s + h));
+    // one of the kReads LDS reads of stage ks, ks % 4 = u, into register set u & 1
+    constexpr int kReads = 3 * (4 + MI);
+    auto read = [&](auto u_c, int ks, int q) __attribute__((always_inline)) {
+      constexpr int u = decltype(u_c)::value, S = u & 1;
+      const uint8_t* slot = smem + (u >> 1) * kSlotBytes;
       const uint8_t* sc = smem + kRingBytes + ((ks >> 2) & 1) * kScaleSlot;
-      sa[S][i] = *reinterpret_cast<const int*>(sc + arow[i] * 16 + 4 * u);
-    };
-    auto read_b = [&](auto set_c, int u, int ks, int j) __attribute__((always_inline)) {
-      constexpr int S = decltype(set_c)::value;
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        b[S][j][s] = *reinterpret_cast<const v4i*>(slot_at(u) + BM * BK + swz(bcol[j], 2 * s + h));
-      const uint8_t* sc = smem + kRingBytes + ((ks >> 2) & 1) * kScaleSlot + BM * 16;
-      sb[S][j] = *reinterpret_cast<const int*>(sc + (u * BN + bcol[j]) * 4);
+      const int f = q / 3, s = q % 3;               // fragment, then its two halves and its scales
+      if (f < 4) {
+        if (s < 2) b[S][f][s] = *reinterpret_cast<const v4i*>(slot + BM * BK + swz(bcol[f], 4 * S + 2 * s + h));
+        else sb[S][f] = *reinterpret_cast<const int*>(sc + BM * 16 + (u * BN + bcol[f]) * 4);
+      } else {
+        if (s < 2) a[S][f - 4][s] = *reinterpret_cast<const v4i*>(slot + swz(arow[f - 4], 4 * S + 2 * s + h));
+        else sa[S][f - 4] = *reinterpret_cast<const int*>(sc + arow[f - 4] * 16 + 4 * u);
+      }
     };
 
     v16f acc[MI][4];
@@ -277,55 +334,61 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-    // ---- prologue: stages 0..3 in flight, stage 0 in registers
+    // ---- prologue: pairs 0 and 1 in flight, stage 0 in registers
     copy_scales(0);
-    const int pre = min(nk, kStages);
-    for (int s = 0; s < pre; ++s)
 #pragma unroll
-      for (int q = 0; q < kLoads; ++q) copy(s, s, q);
-    if (pre == 4) wait_vmem_lds<3 * kLoads>();
-    else wait_vmem_lds<0>();
+    for (int q = 0; q < kLoads; ++q) copy(0, 0, q);
+    if (nk > 2) {
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) copy(1, 1, q);
+      wait_vmem_lds<kLoads>();
+    } else {
+      wait_vmem_lds<0>();
+    }
     barrier_only();
 #pragma unroll
-    for (int i = 0; i < MI; ++i) read_a(std::integral_constant<int, 0>{}, 0, 0, i);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) read_b(std::integral_constant<int, 0>{}, 0, 0, j);
+    for (int q = 0; q < kReads; ++q) read(std::integral_constant<int, 0>{}, 0, q);
 
     // One stage, ks % 4 = U: its operands are in register set U & 1.  MAIN: four more stages follow.
     // The scale words are shifted to the lane's blocks (h, 2 + h) where they are used, so that
-    // nothing waits for the reads of the next stage.
+    // nothing waits for the reads of the next stage.  A SIMD has one wave, which issues in order: the
+    // next stage's reads and the copies stand one by one between the matrix instructions and issue
+    // while those run.
     auto step = [&](int ks, auto u_c, auto main_c) __attribute__((always_inline)) {
-      constexpr int U = decltype(u_c)::value, S = U & 1, NU = (U + 1) & 3;
+      constexpr int U = decltype(u_c)::value, S = U & 1;
       constexpr bool MAIN = decltype(main_c)::value;
-      using Next = std::integral_constant<int, 1 - S>;
-      const bool more = MAIN || ks + 1 < nk, ahead = MAIN || ks + 4 < nk;
-      if (more) {
-        // stage ks + 1 has landed when only the copies of stages ks + 2 and ks + 3 are left
-        // (and the scales that came with one of them)
-        if (MAIN || ks + 3 < nk) wait_vmem_lds<2 * kLoads + (U == 1 || U == 2 ? 2 : 0)>();
-        else wait_vmem_lds<0>();
+      using Next = std::integral_constant<int, (U + 1) & 3>;
+      // In a pair's second stage every wave has read that pair: its slot takes the pair two ahead,
+      // and the next pair (the only copies in flight) has to be there.
+      const bool more = MAIN || ks + 1 < nk, ahead = S == 1 && (MAIN || ks + 3 < nk);
+      if (S == 1 && more) {
+        wait_vmem_lds<0>();
         barrier_only();
       }
-      int xa[MI];
+      int xa[MI], xb[4];
 #pragma unroll
       for (int i = 0; i < MI; ++i) xa[i] = sa[S][i] >> (8 * h);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (ahead) {
-          if (U == 0 && j == 0) copy_scales(ks + 4);
+      for (int j = 0; j < 4; ++j) xb[j] = sb[S][j] >> (8 * h);
+      constexpr int kSlots = 8 * MI;                // matrix instructions; the copies go out in the first three quarters
+      constexpr int kOut = U == 1 ? kLoads + 2 : U == 3 ? kLoads : 0;
 #pragma unroll
-          for (int q = j * kLoads / 4; q < (j + 1) * kLoads / 4; ++q) copy(ks + 4, U, q);
+      for (int t = 0; t < kSlots; ++t) {
+        const int s = t / (4 * MI), j = t / MI % 4, i = t % MI;
+        if (s == 0) acc[i][j] = mfma_mxfp4_32<0>(b[S][j][0], a[S][i][0], acc[i][j], xb[j], xa[i]);
+        else acc[i][j] = mfma_mxfp4_32<2>(b[S][j][1], a[S][i][1], acc[i][j], xb[j], xa[i]);
+        if (ahead) {
+#pragma unroll
+          for (int o = t * kOut / (6 * MI); o < min((t + 1) * kOut / (6 * MI), kOut); ++o) {
+            if (o < kLoads) copy((ks + 3) >> 1, U >> 1, o);
+            else if (o == kLoads) copy_scales(ks + 3);
+          }
         }
         if (more) {
-          read_b(Next{}, NU, ks + 1, j);
 #pragma unroll
-          for (int i = j * MI / 4; i < (j + 1) * MI / 4; ++i) read_a(Next{}, NU, ks + 1, i);
+          for (int o = t * kReads / (kSlots - 1); o < min((t + 1) * kReads / (kSlots - 1), kReads); ++o)
+            read(Next{}, ks + 1, o);
         }
-        const int xb = sb[S][j] >> (8 * h);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) acc[i][j] = mfma_mxfp4_32<0>(b[S][j][0], a[S][i][0], acc[i][j], xb, xa[i]);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) acc[i][j] = mfma_mxfp4_32<2>(b[S][j][1], a[S][i][1], acc[i][j], xb, xa[i]);
         sched_fence();
       }
     };
@@ -350,13 +413,12 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
     // ---- epilogue: a lane holds row arow[i], columns 8q + 4h + 0..3 of each fragment.  Lanes l and
     // l + 32 hold the same row and trade 8-byte groups, so that every store is 16 bytes.
     auto store_frag = [&](uint16_t* rowp, const v2i* pq) __attribute__((always_inline)) {
-      const v2i s0 = h ? pq[0] : pq[1], s1 = h ? pq[2] : pq[3];
-      const int r00 = __shfl_xor(s0[0], 32), r01 = __shfl_xor(s0[1], 32);
-      const int r10 = __shfl_xor(s1[0], 32), r11 = __shfl_xor(s1[1], 32);
-      const v4i x0 = h ? (v4i){r00, r01, pq[1][0], pq[1][1]} : (v4i){pq[0][0], pq[0][1], r00, r01};
-      const v4i x1 = h ? (v4i){r10, r11, pq[3][0], pq[3][1]} : (v4i){pq[2][0], pq[2][1], r10, r11};
-      *reinterpret_cast<v4i*>(rowp + 8 * h) = x0;
-      *reinterpret_cast<v4i*>(rowp + 16 + 8 * h) = x1;
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        const auto x = __builtin_amdgcn_permlane32_swap(pq[q][0], pq[q + 1][0], false, false);
+        const auto y = __builtin_amdgcn_permlane32_swap(pq[q][1], pq[q + 1][1], false, false);
+        *reinterpret_cast<v4i*>(rowp + 8 * q + 8 * h) = (v4i){(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
+      }
     };
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -396,19 +458,18 @@ hipError_t launch_gmm_mxfp4(const uint8_t* aq, const uint8_t* ascale, const uint
   const uint32_t* bs = reinterpret_cast<const uint32_t*>(wscale);
   if ((long long)(T + 1) * (K / 2) < (1LL << 32) && M >= 64 * G) {
     const long long tiles = std::min<long long>(M, ((long long)M + BM - 1) / BM + G);
-    const size_t lds = kTileLds + sizeof(int) * (3 * (size_t)G + 1);
     if (swiglu)
-      hipLaunchKernelGGL(gmm_mxfp4_tile_kernel<true>, dim3((unsigned)(tiles * (N / 256))), dim3(256), lds, stream, aq,
+      hipLaunchKernelGGL(gmm_mxfp4_tile_kernel<true>, dim3((unsigned)(tiles * (N / 256))), dim3(256), kTileLds, stream, aq,
                          ascale, codes, wscale, group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
     else
-      hipLaunchKernelGGL(gmm_mxfp4_tile_kernel<false>, dim3((unsigned)(tiles * ((N + 255) / 256))), dim3(256), lds,
+      hipLaunchKernelGGL(gmm_mxfp4_tile_kernel<false>, dim3((unsigned)(tiles * ((N + 255) / 256))), dim3(256), kTileLds,
                          stream, aq, ascale, codes, wscale, group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
     return hipGetLastError();
   }
   constexpr int MA = 4;
   const long long tiles = std::min<long long>(M, ((long long)M + 16 * MA - 1) / (16 * MA) + G);
   const dim3 grid((unsigned)(tiles * (N / 32)));
-  const size_t lds = sizeof(float) * 4 * kWaves * MA * 2 * 64 + sizeof(int) * (3 * (size_t)G + 1);
+  const size_t lds = sizeof(float) * 4 * kWaves * MA * 2 * 64;
   if (swiglu)
     hipLaunchKernelGGL((gmm_mxfp4_split_kernel<MA, true>), grid, dim3(64 * kWaves), lds, stream, aq, as, codes, bs,
                        group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
