@@ -12,6 +12,7 @@ The C contract of every call is documented in include/fp8_moe_grouped.h.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -119,15 +120,30 @@ def workspace_bytes(op: int, M: int, K: int, N: int, G: int, tile_m: int = 512) 
 
 # --------------------------------------------------------------------------- marshalling
 
+# A decoded token's call runs for a few microseconds on the GPU, so what a call
+# costs the host counts: plain integers for pointers, the current stream's handle
+# without a Stream object (0.1 us, not 2), and no device switch where the device
+# is the current one already (0.2 us, not 1.4).
+
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(dev) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+def _stream(dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(dev):
+    """A context in which dev is the current device."""
+    return _HERE_ALREADY if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _req(t, name, dtype, ndim):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == ndim and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -136,15 +152,19 @@ def _req(t, name, dtype, ndim):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _same_device(*ts):
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"all tensors must be on one device, got {devs}")
-    return devs.pop()
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"all tensors must be on one device, got {set(t.device for t in ts if t is not None)}")
+    return dev
 
 
 def _call(name, *args):
@@ -156,7 +176,8 @@ def _call(name, *args):
 def _workspace(op, M, K, N, G, dev, tile_m=512, workspace=None):
     need = workspace_bytes(op, M, K, N, G, tile_m)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.numel() < need:
         raise ValueError(f"workspace has {workspace.numel()} bytes, {need} needed")
     return workspace, need
@@ -187,7 +208,7 @@ def _fwd(name, op, lhs, codes, scale, group_sizes, out, debug, dev_status, works
     dbg_scale = torch.empty((M,), dtype=torch.float32, device=dev) if debug else None
     ws, need = _workspace(op, M, K, N, G, dev, workspace=workspace)
     extra = (_ptr(preact),) if swiglu else ()
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call(name, _ptr(lhs), _ptr(codes), _ptr(scale), _ptr(group_sizes), M, K, N, G, _ptr(out), *extra,
               _ptr(dbg_codes), _ptr(dbg_scale), _ptr(ws), need, _ptr(dev_status), _stream(dev))
     res = (out,) + ((preact,) if preact is not None else ()) + ((dbg_codes, dbg_scale) if debug else ())
@@ -215,7 +236,7 @@ def gmm_fp8_fwd_noalloc(lhs, codes, scale, group_sizes, *, out=None, dev_status=
     if K2 != K or tuple(scale.shape) != (G, N) or group_sizes.shape[0] != G:
         raise ValueError("shape mismatch")
     out = _out(out, (M, N), torch.bfloat16, dev, "out")
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("gmm_fp8_fwd_noalloc", _ptr(lhs), _ptr(codes), _ptr(scale), _ptr(group_sizes), M, K, N, G, _ptr(out),
               _ptr(dev_status), _stream(dev))
     return out
@@ -254,7 +275,7 @@ def gmm_fp8_fwd_variant(lhs, codes, scale, group_sizes, *, lhs_block=0, scale_bf
     dbg_codes = torch.empty((M, K), dtype=torch.uint8, device=dev) if debug else None
     dbg_scale = torch.empty((M, nb), dtype=torch.float32, device=dev) if debug else None
     ws, need = _workspace(OP_FWD_VARIANT, M, K, N, G, dev, tile_m=lhs_block, workspace=workspace)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("gmm_fp8_fwd_variant", _ptr(lhs), _ptr(codes), _ptr(scale), _ptr(group_sizes), M, K, N, G,
               int(lhs_block), flags, _ptr(out), _ptr(dbg_codes), _ptr(dbg_scale), _ptr(ws), need, _ptr(dev_status),
               _stream(dev))
@@ -274,7 +295,7 @@ def quantize_rows_fp8(lhs, group_sizes, *, codes=None, scales=None):
         scales = torch.empty((M,), dtype=torch.float32, device=dev)
     _req(codes, "codes", torch.uint8, 2)
     _req(scales, "scales", torch.float32, 1)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("quantize_rows_fp8", _ptr(lhs), _ptr(group_sizes), M, K, group_sizes.shape[0], _ptr(codes),
               _ptr(scales), _stream(dev))
     return codes, scales
@@ -299,7 +320,7 @@ def _fwd_q(name, aq, ascale, codes, scale, group_sizes, out, dev_status, swiglu,
         if tuple(preact.shape) != (M, N):
             raise ValueError(f"preact must be [{M}, {N}], got {tuple(preact.shape)}")
     extra = (_ptr(preact),) if swiglu else ()
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call(name, _ptr(aq), _ptr(ascale), _ptr(codes), _ptr(scale), _ptr(group_sizes), M, K, N, G, _ptr(out),
               *extra, _ptr(dev_status), _stream(dev))
     return out
@@ -331,7 +352,7 @@ def gmm_dlhs_fp8(dout, codes, scale, group_sizes, *, out=None, dev_status=None, 
         out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
     _req(out, "out", torch.bfloat16, 2)
     ws, need = _workspace(OP_DLHS, M, K, N, G, dev, workspace=workspace)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("gmm_dlhs_fp8", _ptr(dout), _ptr(codes), _ptr(scale), _ptr(group_sizes), M, K, N, G, _ptr(out),
               _ptr(ws), need, _ptr(dev_status), _stream(dev))
     return out
@@ -356,7 +377,7 @@ def gmm_dswiglu_fp8(dout, codes, scale, group_sizes, preact, *, out=None, dev_st
     _req(out, "out", torch.bfloat16, 2)
     if tuple(out.shape) != (M, 2 * K):
         raise ValueError("out must be [M, 2K]")
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("gmm_dswiglu_fp8", _ptr(dout), _ptr(codes), _ptr(scale), _ptr(group_sizes), _ptr(preact), M, K, N, G,
               _ptr(out), _ptr(dev_status), _stream(dev))
     return out
@@ -399,7 +420,7 @@ def moe_ffn_fp8_fwd(x, wi_codes, wi_scale, wo_codes, wo_scale, group_sizes, *, k
     y = _out(y, (M, H), torch.bfloat16, dev, "y")
     preact = _out(preact, (M, 2 * I), torch.bfloat16, dev, "preact") if (keep_preact or preact is not None) else None
     ws, need = _workspace(OP_FFN_FWD, M, H, I, G, dev, tile_m=0, workspace=workspace)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("moe_ffn_fp8_fwd", _ptr(x), _ptr(wi_codes), _ptr(wi_scale), _ptr(wo_codes), _ptr(wo_scale),
               _ptr(group_sizes), M, H, I, G, _ptr(h), _ptr(preact), _ptr(y), _ptr(ws), need, _ptr(dev_status),
               _stream(dev))
@@ -423,7 +444,7 @@ def moe_ffn_fp8_bwd(x, h, preact, dy, wi_codes, wi_scale, wo_codes, wo_scale, gr
     dwi = _out(dwi, (G, H, 2 * I), torch.float32, dev, "dwi")
     dwo = _out(dwo, (G, I, H), torch.float32, dev, "dwo")
     ws, need = _workspace(OP_FFN_BWD, M, H, I, G, dev, tile_m=512, workspace=workspace)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("moe_ffn_fp8_bwd", _ptr(x), _ptr(h), _ptr(preact), _ptr(dy), _ptr(wi_codes), _ptr(wi_scale),
               _ptr(wo_codes), _ptr(wo_scale), _ptr(group_sizes), M, H, I, G, gd, _ptr(d_preact), _ptr(dx),
               _ptr(dwi), _ptr(dwo), _ptr(ws), need, _ptr(dev_status), _stream(dev))
@@ -452,7 +473,7 @@ def tgmm_quant(lhs, dout, group_sizes, grad_dtype="e5m2", tile_m=512, *, out=Non
     dbg_sL = torch.empty((max(tmax, 1), K), dtype=torch.float32, device=dev) if debug else None
     dbg_sD = torch.empty((max(tmax, 1), N), dtype=torch.float32, device=dev) if debug else None
     ws, need = _workspace(OP_TGMM, M, K, N, G, dev, tile_m=tile_m, workspace=workspace)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("tgmm_quant", _ptr(lhs), _ptr(dout), _ptr(group_sizes), M, K, N, G, gd, tile_m, _ptr(out),
               _ptr(dbg_sL), _ptr(dbg_sD), _ptr(ws), need, _ptr(dev_status), _stream(dev))
     return (out, dbg_sL, dbg_sD) if debug else out
@@ -506,7 +527,7 @@ def tgmm_dense_quant(lhs, dout, group_sizes, grad_dtype="e5m2", *, out=None, deb
     srow = torch.empty((max(M, 1),), dtype=torch.float32, device=dev) if debug else None
     scol = torch.empty((N,), dtype=torch.float32, device=dev) if debug else None
     ws, need = _workspace(OP_TGMM_DENSE, M, K, N, G, dev, tile_m=0, workspace=workspace)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("tgmm_dense_quant", _ptr(lhs), _ptr(dout), _ptr(group_sizes), M, K, N, G, gd, _ptr(out), _ptr(srow),
               _ptr(scol), _ptr(ws), need, _ptr(dev_status), _stream(dev))
     return (out, srow, scol) if debug else out
@@ -523,7 +544,7 @@ def dequantize_fp8_codes(codes, scale, *, out=None):
     if out is None:
         out = torch.empty((G, K, N), dtype=torch.bfloat16, device=dev)
     _req(out, "out", torch.bfloat16, 3)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("dequantize_fp8_codes", _ptr(codes), _ptr(scale), G, K, N, _ptr(out), _stream(dev))
     return out
 
@@ -540,7 +561,7 @@ def _bf16_fwd(name, lhs, w, group_sizes, out, swiglu, dev_status):
     if out is None:
         out = torch.empty((M, N // 2 if swiglu else N), dtype=torch.bfloat16, device=dev)
     _req(out, "out", torch.bfloat16, 2)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call(name, _ptr(lhs), _ptr(w), _ptr(group_sizes), M, K, N, G, _ptr(out), _ptr(dev_status), _stream(dev))
     return out
 
@@ -569,7 +590,7 @@ def gmm_bf16_dlhs(dout, w, group_sizes, *, out=None):
         raise ValueError("shape mismatch")
     if out is None:
         out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("gmm_bf16_dlhs", _ptr(dout), _ptr(w), _ptr(group_sizes), M, K, N, G, _ptr(out), None, _stream(dev))
     return out
 
@@ -608,13 +629,12 @@ def moe_route(logits, k, *, renormalize=True, workspace=None):
     k = int(k)
     if not 1 <= k <= E:
         raise ValueError(f"k must be between 1 and the {E} experts, got {k}")
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    # one allocation for the four outputs of a slot (a view costs the host less than a tensor)
+    ids, weights, row_of_slot, slot_of_row = torch.empty((4, T, k), dtype=torch.int32, device=dev).unbind(0)
+    weights, slot_of_row = weights.view(torch.float32), slot_of_row.view(-1)
     group_sizes = torch.empty((E,), dtype=torch.int32, device=dev)
-    row_of_slot = torch.empty((T, k), dtype=torch.int32, device=dev)
-    slot_of_row = torch.empty((T * k,), dtype=torch.int32, device=dev)
     ws, need = _workspace(OP_ROUTE, T, E, k, 1, dev, tile_m=0, workspace=workspace)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("moe_route", _ptr(logits), LOGIT_DTYPES[logits.dtype], T, E, k, bool(renormalize), _ptr(ids),
               _ptr(weights), _ptr(group_sizes), _ptr(row_of_slot), _ptr(slot_of_row), _ptr(ws), need, _stream(dev))
     return MoeRouting(ids, weights, group_sizes, row_of_slot, slot_of_row)
@@ -632,7 +652,7 @@ def moe_route_bwd(dweights, logits, ids, weights, *, renormalize=True, out=None)
     _req_slots(dweights, "dweights", torch.float32, T, k)
     dev = _same_device(dweights, logits, ids, weights)
     out = _out(out, (T, E), logits.dtype, dev, "out")
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("moe_route_bwd", _ptr(dweights), _ptr(logits), LOGIT_DTYPES[logits.dtype], _ptr(ids), _ptr(weights), T,
               E, k, bool(renormalize), _ptr(out), _stream(dev))
     return out
@@ -656,7 +676,7 @@ def moe_permute(x, row_of_slot, *, out=None):
     _req(out, "out", torch.bfloat16, 2)
     if out.shape[1] != H or out.device != dev:
         raise ValueError(f"out must be [R, {H}] on {dev}, got {tuple(out.shape)} on {out.device}")
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("moe_permute", _ptr(x), _ptr(row_of_slot), T, k, out.shape[0], H, _ptr(out), _stream(dev))
     return out
 
@@ -670,7 +690,7 @@ def moe_permute_fp8(x, row_of_slot, *, codes=None, scales=None):
     codes = _out(codes, (R, H), torch.uint8, dev, "codes")
     scales = _out(scales, (R,), torch.float32, dev, "scales")
     _same_device(x, codes, scales)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("moe_permute_fp8", _ptr(x), _ptr(row_of_slot), T, k, R, H, _ptr(codes), _ptr(scales), _stream(dev))
     return codes, scales
 
@@ -683,7 +703,7 @@ def moe_combine(y, row_of_slot, weights=None, *, out=None):
         _req_slots(weights, "weights", torch.float32, T, k)
     out = _out(out, (T, H), torch.bfloat16, dev, "out")
     _same_device(y, weights, out)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("moe_combine", _ptr(y), _ptr(row_of_slot), _ptr(weights), T, k, y.shape[0], H, _ptr(out), _stream(dev))
     return out
 
@@ -699,7 +719,7 @@ def moe_combine_bwd(dout, y, row_of_slot, weights, *, dy=None, dweights=None):
     dy = _out(dy, tuple(y.shape), torch.bfloat16, dev, "dy")
     dweights = _out(dweights, (T, k), torch.float32, dev, "dweights")
     _same_device(dout, y, weights, dy, dweights)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("moe_combine_bwd", _ptr(dout), _ptr(y), _ptr(row_of_slot), _ptr(weights), T, k, y.shape[0], H, _ptr(dy),
               _ptr(dweights), _stream(dev))
     return dy, dweights
@@ -716,7 +736,7 @@ def quantize_mxfp4_weights(w, *, codes=None, scales=None):
     codes = _out(codes, (G, N, K // 2), torch.uint8, dev, "codes")
     scales = _out(scales, (G, K // 128, N, 4), torch.uint8, dev, "scales")
     _same_device(w, codes, scales)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("quantize_mxfp4_weights", _ptr(w), K, N, G, _ptr(codes), _ptr(scales), _stream(dev))
     return codes, scales
 
@@ -739,7 +759,7 @@ def dequantize_mxfp4(codes, scales, *, out=None):
     dev = _same_device(codes, scales)
     out = _out(out, (G, N, K), torch.bfloat16, dev, "out")
     _same_device(codes, out)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call("dequantize_mxfp4", _ptr(codes), _ptr(scales), K, N, G, _ptr(out), _stream(dev))
     return out
 
@@ -760,7 +780,7 @@ def _mxfp4_product(name, x, codes, scales, group_sizes, slot_of_row, topk, out, 
     out = _out(out, (M, N // 2 if swiglu else N), torch.bfloat16, dev, "out")
     _same_device(x, out)
     ws, need = _workspace(OP_MXFP4, T, K, N, G, dev, tile_m=0, workspace=workspace)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _call(name, _ptr(x), _ptr(codes), _ptr(scales), _ptr(group_sizes), _ptr(slot_of_row), int(topk), T, M, K, N, G,
               _ptr(out), _ptr(ws), need, _ptr(dev_status), _stream(dev))
     return out

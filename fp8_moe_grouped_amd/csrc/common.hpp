@@ -244,6 +244,20 @@ __device__ __forceinline__ int wave_incl_scan(int v) {
   return v;
 }
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {     // lanes without a source add 0
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+// Inclusive prefix sum across the wave without LDS.
+__device__ __forceinline__ int wave_scan_dpp(int v) {
+  v = dpp_add<0x111, 0xF>(v);                       // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);                       // row_bcast 15 into rows 1 and 3
+  return dpp_add<0x143, 0xC>(v);                    // row_bcast 31 into rows 2 and 3
+}
+
 // ----------------------------------------------------------------- schedule
 
 // Number of valid rows: sum of max(size, 0), clamped to M.  Computed by one

@@ -32,20 +32,6 @@ __device__ __forceinline__ v4f mfma_mxfp4(const v4i& a, const v4i& b, const v4f&
 
 // ---------------------------------------------------------------- schedule
 
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_add(int v) {     // lanes without a source add 0
-  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
-}
-// Inclusive prefix sum across the wave without LDS.
-__device__ __forceinline__ int wave_scan_dpp(int v) {
-  v = dpp_add<0x111, 0xF>(v);                       // row_shr 1, 2, 4, 8
-  v = dpp_add<0x112, 0xF>(v);
-  v = dpp_add<0x114, 0xF>(v);
-  v = dpp_add<0x118, 0xF>(v);
-  v = dpp_add<0x142, 0xA>(v);                       // row_bcast 15 into rows 1 and 3
-  return dpp_add<0x143, 0xC>(v);                    // row_bcast 31 into rows 2 and 3
-}
-
 // The experts' rows and tiles of BM rows, 64 experts at a time, one a lane.  Every
 // wave finds its own tile in registers: the LDS table of build_group_table (one
 // wave's shuffles, a barrier, a binary search) took 9400 cycles from the block's

@@ -14,16 +14,24 @@
 //   dx[t, ids_j] = w_j (dw_j - s), 0 elsewhere          (renormalize)
 //   dx[t, e]     = [e = ids_j] w_j dw_j - p_e s         (otherwise)
 //
-// A wave holds one token's logits, as keys whose unsigned order is the logits'
-// order, and takes the maximum k times.  A token's choices are distinct, so the
-// wave counts them into its LDS histogram without conflicts, and the count
-// before the increment is the slot's rank among the wave's slots of that
-// expert.  Waves of a block and then blocks are joined by prefix sums of the
-// histograms: the order of slots never depends on timing.
+// A token's logits lie in a row of 16 lanes (four tokens a wave) or, for more than
+// 256 experts or 16 choices, in the whole wave; each becomes a key that holds its
+// order and its expert, so that keys are distinct and the lower expert wins a tie.
+// A lane sorts its keys once with a network; k times the largest head over the
+// lanes is taken and its lane's list moves up.  (Searching all keys k times, one
+// token a wave, was bound by its instructions: 18 us for 16384 x 256 bf16, k = 8,
+// against 8.1 us now, of which 2 us are the bytes.)
+//
+// A token's choices are distinct, so a wave counts them into its LDS histogram
+// without conflicts, and the count before the increment is the slot's rank among
+// the wave's slots of that expert.  Waves of a block and then blocks are joined by
+// prefix sums of the histograms: the order of slots never depends on timing.
 #include "common.hpp"
 #include "launch.hpp"
 
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 namespace fp8gmm {
 namespace {
@@ -33,186 +41,336 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kTokensPerWave = 4;
 constexpr int kTokensPerBlock = kWaves * kTokensPerWave;   // per chunk
 constexpr int kMaxBlocks = 512;                     // longer batches give a block several chunks
-constexpr uint32_t kKeyMasked = 0x007FFFFFu;        // key of -inf
-
-// Unsigned order of the keys = order of the floats; -0 equals +0, NaN is above +inf.
-__device__ __forceinline__ uint32_t order_key(float x) {
-  const uint32_t u = __float_as_uint(x + 0.0f);     // -0 + 0 = +0
-  const uint32_t key = u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
-  return x != x ? 0xFFFFFFFFu : key;
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu));
-}
 
 template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
+__device__ __forceinline__ uint32_t dpp_row(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
-// Maximum over the wave, in a scalar register (rotations within rows of 16, then the four rows).
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-  v = dpp_max<0x128>(v);
-  v = dpp_max<0x124>(v);
-  v = dpp_max<0x122>(v);
-  v = dpp_max<0x121>(v);
-  const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16));
-  const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
-  return max(a, b);
+template <int CTRL>
+__device__ __forceinline__ float dpp_row(float v) {
+  return __uint_as_float(dpp_row<CTRL>(__float_as_uint(v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_row(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp_row<CTRL>((uint32_t)u) | (uint64_t)dpp_row<CTRL>((uint32_t)(u >> 32)) << 32);
+}
+// v of the lane whose row index differs in bit 0 (B = 16) or bit 1 (B = 32): exchanges rows or halves.
+template <int B>
+__device__ __forceinline__ uint32_t other_rows(uint32_t v, bool upper) {
+  if (B == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return upper ? r[0] : r[1];
+  }
+  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return upper ? r[0] : r[1];
+}
+template <int B>
+__device__ __forceinline__ float other_rows(float v, bool upper) {
+  return __uint_as_float(other_rows<B>(__float_as_uint(v), upper));
+}
+template <int B>
+__device__ __forceinline__ double other_rows(double v, bool upper) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)other_rows<B>((uint32_t)u, upper) |
+                                        (uint64_t)other_rows<B>((uint32_t)(u >> 32), upper) << 32);
 }
 
-__device__ __forceinline__ float wave_fsum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+// Reduction over the L lanes that share a token, to all of them (rotations within a row, then across rows).
+// Every lane joins the same pairs, so all hold the same sum.
+template <int L, typename T, typename F>
+__device__ __forceinline__ T reduce(T v, F f) {
+  v = f(v, dpp_row<0x128>(v));
+  v = f(v, dpp_row<0x124>(v));
+  v = f(v, dpp_row<0x122>(v));
+  v = f(v, dpp_row<0x121>(v));
+  if (L == 64) {
+    v = f(v, other_rows<16>(v, (threadIdx.x & 16) != 0));
+    v = f(v, other_rows<32>(v, (threadIdx.x & 32) != 0));
+  }
   return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return reduce<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+  return reduce<L>(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
+}
+
+// The wave's lanes see each other's LDS writes past this point: LDS serves a wave in order, and
+// the compiler may neither move nor forward accesses across it.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 __device__ __forceinline__ float load_logit(const float* x) { return *x; }
 __device__ __forceinline__ float load_logit(const uint16_t* x) { return __uint_as_float((uint32_t)*x << 16); }
 
-// The k choices of one token: lane j < k returns choice j.  V logits per lane,
-// logit e = 64 * i + lane in x[i].
-template <int V>
-__device__ __forceinline__ void choose(const float (&x)[V], int E, int k, bool renorm, int lane, int& id, float& w) {
-  uint32_t key[V];
+// Keys: larger for the larger logit, then for the lower expert.  -0 equals +0, NaN is above +inf;
+// a masked logit (-inf) is at or below kMasked, a place past the experts is kNone.
+template <typename TX>
+struct Order;
+
+// bf16: the bits as an unsigned number, the complement of the expert below them.
+template <>
+struct Order<uint16_t> {
+  using Key = uint32_t;
+  static constexpr Key kMasked = 0x007FFFFFu, kNone = 0;
+  static __device__ __forceinline__ Key key(float x, int e) {
+    const uint32_t u = __float_as_uint(x + 0.0f);   // -0 + 0 = +0
+    const uint32_t o = x != x ? 0xFFFF0000u : u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+    return (o & 0xFFFF0000u) | (uint32_t)(0xFFFF - e);
+  }
+  static __device__ __forceinline__ int expert(Key k) { return 0xFFFF - (int)(k & 0xFFFFu); }
+  static __device__ __forceinline__ float value(Key k) {
+    return __uint_as_float(k & 0x80000000u ? (k & 0x7FFF0000u) : ~(k | 0xFFFFu));
+  }
+  static __device__ __forceinline__ Key larger(Key a, Key b) { return max(a, b); }
+  static __device__ __forceinline__ Key smaller(Key a, Key b) { return min(a, b); }
+};
+
+// f32: the value in f64, whose mantissa has 29 bits to spare for the expert (a negative key grows
+// with its distance from zero, so it takes the expert itself); infinities and NaN become finite
+// numbers beyond the f32 range, so that maximum and minimum instructions order them.
+template <>
+struct Order<float> {
+  using Key = double;
+  static constexpr Key kInf = 0x1p200, kNan = 0x1p300, kMasked = -0x1p200, kNone = -0x1p400;
+  static __device__ __forceinline__ Key key(float x, int e) {
+    double d = __builtin_fmin(__builtin_fmax((double)(x + 0.0f), -kInf), kInf);
+    d = x != x ? kNan : d;
+    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, d) | (uint64_t)(uint32_t)(d < 0 ? e : 1023 - e));
+  }
+  static __device__ __forceinline__ int expert(Key k) {
+    const int low = (int)(__builtin_bit_cast(uint64_t, k) & 1023);
+    return k < 0 ? low : 1023 - low;
+  }
+  static __device__ __forceinline__ float value(Key k) {
+    const double d = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~1023ull);
+    return d == kNan ? __builtin_nanf("") : (float)d;   // 2^200 overflows to infinity
+  }
+  static __device__ __forceinline__ Key larger(Key a, Key b) { return __builtin_fmax(a, b); }
+  static __device__ __forceinline__ Key smaller(Key a, Key b) { return __builtin_fmin(a, b); }
+};
+
+// Batcher's odd-even merge sort of n = 4, 8 or 16 as a list of exchanges.
+struct Network {
+  int n = 0;
+  uint8_t a[64] = {}, b[64] = {};
+};
+constexpr Network network(int n) {
+  Network w;
+  for (int p = 1; p < n; p *= 2)
+    for (int k = p; k >= 1; k /= 2)
+      for (int j = k % p; j + k < n; j += 2 * k)
+        for (int i = 0; i < k && i + j + k < n; ++i)
+          if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            w.a[w.n] = (uint8_t)(i + j);
+            w.b[w.n] = (uint8_t)(i + j + k);
+            ++w.n;
+          }
+  return w;
+}
+template <typename O, int V, int... I>
+__device__ __forceinline__ void sort_down(typename O::Key (&s)[V], std::integer_sequence<int, I...>) {
+  constexpr Network w = network(V);
+  auto exchange = [&](auto& x, auto& y) {
+    const auto big = O::larger(x, y), small = O::smaller(x, y);
+    x = big;
+    y = small;
+  };
+  (exchange(s[w.a[I]], s[w.b[I]]), ...);
+}
+
+// Lane `at` of the L that share a token holds the experts of chunks at, at + L, ..: C logits each (16 bytes).
+template <int L, int C>
+__device__ __forceinline__ int expert_of(int at, int i) { return (i / C * L + at) * C + i % C; }
+
+template <int L, int V, typename TX>
+__device__ __forceinline__ void load_logits(const TX* row, int E, int at, bool here, bool wide, float (&x)[V]) {
+  constexpr int C = 16 / (int)sizeof(TX);
+  if (wide) {                                       // E is a multiple of C: a chunk is inside or outside
 #pragma unroll
-  for (int i = 0; i < V; ++i) key[i] = 64 * i + lane < E ? order_key(x[i]) : 0u;
-  uint32_t top = 0;
-  id = -1;
-  uint32_t mine = kKeyMasked;
-  for (int j = 0; j < k; ++j) {
-    uint32_t m = key[0];
+    for (int i = 0; i < V; i += C) {
+      const int e = expert_of<L, C>(at, i);
+      const v4i w = here && e < E ? *reinterpret_cast<const v4i*>(row + e) : (v4i){0, 0, 0, 0};
 #pragma unroll
-    for (int i = 1; i < V; ++i) m = max(m, key[i]);
-    m = wave_umax(m);
-    if (j == 0) top = m;
-    if (m <= kKeyMasked) break;                     // only masked logits are left
-    bool found = false;
+      for (int c = 0; c < C; ++c)
+        x[i + c] = C == 4 ? __uint_as_float((uint32_t)w[c % 4])
+                          : (c & 1 ? bf16_hi((uint32_t)w[c / 2 % 4]) : bf16_lo((uint32_t)w[c / 2 % 4]));
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const uint64_t hit = __ballot(key[i] == m);
-      if (!found && hit != 0) {                     // the lowest index of the largest value
-        const int at = __ffsll((unsigned long long)hit) - 1;
-        if (lane == at) key[i] = 0;
-        if (lane == j) {
-          id = 64 * i + at;
-          mine = m;
-        }
-        found = true;
-      }
+      const int e = expert_of<L, C>(at, i);
+      x[i] = here && e < E ? load_logit(row + e) : 0.f;
     }
   }
-  const float big = key_value(top);
-  float total;
-  const float e = id >= 0 ? expf(key_value(mine) - big) : 0.f;
-  if (renorm) {
-    total = wave_fsum(e);
-  } else {
-    total = 0.f;
+}
+
+// The k choices of a token: lane j < k of its lanes returns choice j.  A lane's list never moves up
+// more than k - 1 places, so its first D = min(V, k's bound) keys are all that is read.
+template <int L, int V, int D, typename TX>
+__device__ __forceinline__ void choose(const float (&x)[V], int E, int k, bool renorm, int at, int& id, float& w) {
+  using O = Order<TX>;
+  using Key = typename O::Key;
+  constexpr int C = 16 / (int)sizeof(TX);
+  float big = -__builtin_inff(), total = 0.f;
+  if (!renorm) {                                    // over all logits, before their registers become keys
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (64 * i + lane < E) total += expf(x[i] - big);
-    total = wave_fsum(total);
+      if (expert_of<L, C>(at, i) < E) big = __builtin_fmaxf(big, x[i]);
+    big = lanes_max<L>(big);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (expert_of<L, C>(at, i) < E) total += expf(x[i] - big);
+    total = lanes_sum<L>(total);
   }
+  Key s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = expert_of<L, C>(at, i);
+    s[i] = e < E ? O::key(x[i], e) : O::kNone;
+  }
+  sort_down<O>(s, std::make_integer_sequence<int, network(V).n>{});
+  Key top = O::kNone, mine = O::kNone;
+  for (int j = 0; j < k; ++j) {
+    const Key m = reduce<L>(s[0], [](Key a, Key b) { return O::larger(a, b); });
+    if (j == 0) top = m;
+    if (at == j) mine = m;
+    const bool taken = s[0] == m;
+#pragma unroll
+    for (int i = 0; i < D; ++i) {                   // copies: a conditional of two elements would index the array
+      const Key own = s[i], next = i + 1 < D ? Key(s[i + 1]) : O::kNone;
+      s[i] = taken ? next : own;
+    }
+  }
+  id = mine > O::kMasked ? O::expert(mine) : -1;
+  if (renorm) big = O::value(top);
+  const float e = id >= 0 ? expf(O::value(mine) - big) : 0.f;
+  if (renorm) total = lanes_sum<L>(e);
   w = id >= 0 ? e / total : 0.f;
 }
 
 // hist holds a block's slots per expert as 16 bits (a block has fewer than 2^16
 // tokens, and a token chooses an expert once): [blocks][Ep], Ep = E rounded up to 8.
-// ONE: the grid is one block, which places the slots itself.
-template <int V, typename TX, bool ONE>
+// ONE: the grid is one block, of as many waves as its tokens need, which places the
+// slots itself.
+template <int L, int V, int D, typename TX, bool ONE>
 __global__ __launch_bounds__(kThreads) void route_topk_kernel(const TX* __restrict__ logits, int T, int E, int k,
                                                              int renorm, int chunks, int* __restrict__ ids,
                                                              float* __restrict__ weights, int* __restrict__ row_of_slot,
                                                              uint16_t* __restrict__ hist, int* __restrict__ group_sizes,
                                                              int* __restrict__ slot_of_row) {
+  constexpr int kRounds = kTokensPerWave * L / 64;  // tokens of a wave, 64 / L at a time
   extern __shared__ int smem[];
   int* const seen = smem;                           // [E] slots of earlier chunks (ONE: first row of the expert)
-  int* const cnt = smem + E;                        // [kWaves][E]
+  int* const cnt = smem + E;                        // [waves][E]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  for (int e = tid; e < E; e += kThreads) seen[e] = 0;
+  const int threads = blockDim.x, waves = threads >> 6;
+  const int at = lane % L, sub = lane / L;
+  const bool wide = E % (16 / (int)sizeof(TX)) == 0;
+  for (int e = tid; e < E; e += threads) seen[e] = 0;
   for (int c = 0; c < chunks; ++c) {
-    const int t0 = (blockIdx.x * chunks + c) * kTokensPerBlock + wave * kTokensPerWave;
-    for (int i = tid; i < kWaves * E; i += kThreads) cnt[i] = 0;
-    float x[kTokensPerWave][V];
-#pragma unroll
-    for (int q = 0; q < kTokensPerWave; ++q)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = 64 * i + lane;
-        x[q][i] = (t0 + q < T && e < E) ? load_logit(logits + (size_t)(t0 + q) * E + e) : 0.f;
-      }
+    const int t0 = (blockIdx.x * chunks + c) * kTokensPerBlock + wave * kTokensPerWave + sub;
+    float x[V];
+    load_logits<L, V>(logits + (size_t)t0 * E, E, at, t0 < T, wide, x);
+    for (int i = tid; i < waves * E; i += threads) cnt[i] = 0;
     __syncthreads();
-    int id[kTokensPerWave], rank[kTokensPerWave];
+    int id[kRounds], rank[kRounds];
 #pragma unroll
-    for (int q = 0; q < kTokensPerWave; ++q) {
-      id[q] = -1;
+    for (int q = 0; q < kRounds; ++q) {
+      const int t = t0 + q * (64 / L);
+      float w;
+      if (q > 0) load_logits<L, V>(logits + (size_t)t * E, E, at, t < T, wide, x);
+      choose<L, V, D, TX>(x, E, k, renorm != 0, at, id[q], w);
       rank[q] = 0;
-      if (t0 + q < T) {
-        float w;
-        choose<V>(x[q], E, k, renorm != 0, lane, id[q], w);
-        if (lane < k) {
-          const size_t at = (size_t)(t0 + q) * k + lane;
-          ids[at] = id[q];
-          weights[at] = w;
-          if (id[q] >= 0) {
-            rank[q] = cnt[wave * E + id[q]];
-            cnt[wave * E + id[q]] = rank[q] + 1;
-          }
+      const bool mine = t < T && at < k;
+      if (mine) {
+        const size_t slot = (size_t)t * k + at;
+        ids[slot] = id[q];
+        weights[slot] = w;
+      }
+#pragma unroll
+      for (int v = 0; v < 64 / L; ++v) {            // one token after the other
+        if (mine && id[q] >= 0 && sub == v) {
+          rank[q] = cnt[wave * E + id[q]];
+          cnt[wave * E + id[q]] = rank[q] + 1;
         }
+        wave_lds_order();
       }
     }
     __syncthreads();
-    for (int e = tid; e < E; e += kThreads) {       // counts -> first rank of each wave
+    for (int e = tid; e < E; e += threads) {        // counts -> first rank of each wave
       int s = seen[e];
+      if (ONE) {                                    // one wave to 16
+        for (int v = 0; v < waves; ++v) {
+          const int n = cnt[v * E + e];
+          cnt[v * E + e] = s;
+          s += n;
+        }
+      } else {
+        int n[kWaves];
 #pragma unroll
-      for (int v = 0; v < kWaves; ++v) {
-        const int n = cnt[v * E + e];
-        cnt[v * E + e] = s;
-        s += n;
+        for (int v = 0; v < kWaves; ++v) n[v] = cnt[v * E + e];
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+          cnt[v * E + e] = s;
+          s += n[v];
+        }
       }
       seen[e] = s;
     }
     __syncthreads();
     if (ONE) {
-      const int n = tid < E ? seen[tid] : 0;        // E <= kThreads
-      if (tid < E) group_sizes[tid] = n;
-      __shared__ int part[kWaves];
-      const int incl = wave_incl_scan(n);
-      if (lane == 63) part[wave] = incl;
+      int all = 0;
+      if (wave == 0)                                // slots per expert -> first row of the expert
+        for (int base = 0; base < E; base += 64) {
+          const int e = base + lane, n = e < E ? seen[e] : 0;
+          const int upto = all + wave_scan_dpp(n);
+          if (e < E) {
+            group_sizes[e] = n;
+            seen[e] = upto - n;
+          }
+          all = __builtin_amdgcn_readlane(upto, 63);
+        }
       __syncthreads();
-      int before = 0, all = 0;
+      // rows past the last slot's: as many as there are masked choices
+      if (wave == 0)
+        for (int r = all + lane; r < T * k; r += 64) slot_of_row[r] = -1;
 #pragma unroll
-      for (int v = 0; v < kWaves; ++v) {
-        if (v < wave) before += part[v];
-        all += part[v];
-      }
-      if (tid < E) seen[tid] = before + incl - n;
-      __syncthreads();
-      for (int r = all + tid; r < T * k; r += kThreads) slot_of_row[r] = -1;
-#pragma unroll
-      for (int q = 0; q < kTokensPerWave; ++q)
-        if (t0 + q < T && lane < k) {
-          const int slot = (t0 + q) * k + lane;
+      for (int q = 0; q < kRounds; ++q) {
+        const int t = t0 + q * (64 / L);
+        if (t < T && at < k) {
+          const int slot = t * k + at;
           const int row = id[q] < 0 ? -1 : seen[id[q]] + cnt[wave * E + id[q]] + rank[q];
           row_of_slot[slot] = row;
           if (row >= 0) slot_of_row[row] = slot;
         }
+      }
     } else {
 #pragma unroll
-      for (int q = 0; q < kTokensPerWave; ++q)
-        if (t0 + q < T && lane < k && id[q] >= 0)   // rank within the block for now
-          row_of_slot[(size_t)(t0 + q) * k + lane] = cnt[wave * E + id[q]] + rank[q];
+      for (int q = 0; q < kRounds; ++q) {
+        const int t = t0 + q * (64 / L);
+        if (t < T && at < k && id[q] >= 0)          // rank within the block for now
+          row_of_slot[(size_t)t * k + at] = cnt[wave * E + id[q]] + rank[q];
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
   if (!ONE) {
     const int Ep = (E + 7) & ~7;
-    for (int e = tid; e < Ep; e += kThreads) hist[(size_t)blockIdx.x * Ep + e] = (uint16_t)(e < E ? seen[e] : 0);
+    for (int e = tid; e < Ep; e += threads) hist[(size_t)blockIdx.x * Ep + e] = (uint16_t)(e < E ? seen[e] : 0);
   }
 }
 
 // Places the slots of block b: an expert's first row, plus its slots in earlier
 // blocks, plus the rank within the block that route_topk_kernel left in row_of_slot.
+// Every block sums the whole histogram (128 KB at 16384 x 256, from L2) instead of a
+// launch between that would scan it.
 __global__ __launch_bounds__(kThreads) void route_place_kernel(const int* __restrict__ ids,
                                                               const uint16_t* __restrict__ hist, int T, int E, int k,
                                                               int chunks, int* __restrict__ group_sizes,
@@ -225,15 +383,20 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const int* __rest
   __shared__ int part[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int b = blockIdx.x, nb = gridDim.x;
+  auto place = [&](int e) { return (e & 7) * ne + (e >> 3); };   // eight lanes' experts in different banks
+  const int s0 = b * chunks * kTokensPerBlock * k;  // T * k < 2^24, and a block starts below T
+  const int s1 = min(s0 + chunks * kTokensPerBlock * k, T * k);
+  const int mine = s0 + tid;                        // the first slot's loads run while the histogram is summed
+  int id0 = mine < s1 ? ids[mine] : -1, rank0 = mine < s1 ? row_of_slot[mine] : 0;
   for (int e = tid; e < 2 * Ep; e += kThreads) smem[e] = 0;
   __syncthreads();
   // thread (segment, 8 experts): the histogram's rows segment, segment + nseg, ...
-  const int nseg = kThreads / ne, seg = tid / ne, e0 = (tid % ne) * 8;
+  const int nseg = kThreads / ne, seg = tid / ne, g8 = tid % ne;
   if (seg < nseg) {
     int before[8] = {}, all[8] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (int r = seg; r < nb; r += nseg) {
-      const v4i h = *reinterpret_cast<const v4i*>(hist + (size_t)r * Ep + e0);
+      const v4i h = *reinterpret_cast<const v4i*>(hist + (size_t)r * Ep + 8 * g8);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int n = (int)(((uint32_t)h[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
@@ -243,14 +406,14 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const int* __rest
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {                   // sums of whole numbers: any order gives the same
-      if (before[i]) atomicAdd(&first[e0 + i], before[i]);
-      if (all[i]) atomicAdd(&total[e0 + i], all[i]);
+      if (before[i]) atomicAdd(&first[i * ne + g8], before[i]);
+      if (all[i]) atomicAdd(&total[i * ne + g8], all[i]);
     }
   }
   __syncthreads();
-  const int n = tid < E ? total[tid] : 0;           // E <= kThreads
+  const int n = tid < E ? total[place(tid)] : 0;    // E <= kThreads
   if (b == 0 && tid < E) group_sizes[tid] = n;
-  const int incl = wave_incl_scan(n);
+  const int incl = wave_scan_dpp(n);
   if (lane == 63) part[wave] = incl;
   __syncthreads();
   int offset = 0, rows = 0;
@@ -259,79 +422,95 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const int* __rest
     if (v < wave) offset += part[v];
     rows += part[v];
   }
-  if (tid < E) first[tid] += offset + incl - n;
+  if (tid < E) first[place(tid)] += offset + incl - n;
   __syncthreads();
-  const int s0 = b * chunks * kTokensPerBlock * k;  // T * k < 2^24, and a block starts below T
-  const int s1 = min(s0 + chunks * kTokensPerBlock * k, T * k);
-  for (int s = s0 + tid; s < s1; s += kThreads) {
-    const int id = ids[s];
-    const int row = id < 0 ? -1 : first[id] + row_of_slot[s];
+  for (int s = mine; s < s1; s += kThreads) {
+    const int id = s == mine ? id0 : ids[s], rank = s == mine ? rank0 : row_of_slot[s];
+    const int row = id < 0 ? -1 : first[place(id)] + rank;
     row_of_slot[s] = row;
     if (row >= 0) slot_of_row[row] = s;
     if (s >= rows) slot_of_row[s] = -1;             // no slot is placed there
   }
 }
 
-__device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = (uint16_t)pack_bf16x2(v, 0.f); }
-
-// One wave per token.  Lane j < k holds choice j; its share of the gradient is
-// handed to the lane that holds the logit.
-template <int V, typename TX>
+// Gradient.  Lanes share tokens as above: lane j < k holds choice j and puts its
+// term into the token's row in LDS (the wave's own, so no barrier), which the lanes
+// then read as their chunks.
+template <int L, int V, typename TX>
 __global__ __launch_bounds__(256) void route_bwd_kernel(const float* __restrict__ dweights,
                                                         const TX* __restrict__ logits, const int* __restrict__ ids,
                                                         const float* __restrict__ weights, int T, int E, int k,
                                                         int renorm, TX* __restrict__ dlogits) {
-  const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (t >= T) return;
+  constexpr int C = 16 / (int)sizeof(TX);
+  __shared__ __attribute__((aligned(16))) float rows[4][64 * V];
+  const int lane = threadIdx.x & 63, at = lane % L, sub = lane / L;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = (blockIdx.x * 4 + wave) * (64 / L) + sub;
+  const bool here = t < T, wide = E % C == 0;
+  float* const row = rows[wave] + sub * L * V;
   int id = -1;
   float w = 0.f, dw = 0.f;
-  if (lane < k) {
-    const size_t at = (size_t)t * k + lane;
-    id = ids[at];
-    if (id >= 0 && id < E) {                        // a masked choice's gradient is not read
-      w = weights[at];
-      dw = dweights[at];
+  if (here && at < k) {
+    const size_t s = (size_t)t * k + at;
+    id = ids[s];
+    w = weights[s];
+    dw = dweights[s];
+    if (id < 0 || id >= E) {                        // a masked choice's gradient does not count
+      id = -1;
+      w = dw = 0.f;
     }
   }
-  const float inner = wave_fsum(w * dw);
+  float x[V];
+  if (!renorm) load_logits<L, V>(logits + (size_t)t * E, E, at, here, wide, x);
+#pragma unroll
+  for (int i = 0; i < V; i += 4) *reinterpret_cast<v4f*>(row + expert_of<L, C>(at, i)) = (v4f){0.f, 0.f, 0.f, 0.f};
+  const float inner = lanes_sum<L>(w * dw);
+  wave_lds_order();
+  if (id >= 0) atomicAdd(row + id, w * (renorm ? dw - inner : dw));   // experts of a token are distinct
+  wave_lds_order();
   float d[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) d[i] = 0.f;
-  const float here = w * (renorm ? dw - inner : dw);
-  for (int j = 0; j < k; ++j) {
-    const int e = __builtin_amdgcn_readlane(id, j);
-    const float v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, here), j));
+  for (int i = 0; i < V; i += 4) {
+    const v4f v = *reinterpret_cast<const v4f*>(row + expert_of<L, C>(at, i));
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e == 64 * i + lane) d[i] += v;
+    for (int c = 0; c < 4; ++c) d[i + c] = v[c];
   }
   if (!renorm) {
-    float x[V], top = -__builtin_inff();
+    float top = -__builtin_inff(), total = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (expert_of<L, C>(at, i) < E) top = __builtin_fmaxf(top, x[i]);
+    top = lanes_max<L>(top);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = 64 * i + lane;
-      x[i] = e < E ? load_logit(logits + (size_t)t * E + e) : -__builtin_inff();
-      top = __builtin_fmaxf(top, x[i]);
+      x[i] = expert_of<L, C>(at, i) < E ? expf(x[i] - top) : 0.f;
+      total += x[i];
     }
-    top = wave_max(top);
-    if (top != -__builtin_inff()) {                 // a token without experts has no gradient
-      float total = 0.f;
+    total = lanes_sum<L>(total);
+    const bool some = top != -__builtin_inff();     // a token without experts has no gradient
+    const float share = inner / total;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        x[i] = expf(x[i] - top);
-        total += x[i];
-      }
-      total = wave_fsum(total);
-#pragma unroll
-      for (int i = 0; i < V; ++i) d[i] -= x[i] / total * inner;
-    }
+    for (int i = 0; i < V; ++i) d[i] = some ? d[i] - x[i] * share : 0.f;
   }
+  if (!here) return;
+  TX* const out = dlogits + (size_t)t * E;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = 64 * i + lane;
-    if (e < E) store_logit(dlogits + (size_t)t * E + e, d[i]);
+  for (int i = 0; i < V; i += C) {
+    const int e = expert_of<L, C>(at, i);
+    uint32_t o[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      o[c] = C == 4 ? __float_as_uint(d[i + c]) : pack_bf16x2(d[i + C / 4 * c], d[i + C / 4 * c + 1]);
+    if (wide) {
+      if (e < E) *reinterpret_cast<v4i*>(out + e) = (v4i){(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (e + c < E) {
+          if constexpr (C == 4) out[e + c] = d[i + c];
+          else out[e + c] = (TX)(o[c / 2] >> (16 * (c & 1)));
+        }
+    }
   }
 }
 
@@ -341,19 +520,20 @@ int route_blocks(int T, int& chunks) {
   return (nc + chunks - 1) / chunks;
 }
 
-template <int V, typename TX>
+template <int L, int V, int D, typename TX>
 hipError_t route_impl(const TX* logits, int T, int E, int k, int renorm, int* ids, float* weights, int* group_sizes,
                       int* row_of_slot, int* slot_of_row, uint16_t* hist, hipStream_t stream) {
   int chunks;
   const int nb = route_blocks(T, chunks);
-  const size_t lds = sizeof(int) * (size_t)E * (kWaves + 1);
   if (nb <= 1) {
-    hipLaunchKernelGGL((route_topk_kernel<V, TX, true>), dim3(1), dim3(kThreads), lds, stream, logits, T, E, k, renorm,
-                       1, ids, weights, row_of_slot, hist, group_sizes, slot_of_row);
+    const int waves = std::max(1, (T + kTokensPerWave - 1) / kTokensPerWave);
+    hipLaunchKernelGGL((route_topk_kernel<L, V, D, TX, true>), dim3(1), dim3(64 * waves), sizeof(int) * E * (waves + 1),
+                       stream, logits, T, E, k, renorm, 1, ids, weights, row_of_slot, hist, group_sizes, slot_of_row);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((route_topk_kernel<V, TX, false>), dim3(nb), dim3(kThreads), lds, stream, logits, T, E, k, renorm,
-                     chunks, ids, weights, row_of_slot, hist, group_sizes, slot_of_row);
+  hipLaunchKernelGGL((route_topk_kernel<L, V, D, TX, false>), dim3(nb), dim3(kThreads), sizeof(int) * E * (kWaves + 1),
+                     stream, logits, T, E, k, renorm, chunks, ids, weights, row_of_slot, hist, group_sizes,
+                     slot_of_row);
   hipError_t st = hipGetLastError();
   if (st != hipSuccess) return st;
   hipLaunchKernelGGL(route_place_kernel, dim3(nb), dim3(kThreads), sizeof(int) * 2 * (size_t)((E + 7) & ~7), stream,
@@ -361,30 +541,40 @@ hipError_t route_impl(const TX* logits, int T, int E, int k, int renorm, int* id
   return hipGetLastError();
 }
 
+// A lane holds whole 16-byte chunks: 4 logits in f32, 8 in bf16.
 template <typename TX>
 hipError_t route_pick(const TX* logits, int T, int E, int k, int renorm, int* ids, float* weights, int* group_sizes,
                       int* row_of_slot, int* slot_of_row, uint16_t* hist, hipStream_t stream) {
-#define ROUTE(V) \
-  route_impl<V, TX>(logits, T, E, k, renorm, ids, weights, group_sizes, row_of_slot, slot_of_row, hist, stream)
-  if (E <= 64) return ROUTE(1);
-  if (E <= 128) return ROUTE(2);
-  if (E <= 256) return ROUTE(4);
-  if (E <= 512) return ROUTE(8);
-  return ROUTE(16);
+  constexpr int C = 16 / (int)sizeof(TX);
+#define ROUTE(L, V)                                                                                                    \
+  (k <= 8 ? route_impl<L, V, V < 8 ? V : 8, TX>(logits, T, E, k, renorm, ids, weights, group_sizes, row_of_slot,       \
+                                                slot_of_row, hist, stream)                                             \
+          : route_impl<L, V, V, TX>(logits, T, E, k, renorm, ids, weights, group_sizes, row_of_slot, slot_of_row, hist, \
+                                    stream))
+  if (k <= 16) {
+    if (E <= 16 * C) return ROUTE(16, C);
+    if (E <= 128) return ROUTE(16, 8);              // f32 alone: 16 * C is 128 in bf16
+    if (E <= 256) return ROUTE(16, 16);
+  }
+  if (E <= 64 * C) return ROUTE(64, C);
+  if (E <= 512) return ROUTE(64, 8);                // f32 alone
+  return ROUTE(64, 16);
 #undef ROUTE
 }
 
 template <typename TX>
 hipError_t route_bwd_pick(const float* dweights, const TX* logits, const int* ids, const float* weights, int T, int E,
                           int k, int renorm, TX* dlogits, hipStream_t stream) {
-#define ROUTE(V)                                                                                                     \
-  hipLaunchKernelGGL((route_bwd_kernel<V, TX>), dim3((T + 3) / 4), dim3(256), 0, stream, dweights, logits, ids, weights, \
-                     T, E, k, renorm, dlogits)
-  if (E <= 64) ROUTE(1);
-  else if (E <= 128) ROUTE(2);
-  else if (E <= 256) ROUTE(4);
-  else if (E <= 512) ROUTE(8);
-  else ROUTE(16);
+  constexpr int C = 16 / (int)sizeof(TX);
+#define ROUTE(L, V)                                                                                               \
+  hipLaunchKernelGGL((route_bwd_kernel<L, V, TX>), dim3((T + 256 / L - 1) / (256 / L)), dim3(256), 0, stream,      \
+                     dweights, logits, ids, weights, T, E, k, renorm, dlogits)
+  if (k <= 16 && E <= 16 * C) ROUTE(16, C);
+  else if (k <= 16 && E <= 128) ROUTE(16, 8);       // f32 alone: 16 * C is 128 in bf16
+  else if (k <= 16 && E <= 256) ROUTE(16, 16);
+  else if (E <= 64 * C) ROUTE(64, C);
+  else if (E <= 512) ROUTE(64, 8);                  // f32 alone
+  else ROUTE(64, 16);
 #undef ROUTE
   return hipGetLastError();
 }
