@@ -6,14 +6,10 @@
 //   out[r, n] = bf16(y[r, n]),  or with SwiGLU over columns [gate | up] of N = 2I:
 //   out[r, i] = bf16( silu(y[r, i]) * y[r, I + i] )
 //
-// The scaled matrix instruction (16x16x128) applies the blocks' powers of two and
-// accumulates in f32.  A lane's operand is 32 consecutive k of one row, which is
-// one block with one scale byte.  The weight is the first operand, so a lane ends
-// with four consecutive columns of one row.
-//
-// A block owns 16*MA rows x 32 columns of one expert (16 gate and the matching 16
-// up columns for SwiGLU); its four waves share the contraction, 256 k (one cache
-// line of codes a row) at a time in turn, and join their sums in LDS.
+// The scaled matrix instruction (32x32x64) applies the blocks' powers of two and
+// accumulates in f32.  A lane's operand is 32 consecutive k of one row, which is one
+// block with one scale byte.  The weight is the first operand, so a lane ends with
+// four consecutive columns of one row.
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -22,13 +18,6 @@
 
 namespace fp8gmm {
 namespace {
-
-constexpr int kWaves = 4;
-
-__device__ __forceinline__ v4f mfma_mxfp4(const v4i& a, const v4i& b, const v4f& c, int sa, int sb) {
-  const v8i a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, sa, 0, sb);
-}
 
 // ---------------------------------------------------------------- schedule
 
@@ -81,110 +70,203 @@ struct TileMap {
   }
 };
 
-template <int MA, bool SWIGLU>
-__global__ __launch_bounds__(64 * kWaves) void gmm_mxfp4_split_kernel(
-    const uint8_t* __restrict__ aq, const uint32_t* __restrict__ ascale, const uint8_t* __restrict__ codes,
-    const uint32_t* __restrict__ wscale, const int* __restrict__ group_sizes, const int* __restrict__ slot_of_row,
+template <int SEL>
+__device__ __forceinline__ v16f mfma_mxfp4_32(const v4i& a, const v4i& b, const v16f& c, int sa, int sb) {
+  const v8i a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, SEL, sa, SEL, sb);
+}
+
+// Both kernels bring 256 k (a pair of stages of 128) of a row at a time: 128 bytes, one cache line, in eight
+// 16-byte chunks whose place in LDS is turned with the row, so that reads of one chunk of 16 rows hit all banks.
+constexpr int kLine = 128;
+__device__ __forceinline__ int swz(int row, int chunk) { return row * kLine + ((chunk ^ ((row >> 1) & 7)) << 4); }
+
+// Results leave through LDS as rows of COLS bf16 (16 bytes past a multiple of the banks), so that a store
+// instruction writes whole lines: with 32 rows x 32 bytes straight from the fragments 8190 x 768 x 2048 took 38 us
+// in the large tiles, with this 35.
+//
+// put16: 16 columns of a row from the two halves of a wave.  Lanes l and l + 32 hold the same row, columns
+// 8q + 4h + 0..3 (h = lane / 32) as two words a[q], q = 0, 1, and trade them so that each writes 16 bytes.
+template <int COLS>
+constexpr int kOutRow = 2 * COLS + 16;
+__device__ __forceinline__ void put16(uint8_t* p, int h, const v2i& a0, const v2i& a1) {
+  const auto x = __builtin_amdgcn_permlane32_swap(a0[0], a1[0], false, false);
+  const auto y = __builtin_amdgcn_permlane32_swap(a0[1], a1[1], false, false);
+  *reinterpret_cast<v4i*>(p + 16 * h) = (v4i){(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
+}
+// rows x COLS (the last ones cut off at column `end`) to out, whose rows are `ld` apart
+template <int COLS>
+__device__ __forceinline__ void store_rows(const uint8_t* lds, uint16_t* out, size_t ld, int rows, int end) {
+  constexpr int C = COLS / 8;
+  const int c = threadIdx.x % C;
+  if (8 * c >= end) return;
+  for (int r = threadIdx.x / C; r < rows; r += 256 / C)
+    *reinterpret_cast<v4i*>(out + r * ld + 8 * c) = *reinterpret_cast<const v4i*>(lds + r * kOutRow<COLS> + 16 * c);
+}
+__device__ __forceinline__ v2i pack4(float a, float b, float c, float d) {
+  return (v2i){(int)pack_bf16x2(a, b), (int)pack_bf16x2(c, d)};
+}
+__device__ __forceinline__ float silu_mul(float gate, float up) {   // hardware reciprocal: rounded to bf16 right after
+  return gate * __builtin_amdgcn_rcpf(1.0f + __expf(-gate)) * up;
+}
+
+// ---------------------------------------------------------------- few rows
+
+// Bound by the weights' bytes: a block streams 128 columns of one expert (SwiGLU: 64
+// gate and the matching 64 up) past up to 32 * MI of its rows.  Copies to LDS, a pair
+// a row (contiguous lines, streaming policy for the weights: 7.1 TB/s alone, where
+// operand loads of 16 rows x 64 bytes reach 6.1), into a ring of three slots: two
+// pairs in flight a block, two blocks a CU.  A wave multiplies 32 columns, SwiGLU 16
+// gate and their 16 up in one fragment, so that a lane ends with both.
+template <int MI>
+constexpr int kRing = MI <= 2 ? 3 : 2;
+
+template <int MI, bool SWIGLU>
+__global__ __launch_bounds__(256, 2) void gmm_mxfp4_stream_kernel(
+    const uint8_t* __restrict__ aq, const uint8_t* __restrict__ ascale, const uint8_t* __restrict__ codes,
+    const uint8_t* __restrict__ wscale, const int* __restrict__ group_sizes, const int* __restrict__ slot_of_row,
     int topk, int T, int G, int M, int K, int N, uint16_t* __restrict__ out, int* status) {
-  constexpr int BM = 16 * MA;
+  constexpr int BM = 32 * MI, BN = 128;
+  constexpr int kScales = 2 * 4 * 256;              // a wave's words of its rows and of its columns
+  constexpr int kSlot = (BM + BN) * kLine + kScales;
+  constexpr int kLoads = MI + 6;                    // a wave's copies of a pair
+  constexpr int R = kRing<MI>;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  v4f* const part = reinterpret_cast<v4f*>(smem);   // [kWaves][MA * 2][64]
   TileMap<BM> map;
   map.scan(group_sizes, G, M, status);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tiles = map.total, half = N >> 1;
-  const int n_tiles = N / 32;
+  const int tiles = map.total, half = N >> 1, n_tiles = N / BN;
   if ((int)blockIdx.x >= tiles * n_tiles) return;
-  const int mt = blockIdx.x % tiles, nt = blockIdx.x / tiles;
+  int mt, nt;
+  if (n_tiles % 8 == 0) {                           // all row tiles of a column tile on one XCD
+    const int i = blockIdx.x / 8;
+    mt = i % tiles;
+    nt = blockIdx.x % 8 + 8 * (i / tiles);
+  } else {
+    mt = blockIdx.x % tiles;
+    nt = blockIdx.x / tiles;
+  }
   int g = 0, g0 = 0, g1 = 0, tile = 0;
   map.locate(group_sizes, G, M, mt, g, g0, g1, tile);
   const int row0 = g0 + tile * BM, rows = min(BM, g1 - row0);
 
-  const int q = lane >> 4, r16 = lane & 15;
-  const int kw = K / 128;                           // scale words of a row
-  const uint8_t* ap[MA];
-  const uint32_t* as[MA];
-#pragma unroll
-  for (int i = 0; i < MA; ++i) {
-    const int row = row0 + min(16 * i + r16, rows - 1);   // rows past the expert's end repeat its last
-    int token = row;
-    if (slot_of_row) {
-      const int slot = slot_of_row[row];
-      token = slot < 0 ? T : min(slot / topk, T);   // row T of the quantized activations is zero
-    }
-    ap[i] = aq + (size_t)token * (K / 2) + 16 * q;
-    as[i] = ascale + (size_t)token * ((kw + 3) & ~3);
-  }
-  int col[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) col[j] = SWIGLU ? j * half + nt * 16 + r16 : nt * 32 + 16 * j + r16;
-  const uint8_t* bp[2];
-  const uint32_t* bs[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    bp[j] = codes + ((size_t)g * N + col[j]) * (K / 2) + 16 * q;
-    bs[j] = wscale + (size_t)g * kw * N + col[j];
-  }
-
-  v4f acc[MA][2];
-#pragma unroll
-  for (int i = 0; i < MA; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-  auto block128 = [&](int kb) __attribute__((always_inline)) {
-    v4i a[MA], b[2];
-    int sa[MA], sb[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      b[j] = *reinterpret_cast<const v4i*>(bp[j] + 64 * kb);
-      sb[j] = (int)(bs[j][(size_t)kb * N] >> (8 * q));
-    }
-#pragma unroll
-    for (int i = 0; i < MA; ++i) {
-      a[i] = *reinterpret_cast<const v4i*>(ap[i] + 64 * kb);
-      sa[i] = (int)(as[i][kb] >> (8 * q));
-    }
-#pragma unroll
-    for (int i = 0; i < MA; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mfma_mxfp4(b[j], a[i], acc[i][j], sb[j], sa[i]);
+  const int kw = K / 128, np = (kw + 1) / 2;
+  const uint32_t abytes = (uint32_t)K / 2, sbytes = (uint32_t)((kw + 3) / 4) * 16;
+  const BufRsrc rb = make_rsrc(codes + (size_t)g * N * abytes, (uint32_t)N * abytes);
+  const BufRsrc rsb = make_rsrc(wscale + (size_t)g * kw * N * 4, (uint32_t)kw * (uint32_t)N * 4u);
+  auto column = [&](int c) {                        // column of tile column c
+    if (!SWIGLU) return nt * BN + c;
+    const int at = nt * 64 + (c >> 5) * 16 + (c & 15);
+    return c & 16 ? half + at : at;
   };
-  for (int kb = 2 * wave; kb < kw; kb += 2 * kWaves) {
-    block128(kb);
-    if (kb + 1 < kw) block128(kb + 1);
+  uint32_t vb[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = 32 * wave + 8 * j + (lane >> 3);
+    vb[j] = (uint32_t)column(c) * abytes + (uint32_t)(((lane & 7) ^ ((c >> 1) & 7)) << 4);
+  }
+  const uint32_t vsb = ((uint32_t)(lane >> 5) * (uint32_t)N + (uint32_t)column(32 * wave + (lane & 31))) * 4u;
+  auto copy_weights = [&](int p, uint8_t* slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, LDS_PTR(void, slot + BM * kLine + (4 * wave + j) * 1024), 16, vb[j],
+                                               (uint32_t)p * kLine, 0, kCpolStream);
+    dma4(rsb, slot + (BM + BN) * kLine + 1024 + wave * 256, vsb, (uint32_t)p * (uint32_t)N * 8u);
+  };
+  copy_weights(0, smem);
+
+  // a wave copies 8 * MI rows; rows past the tile's end repeat its last
+  const int row = row0 + min(8 * MI * wave + min(lane, 8 * MI - 1), rows - 1);
+  int token = row;
+  if (slot_of_row) {
+    const int slot = slot_of_row[row];
+    token = slot < 0 ? T : min(slot / topk, T);     // row T of the quantized activations is zero
+  }
+  const uint8_t* va[MI];
+#pragma unroll
+  for (int j = 0; j < MI; ++j) {
+    const int r = 8 * (MI * wave + j) + (lane >> 3);
+    va[j] = aq + (size_t)__shfl(token, 8 * j + (lane >> 3)) * abytes + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+  }
+  const uint8_t* const vsa = ascale + (size_t)__shfl(token, (lane >> 1) & (8 * MI - 1)) * sbytes + 4 * (lane & 1);
+  auto copy_rows = [&](int p, uint8_t* slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < MI; ++j) copy16(va[j] + (size_t)p * kLine, slot + (MI * wave + j) * 1024);
+    copy4(vsa + 8 * p, slot + (BM + BN) * kLine + wave * 256);
+  };
+  copy_rows(0, smem);
+  if (R == 3 && np > 1) {
+    copy_weights(1, smem + kSlot);
+    copy_rows(1, smem + kSlot);
   }
 
+  const int h = lane >> 5, r32 = lane & 31, bcol = 32 * wave + r32;
+  v16f acc[MI];
 #pragma unroll
-  for (int i = 0; i < MA; ++i)
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) part[(wave * MA * 2 + 2 * i + j) * 64 + lane] = acc[i][j];
-  __syncthreads();
-  // wave w finishes fragments w, w + 4, ..: lane holds row r16, columns 4q + 0..3
-  for (int i = wave; i < MA; i += kWaves) {
-    v4f y[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      y[j] = part[(2 * i + j) * 64 + lane];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) y[j] += part[(w * MA * 2 + 2 * i + j) * 64 + lane];
+    for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+  int cur = 0, ahead = R - 1;                       // slots of pair p and of pair p + R - 1
+  for (int p = 0; p < np; ++p) {
+    if (R == 3 && p + 1 < np) wait_vmem_lds<kLoads>();   // pair p is there, pair p + 1 on its way
+    else wait_vmem_lds<0>();
+    barrier_only();                                 // and every wave has read pair p - 1
+    if (p + R - 1 < np) {
+      copy_weights(p + R - 1, smem + ahead * kSlot);
+      copy_rows(p + R - 1, smem + ahead * kSlot);
     }
-    const int m = 16 * i + r16;
-    if (m >= rows) continue;
-    if (SWIGLU) {
-      float o[4];
+    const uint8_t* const slot = smem + cur * kSlot;
+    const uint8_t* const sc = slot + (BM + BN) * kLine;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)   // hardware reciprocal: the product is rounded to bf16 right after
-        o[e] = y[0][e] * __builtin_amdgcn_rcpf(1.0f + __expf(-y[0][e])) * y[1][e];
-      const v2i p = {(int)pack_bf16x2(o[0], o[1]), (int)pack_bf16x2(o[2], o[3])};
-      *reinterpret_cast<v2i*>(out + (size_t)(row0 + m) * half + nt * 16 + 4 * q) = p;
+    for (int u = 0; u < 2; ++u) {
+      if (2 * p + u >= kw) break;                   // an odd K / 128 ends in half a pair
+      const int xb = *reinterpret_cast<const int*>(sc + 1024 + wave * 256 + (32 * u + r32) * 4) >> (8 * h);
+      v4i b[2], a[MI][2];
+      int xa[MI];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) b[s] = *reinterpret_cast<const v4i*>(slot + BM * kLine + swz(bcol, 4 * u + 2 * s + h));
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int r = 32 * i + r32;
+        xa[i] = *reinterpret_cast<const int*>(sc + r / (8 * MI) * 256 + (2 * (r % (8 * MI)) + u) * 4) >> (8 * h);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) a[i][s] = *reinterpret_cast<const v4i*>(slot + swz(r, 4 * u + 2 * s + h));
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) acc[i] = mfma_mxfp4_32<0>(b[0], a[i][0], acc[i], xb, xa[i]);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) acc[i] = mfma_mxfp4_32<2>(b[1], a[i][1], acc[i], xb, xa[i]);
+    }
+    cur = cur == R - 1 ? 0 : cur + 1;
+    ahead = ahead == R - 1 ? 0 : ahead + 1;
+  }
+
+  // a lane holds row 32 i + r32, columns 8q + 4h + 0..3 of its wave's 32
+  constexpr int COLS = SWIGLU ? 64 : 128;
+  static_assert(BM * kOutRow<COLS> <= R * kSlot, "the results fit the ring");
+  wait_vmem_lds<0>();
+  barrier_only();                                   // every wave has read the last pair
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const v16f& c = acc[i];
+    uint8_t* const o = smem + (32 * i + r32) * kOutRow<COLS>;
+    if (SWIGLU) {
+      v2i v[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        v[q] = pack4(silu_mul(c[4 * q], c[4 * q + 8]), silu_mul(c[4 * q + 1], c[4 * q + 9]),
+                     silu_mul(c[4 * q + 2], c[4 * q + 10]), silu_mul(c[4 * q + 3], c[4 * q + 11]));
+      put16(o + 32 * wave, h, v[0], v[1]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const v2i p = {(int)pack_bf16x2(y[j][0], y[j][1]), (int)pack_bf16x2(y[j][2], y[j][3])};
-        *reinterpret_cast<v2i*>(out + (size_t)(row0 + m) * N + nt * 32 + 16 * j + 4 * q) = p;
-      }
+      for (int q = 0; q < 4; q += 2)
+        put16(o + 64 * wave + 16 * q, h, pack4(c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]),
+              pack4(c[4 * q + 4], c[4 * q + 5], c[4 * q + 6], c[4 * q + 7]));
     }
   }
+  __syncthreads();
+  const size_t ld = SWIGLU ? half : N;
+  store_rows<COLS>(smem, out + row0 * ld + nt * COLS, ld, rows, COLS);
 }
 
 // ---------------------------------------------------------------- large tiles
@@ -203,20 +285,12 @@ __global__ __launch_bounds__(64 * kWaves) void gmm_mxfp4_split_kernel(
 // next stage's operands are read into the other, and the copies of the pair two
 // ahead go to the slot that was just read.  Scale words (four blocks of 32 k)
 // arrive two pairs at a time.
-constexpr int BM = 256, BN = 256, BK = 128;         // BK in bytes: the 256 k of a pair
-constexpr int kSlotBytes = (BM + BN) * BK;
+constexpr int BM = 256, BN = 256;
+constexpr int kSlotBytes = (BM + BN) * kLine;
 constexpr int kRingBytes = 2 * kSlotBytes;
 constexpr int kScaleSlot = BM * 16 + 4 * BN * 4;    // four stages' scale words, rows then columns
 constexpr int kTileLds = kRingBytes + 2 * kScaleSlot;
 static_assert(kTileLds <= 160 * 1024, "ring and scales fit the LDS");
-
-__device__ __forceinline__ int swz(int row, int chunk) { return row * BK + ((chunk ^ ((row >> 1) & 7)) << 4); }
-
-template <int SEL>
-__device__ __forceinline__ v16f mfma_mxfp4_32(const v4i& a, const v4i& b, const v16f& c, int sa, int sb) {
-  const v8i a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, SEL, sa, SEL, sb);
-}
 
 template <bool SWIGLU>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(1, 1)))
@@ -278,8 +352,8 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
     vsb = ((uint32_t)wave * (uint32_t)N + (uint32_t)column(4 * lane)) * 4u;
     auto copy = [&](int p, int u, int q) __attribute__((always_inline)) {    // copy q of pair p into slot u
       uint8_t* const s = smem + u * kSlotBytes;
-      if (q < 2 * MI) dma16(ra, s + (2 * MI * wave + q) * 1024, va[q], (uint32_t)p * BK);
-      else dma16(rb, s + BM * BK + (8 * wave + q - 2 * MI) * 1024, vb[q - 2 * MI], (uint32_t)p * BK);
+      if (q < 2 * MI) dma16(ra, s + (2 * MI * wave + q) * 1024, va[q], (uint32_t)p * kLine);
+      else dma16(rb, s + BM * kLine + (8 * wave + q - 2 * MI) * 1024, vb[q - 2 * MI], (uint32_t)p * kLine);
     };
     auto copy_scales = [&](int ks) __attribute__((always_inline)) {          // of stages ks .. ks + 3, ks a multiple of 4
       uint8_t* const s = smem + kRingBytes + ((ks >> 2) & 1) * kScaleSlot;
@@ -304,7 +378,7 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
       const uint8_t* sc = smem + kRingBytes + ((ks >> 2) & 1) * kScaleSlot;
       const int f = q / 3, s = q % 3;               // fragment, then its two halves and its scales
       if (f < 4) {
-        if (s < 2) b[S][f][s] = *reinterpret_cast<const v4i*>(slot + BM * BK + swz(bcol[f], 4 * S + 2 * s + h));
+        if (s < 2) b[S][f][s] = *reinterpret_cast<const v4i*>(slot + BM * kLine + swz(bcol[f], 4 * S + 2 * s + h));
         else sb[S][f] = *reinterpret_cast<const int*>(sc + BM * 16 + (u * BN + bcol[f]) * 4);
       } else {
         if (s < 2) a[S][f - 4][s] = *reinterpret_cast<const v4i*>(slot + swz(arow[f - 4], 4 * S + 2 * s + h));
@@ -396,20 +470,13 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
       if (ks + 3 < nk) step(ks + 3, U3{}, std::false_type{});
     }
 
-    // ---- epilogue: a lane holds row arow[i], columns 8q + 4h + 0..3 of each fragment.  Lanes l and
-    // l + 32 hold the same row and trade 8-byte groups, so that every store is 16 bytes.
-    auto store_frag = [&](uint16_t* rowp, const v2i* pq) __attribute__((always_inline)) {
-#pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        const auto x = __builtin_amdgcn_permlane32_swap(pq[q][0], pq[q + 1][0], false, false);
-        const auto y = __builtin_amdgcn_permlane32_swap(pq[q][1], pq[q + 1][1], false, false);
-        *reinterpret_cast<v4i*>(rowp + 8 * q + 8 * h) = (v4i){(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
-      }
-    };
+    // ---- epilogue: a lane holds row arow[i], columns 8q + 4h + 0..3 of each fragment
+    constexpr int COLS = SWIGLU ? BN / 2 : BN;
+    static_assert(BM * kOutRow<COLS> <= kTileLds, "the results fit the LDS");
+    wait_vmem_lds<0>();
+    barrier_only();                                 // every wave has read the last stage
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      if (arow[i] >= rows) continue;
-      const size_t row = (size_t)row0 + arow[i];
 #pragma unroll
       for (int j = 0; j < (SWIGLU ? 2 : 4); ++j) {
         v2i pq[4];
@@ -419,15 +486,18 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float y = acc[i][j][4 * q + e];
-            // hardware reciprocal: the product is rounded to bf16 right after
-            v[e] = SWIGLU ? y * __builtin_amdgcn_rcpf(1.0f + __expf(-y)) * acc[i][(j + 2) & 3][4 * q + e] : y;
+            v[e] = SWIGLU ? silu_mul(y, acc[i][(j + 2) & 3][4 * q + e]) : y;
           }
-          pq[q] = (v2i){(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
+          pq[q] = pack4(v[0], v[1], v[2], v[3]);
         }
-        if (SWIGLU) store_frag(out + row * half + nt * (BN / 2) + wn * 64 + 32 * j, pq);
-        else if (nt * BN + wn * 128 + 32 * j < N) store_frag(out + row * N + nt * BN + wn * 128 + 32 * j, pq);
+        uint8_t* const o = smem + arow[i] * kOutRow<COLS> + COLS * wn + 64 * j;
+        put16(o, h, pq[0], pq[1]);
+        put16(o + 32, h, pq[2], pq[3]);
       }
     }
+    __syncthreads();
+    const size_t ld = SWIGLU ? half : N;
+    store_rows<COLS>(smem, out + row0 * ld + nt * COLS, ld, rows, SWIGLU ? COLS : min(COLS, N - nt * BN));
   };
   if (rows > 192) run(std::integral_constant<int, 4>{});
   else if (rows > 128) run(std::integral_constant<int, 3>{});
@@ -437,31 +507,43 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
 
 }  // namespace
 
+template <int MI>
+static hipError_t launch_stream(const uint8_t* aq, const uint8_t* ascale, const uint8_t* codes, const uint8_t* wscale,
+                                const int* group_sizes, const int* slot_of_row, int topk, int T, int G, int M, int K,
+                                int N, bool swiglu, uint16_t* out, int* status, hipStream_t stream) {
+  const long long tiles = std::min<long long>(M, ((long long)M + 32 * MI - 1) / (32 * MI) + G);
+  const dim3 grid((unsigned)(tiles * (N / 128)));
+  const size_t lds = kRing<MI> * ((32 * MI + 128) * kLine + 2048);
+  if (swiglu)
+    hipLaunchKernelGGL((gmm_mxfp4_stream_kernel<MI, true>), grid, dim3(256), lds, stream, aq, ascale, codes, wscale,
+                       group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
+  else
+    hipLaunchKernelGGL((gmm_mxfp4_stream_kernel<MI, false>), grid, dim3(256), lds, stream, aq, ascale, codes, wscale,
+                       group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
+  return hipGetLastError();
+}
+
 hipError_t launch_gmm_mxfp4(const uint8_t* aq, const uint8_t* ascale, const uint8_t* codes, const uint8_t* wscale,
                             const int* group_sizes, const int* slot_of_row, int topk, int T, int G, int M, int K,
                             int N, bool swiglu, uint16_t* out, int* status, hipStream_t stream) {
-  const uint32_t* as = reinterpret_cast<const uint32_t*>(ascale);
-  const uint32_t* bs = reinterpret_cast<const uint32_t*>(wscale);
-  if ((long long)(T + 1) * (K / 2) < (1LL << 32) && M >= 64 * G) {
-    const long long tiles = std::min<long long>(M, ((long long)M + BM - 1) / BM + G);
-    if (swiglu)
-      hipLaunchKernelGGL(gmm_mxfp4_tile_kernel<true>, dim3((unsigned)(tiles * (N / 256))), dim3(256), kTileLds, stream, aq,
-                         ascale, codes, wscale, group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
-    else
-      hipLaunchKernelGGL(gmm_mxfp4_tile_kernel<false>, dim3((unsigned)(tiles * ((N + 255) / 256))), dim3(256), kTileLds,
-                         stream, aq, ascale, codes, wscale, group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
-    return hipGetLastError();
-  }
-  constexpr int MA = 4;
-  const long long tiles = std::min<long long>(M, ((long long)M + 16 * MA - 1) / (16 * MA) + G);
-  const dim3 grid((unsigned)(tiles * (N / 32)));
-  const size_t lds = sizeof(float) * 4 * kWaves * MA * 2 * 64;
+  // 32 experts, 7168 x 4096, SwiGLU: at 4 rows an expert 70 us with MI = 1 and 74 with 2, at 16 rows 86 and 83, at 64
+  // rows 146 with MI = 2 and 133 with the large tiles.  A contraction of three pairs is over before a large tile's
+  // loads and stores overlap anything: 8190 x 768 x 2048 takes 33 us with MI = 4 (two blocks a CU) and 35 with the
+  // large tiles, 8190 x 1024 x 2048 37 with either.  The large tiles have 32-bit offsets to the rows.
+#define STREAM(MI)                                                                                                  \
+  launch_stream<MI>(aq, ascale, codes, wscale, group_sizes, slot_of_row, topk, T, G, M, K, N, swiglu, out, status, \
+                    stream)
+  if (M <= 8 * (long long)G) return STREAM(1);
+  if (M < 64 * (long long)G) return STREAM(2);
+  if (K < 1024 || (long long)(T + 1) * (K / 2) >= (1LL << 32)) return STREAM(4);
+#undef STREAM
+  const long long tiles = std::min<long long>(M, ((long long)M + BM - 1) / BM + G);
   if (swiglu)
-    hipLaunchKernelGGL((gmm_mxfp4_split_kernel<MA, true>), grid, dim3(64 * kWaves), lds, stream, aq, as, codes, bs,
-                       group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
+    hipLaunchKernelGGL(gmm_mxfp4_tile_kernel<true>, dim3((unsigned)(tiles * (N / 256))), dim3(256), kTileLds, stream, aq,
+                       ascale, codes, wscale, group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
   else
-    hipLaunchKernelGGL((gmm_mxfp4_split_kernel<MA, false>), grid, dim3(64 * kWaves), lds, stream, aq, as, codes, bs,
-                       group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
+    hipLaunchKernelGGL(gmm_mxfp4_tile_kernel<false>, dim3((unsigned)(tiles * ((N + 255) / 256))), dim3(256), kTileLds,
+                       stream, aq, ascale, codes, wscale, group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
   return hipGetLastError();
 }
 

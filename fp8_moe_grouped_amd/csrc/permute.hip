@@ -20,12 +20,6 @@
 namespace fp8gmm {
 namespace {
 
-__device__ __forceinline__ float wave_fsum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-
 // One wave per (token, piece of 64 chunks).
 __global__ __launch_bounds__(256) void permute_kernel(const v4i* __restrict__ x, const int* __restrict__ row_of_slot,
                                                       int T, int k, int R, int nch, int pieces,
@@ -38,7 +32,7 @@ __global__ __launch_bounds__(256) void permute_kernel(const v4i* __restrict__ x,
   const v4i v = x[(size_t)t * nch + c];
   for (int j = 0; j < k; ++j) {
     const int row = row_of_slot[(size_t)t * k + j];
-    if ((unsigned)row < (unsigned)R) out[(size_t)row * nch + c] = v;
+    if ((unsigned)row < (unsigned)R) __builtin_nontemporal_store(v, out + (size_t)row * nch + c);
   }
 }
 
@@ -88,7 +82,7 @@ __global__ __launch_bounds__(256) void permute_fp8_kernel(const uint16_t* __rest
     v2i* dst = reinterpret_cast<v2i*>(codes + (size_t)row * H);
 #pragma unroll
     for (int c = 0; c < CPL; ++c)
-      if (lane + 64 * c < nch) dst[lane + 64 * c] = q[c];
+      if (lane + 64 * c < nch) __builtin_nontemporal_store(q[c], dst + lane + 64 * c);
     if (lane == 0) scales[row] = s;
   }
 }
@@ -104,18 +98,27 @@ __global__ __launch_bounds__(256) void combine_kernel(const v4i* __restrict__ y,
   const int c = (int)(unit % pieces) * 64 + (threadIdx.x & 63);
   if (c >= nch) return;
   float a[8] = {};
-#pragma unroll 4
-  for (int j = 0; j < k; ++j) {
-    const int row = row_of_slot[(size_t)t * k + j];
-    if ((unsigned)row >= (unsigned)R) continue;
-    const float w = WEIGHTED ? weights[(size_t)t * k + j] : 1.f;
-    const v4i v = y[(size_t)row * nch + c];
+  for (int j0 = 0; j0 < k; j0 += 8) {               // eight rows' loads in flight
+    v4i v[8];
+    float w[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float lo = bf16_lo((uint32_t)v[e]), hi = bf16_hi((uint32_t)v[e]);
-      a[2 * e] = WEIGHTED ? __builtin_fmaf(w, lo, a[2 * e]) : a[2 * e] + lo;
-      a[2 * e + 1] = WEIGHTED ? __builtin_fmaf(w, hi, a[2 * e + 1]) : a[2 * e + 1] + hi;
+    for (int u = 0; u < 8; ++u) {
+      const int row = j0 + u < k ? row_of_slot[(size_t)t * k + j0 + u] : -1;
+      v[u] = (v4i){0, 0, 0, 0};
+      w[u] = 0.f;
+      if ((unsigned)row < (unsigned)R) {
+        v[u] = __builtin_nontemporal_load(y + (size_t)row * nch + c);
+        w[u] = WEIGHTED ? weights[(size_t)t * k + j0 + u] : 1.f;
+      }
     }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float lo = bf16_lo((uint32_t)v[u][e]), hi = bf16_hi((uint32_t)v[u][e]);
+        a[2 * e] = WEIGHTED ? __builtin_fmaf(w[u], lo, a[2 * e]) : a[2 * e] + lo;
+        a[2 * e + 1] = WEIGHTED ? __builtin_fmaf(w[u], hi, a[2 * e + 1]) : a[2 * e + 1] + hi;
+      }
   }
   v4i o;
 #pragma unroll
@@ -123,37 +126,55 @@ __global__ __launch_bounds__(256) void combine_kernel(const v4i* __restrict__ y,
   out[(size_t)t * nch + c] = o;
 }
 
-// One wave per slot: dot product of the whole row in f32, lanes then joined.
+// One block per token, eight of its rows at a time: dout is read once for them, the
+// waves share the width and join their dot products in a fixed order.
 __global__ __launch_bounds__(256) void combine_bwd_kernel(const v4i* __restrict__ dout, const v4i* __restrict__ y,
                                                           const int* __restrict__ row_of_slot,
-                                                          const float* __restrict__ weights, int slots, int k, int R,
-                                                          int nch, v4i* __restrict__ dy, float* __restrict__ dweights) {
-  const int lane = threadIdx.x & 63;
-  const int s = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (s >= slots) return;
-  const int row = row_of_slot[s];
-  float dot = 0.f;
-  if ((unsigned)row < (unsigned)R) {
-    const float w = weights[s];
-    const v4i* d = dout + (size_t)(s / k) * nch;
-    const v4i* yr = y + (size_t)row * nch;
-    v4i* o = dy + (size_t)row * nch;
-#pragma unroll 2
-    for (int c = lane; c < nch; c += 64) {
-      const v4i g = d[c], v = yr[c];
-      v4i r;
+                                                          const float* __restrict__ weights, int k, int R, int nch,
+                                                          v4i* __restrict__ dy, float* __restrict__ dweights) {
+  __shared__ float part[2][4][8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, t = blockIdx.x;
+  const v4i* const d = dout + (size_t)t * nch;
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    int row[8];
+    float w[8], dot[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float g0 = bf16_lo((uint32_t)g[e]), g1 = bf16_hi((uint32_t)g[e]);
-        dot = __builtin_fmaf(g0, bf16_lo((uint32_t)v[e]), dot);
-        dot = __builtin_fmaf(g1, bf16_hi((uint32_t)v[e]), dot);
-        r[e] = (int)pack_bf16x2(w * g0, w * g1);
-      }
-      o[c] = r;
+    for (int u = 0; u < 8; ++u) {
+      row[u] = j0 + u < k ? row_of_slot[(size_t)t * k + j0 + u] : -1;
+      w[u] = j0 + u < k ? weights[(size_t)t * k + j0 + u] : 0.f;
+      dot[u] = 0.f;
     }
-    dot = wave_fsum(dot);
+    for (int c = tid; c < nch; c += 256) {
+      const v4i g = d[c];
+      v4i v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        v[u] = (v4i){0, 0, 0, 0};
+        if ((unsigned)row[u] < (unsigned)R) v[u] = __builtin_nontemporal_load(y + (size_t)row[u] * nch + c);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if ((unsigned)row[u] >= (unsigned)R) continue;
+        v4i r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float g0 = bf16_lo((uint32_t)g[e]), g1 = bf16_hi((uint32_t)g[e]);
+          dot[u] = __builtin_fmaf(g0, bf16_lo((uint32_t)v[u][e]), dot[u]);
+          dot[u] = __builtin_fmaf(g1, bf16_hi((uint32_t)v[u][e]), dot[u]);
+          r[e] = (int)pack_bf16x2(w[u] * g0, w[u] * g1);
+        }
+        __builtin_nontemporal_store(r, dy + (size_t)row[u] * nch + c);
+      }
+    }
+    float(&p)[4][8] = part[(j0 >> 3) & 1];          // the other half may still be read
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float sum = reduce<64>(dot[u], [](float a, float b) { return a + b; });
+      if (lane == u) p[wave][u] = sum;
+    }
+    __syncthreads();
+    if (tid < 8 && j0 + tid < k) dweights[(size_t)t * k + j0 + tid] = (p[0][tid] + p[1][tid]) + (p[2][tid] + p[3][tid]);
   }
-  if (lane == 0) dweights[s] = dot;
 }
 
 unsigned blocks_of(long long units) { return (unsigned)((units + 3) / 4); }
@@ -202,10 +223,9 @@ hipError_t launch_combine(const uint16_t* y, const int* row_of_slot, const float
 
 hipError_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y, const int* row_of_slot, const float* weights,
                               int T, int k, int R, int H, uint16_t* dy, float* dweights, hipStream_t stream) {
-  const int slots = T * k;
-  hipLaunchKernelGGL(combine_bwd_kernel, dim3(blocks_of(slots)), dim3(256), 0, stream,
-                     reinterpret_cast<const v4i*>(dout), reinterpret_cast<const v4i*>(y), row_of_slot, weights, slots,
-                     k, R, H / 8, reinterpret_cast<v4i*>(dy), dweights);
+  hipLaunchKernelGGL(combine_bwd_kernel, dim3(T), dim3(256), 0, stream, reinterpret_cast<const v4i*>(dout),
+                     reinterpret_cast<const v4i*>(y), row_of_slot, weights, k, R, H / 8, reinterpret_cast<v4i*>(dy),
+                     dweights);
   return hipGetLastError();
 }
 

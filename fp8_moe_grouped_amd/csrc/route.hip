@@ -42,63 +42,6 @@ constexpr int kTokensPerWave = 4;
 constexpr int kTokensPerBlock = kWaves * kTokensPerWave;   // per chunk
 constexpr int kMaxBlocks = 512;                     // longer batches give a block several chunks
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_row(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
-}
-template <int CTRL>
-__device__ __forceinline__ float dpp_row(float v) {
-  return __uint_as_float(dpp_row<CTRL>(__float_as_uint(v)));
-}
-template <int CTRL>
-__device__ __forceinline__ double dpp_row(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, (uint64_t)dpp_row<CTRL>((uint32_t)u) | (uint64_t)dpp_row<CTRL>((uint32_t)(u >> 32)) << 32);
-}
-// v of the lane whose row index differs in bit 0 (B = 16) or bit 1 (B = 32): exchanges rows or halves.
-template <int B>
-__device__ __forceinline__ uint32_t other_rows(uint32_t v, bool upper) {
-  if (B == 16) {
-    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    return upper ? r[0] : r[1];
-  }
-  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return upper ? r[0] : r[1];
-}
-template <int B>
-__device__ __forceinline__ float other_rows(float v, bool upper) {
-  return __uint_as_float(other_rows<B>(__float_as_uint(v), upper));
-}
-template <int B>
-__device__ __forceinline__ double other_rows(double v, bool upper) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, (uint64_t)other_rows<B>((uint32_t)u, upper) |
-                                        (uint64_t)other_rows<B>((uint32_t)(u >> 32), upper) << 32);
-}
-
-// Reduction over the L lanes that share a token, to all of them (rotations within a row, then across rows).
-// Every lane joins the same pairs, so all hold the same sum.
-template <int L, typename T, typename F>
-__device__ __forceinline__ T reduce(T v, F f) {
-  v = f(v, dpp_row<0x128>(v));
-  v = f(v, dpp_row<0x124>(v));
-  v = f(v, dpp_row<0x122>(v));
-  v = f(v, dpp_row<0x121>(v));
-  if (L == 64) {
-    v = f(v, other_rows<16>(v, (threadIdx.x & 16) != 0));
-    v = f(v, other_rows<32>(v, (threadIdx.x & 32) != 0));
-  }
-  return v;
-}
-template <int L>
-__device__ __forceinline__ float lanes_sum(float v) {
-  return reduce<L>(v, [](float a, float b) { return a + b; });
-}
-template <int L>
-__device__ __forceinline__ float lanes_max(float v) {
-  return reduce<L>(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
-}
-
 // The wave's lanes see each other's LDS writes past this point: LDS serves a wave in order, and
 // the compiler may neither move nor forward accesses across it.
 __device__ __forceinline__ void wave_lds_order() {
