@@ -173,6 +173,18 @@ def _call(name, *args):
         raise Fp8GmmError(name, st)
 
 
+def _launch(dev, name, *args):
+    """Calls entry point `name` on dev's current stream (its last argument)."""
+    fn = getattr(_lib or lib(), name)
+    if torch._C._cuda_getDevice() == dev.index:
+        st = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(dev))
+    if st != OK:
+        raise Fp8GmmError(name, st)
+
+
 def _workspace(op, M, K, N, G, dev, tile_m=512, workspace=None):
     need = workspace_bytes(op, M, K, N, G, tile_m)
     if workspace is None:
@@ -634,9 +646,8 @@ def moe_route(logits, k, *, renormalize=True, workspace=None):
     weights, slot_of_row = weights.view(torch.float32), slot_of_row.view(-1)
     group_sizes = torch.empty((E,), dtype=torch.int32, device=dev)
     ws, need = _workspace(OP_ROUTE, T, E, k, 1, dev, tile_m=0, workspace=workspace)
-    with _on(dev):
-        _call("moe_route", _ptr(logits), LOGIT_DTYPES[logits.dtype], T, E, k, bool(renormalize), _ptr(ids),
-              _ptr(weights), _ptr(group_sizes), _ptr(row_of_slot), _ptr(slot_of_row), _ptr(ws), need, _stream(dev))
+    _launch(dev, "moe_route", _ptr(logits), LOGIT_DTYPES[logits.dtype], T, E, k, bool(renormalize), _ptr(ids),
+            _ptr(weights), _ptr(group_sizes), _ptr(row_of_slot), _ptr(slot_of_row), _ptr(ws), need)
     return MoeRouting(ids, weights, group_sizes, row_of_slot, slot_of_row)
 
 
@@ -647,14 +658,14 @@ def moe_route_bwd(dweights, logits, ids, weights, *, renormalize=True, out=None)
     T, E = logits.shape
     _req_slots(ids, "ids", torch.int32)
     k = ids.shape[1]
-    _req_slots(ids, "ids", torch.int32, T, k)
+    if ids.shape[0] != T:
+        raise ValueError(f"ids must be [{T}, k], got {tuple(ids.shape)}")
     _req_slots(weights, "weights", torch.float32, T, k)
     _req_slots(dweights, "dweights", torch.float32, T, k)
     dev = _same_device(dweights, logits, ids, weights)
     out = _out(out, (T, E), logits.dtype, dev, "out")
-    with _on(dev):
-        _call("moe_route_bwd", _ptr(dweights), _ptr(logits), LOGIT_DTYPES[logits.dtype], _ptr(ids), _ptr(weights), T,
-              E, k, bool(renormalize), _ptr(out), _stream(dev))
+    _launch(dev, "moe_route_bwd", _ptr(dweights), _ptr(logits), LOGIT_DTYPES[logits.dtype], _ptr(ids), _ptr(weights), T,
+            E, k, bool(renormalize), _ptr(out))
     return out
 
 
@@ -676,8 +687,7 @@ def moe_permute(x, row_of_slot, *, out=None):
     _req(out, "out", torch.bfloat16, 2)
     if out.shape[1] != H or out.device != dev:
         raise ValueError(f"out must be [R, {H}] on {dev}, got {tuple(out.shape)} on {out.device}")
-    with _on(dev):
-        _call("moe_permute", _ptr(x), _ptr(row_of_slot), T, k, out.shape[0], H, _ptr(out), _stream(dev))
+    _launch(dev, "moe_permute", _ptr(x), _ptr(row_of_slot), T, k, out.shape[0], H, _ptr(out))
     return out
 
 
@@ -690,8 +700,7 @@ def moe_permute_fp8(x, row_of_slot, *, codes=None, scales=None):
     codes = _out(codes, (R, H), torch.uint8, dev, "codes")
     scales = _out(scales, (R,), torch.float32, dev, "scales")
     _same_device(x, codes, scales)
-    with _on(dev):
-        _call("moe_permute_fp8", _ptr(x), _ptr(row_of_slot), T, k, R, H, _ptr(codes), _ptr(scales), _stream(dev))
+    _launch(dev, "moe_permute_fp8", _ptr(x), _ptr(row_of_slot), T, k, R, H, _ptr(codes), _ptr(scales))
     return codes, scales
 
 
@@ -703,8 +712,7 @@ def moe_combine(y, row_of_slot, weights=None, *, out=None):
         _req_slots(weights, "weights", torch.float32, T, k)
     out = _out(out, (T, H), torch.bfloat16, dev, "out")
     _same_device(y, weights, out)
-    with _on(dev):
-        _call("moe_combine", _ptr(y), _ptr(row_of_slot), _ptr(weights), T, k, y.shape[0], H, _ptr(out), _stream(dev))
+    _launch(dev, "moe_combine", _ptr(y), _ptr(row_of_slot), _ptr(weights), T, k, y.shape[0], H, _ptr(out))
     return out
 
 
@@ -719,9 +727,8 @@ def moe_combine_bwd(dout, y, row_of_slot, weights, *, dy=None, dweights=None):
     dy = _out(dy, tuple(y.shape), torch.bfloat16, dev, "dy")
     dweights = _out(dweights, (T, k), torch.float32, dev, "dweights")
     _same_device(dout, y, weights, dy, dweights)
-    with _on(dev):
-        _call("moe_combine_bwd", _ptr(dout), _ptr(y), _ptr(row_of_slot), _ptr(weights), T, k, y.shape[0], H, _ptr(dy),
-              _ptr(dweights), _stream(dev))
+    _launch(dev, "moe_combine_bwd", _ptr(dout), _ptr(y), _ptr(row_of_slot), _ptr(weights), T, k, y.shape[0], H, _ptr(dy),
+            _ptr(dweights))
     return dy, dweights
 
 
@@ -736,8 +743,7 @@ def quantize_mxfp4_weights(w, *, codes=None, scales=None):
     codes = _out(codes, (G, N, K // 2), torch.uint8, dev, "codes")
     scales = _out(scales, (G, K // 128, N, 4), torch.uint8, dev, "scales")
     _same_device(w, codes, scales)
-    with _on(dev):
-        _call("quantize_mxfp4_weights", _ptr(w), K, N, G, _ptr(codes), _ptr(scales), _stream(dev))
+    _launch(dev, "quantize_mxfp4_weights", _ptr(w), K, N, G, _ptr(codes), _ptr(scales))
     return codes, scales
 
 
@@ -759,8 +765,7 @@ def dequantize_mxfp4(codes, scales, *, out=None):
     dev = _same_device(codes, scales)
     out = _out(out, (G, N, K), torch.bfloat16, dev, "out")
     _same_device(codes, out)
-    with _on(dev):
-        _call("dequantize_mxfp4", _ptr(codes), _ptr(scales), K, N, G, _ptr(out), _stream(dev))
+    _launch(dev, "dequantize_mxfp4", _ptr(codes), _ptr(scales), K, N, G, _ptr(out))
     return out
 
 
@@ -780,9 +785,8 @@ def _mxfp4_product(name, x, codes, scales, group_sizes, slot_of_row, topk, out, 
     out = _out(out, (M, N // 2 if swiglu else N), torch.bfloat16, dev, "out")
     _same_device(x, out)
     ws, need = _workspace(OP_MXFP4, T, K, N, G, dev, tile_m=0, workspace=workspace)
-    with _on(dev):
-        _call(name, _ptr(x), _ptr(codes), _ptr(scales), _ptr(group_sizes), _ptr(slot_of_row), int(topk), T, M, K, N, G,
-              _ptr(out), _ptr(ws), need, _ptr(dev_status), _stream(dev))
+    _launch(dev, name, _ptr(x), _ptr(codes), _ptr(scales), _ptr(group_sizes), _ptr(slot_of_row), int(topk), T, M, K, N, G,
+            _ptr(out), _ptr(ws), need, _ptr(dev_status))
     return out
 
 

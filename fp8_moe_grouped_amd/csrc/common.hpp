@@ -228,6 +228,17 @@ __device__ __forceinline__ void prio_by_progress(int p) {
 // sequence; consecutive calls with the same id interleave the classes.
 #define SCHED_GROUP(mask, n) __builtin_amdgcn_sched_group_barrier((mask), (n), 0)
 
+// ----------------------------------------------------------------- long grids
+
+// A launch dimension holds fewer than 2^32 threads: longer grids of 256-thread blocks continue in y.  Blocks past
+// the last one exist, so a kernel checks its index.
+inline dim3 linear_grid(long long blocks) {
+  constexpr long long kWide = 1 << 23;
+  if (blocks <= kWide) return dim3((unsigned)blocks);
+  return dim3((unsigned)kWide, (unsigned)((blocks + kWide - 1) / kWide));
+}
+__device__ __forceinline__ long long linear_block() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // ----------------------------------------------------------------- reductions
 
 template <int CTRL>

@@ -48,7 +48,7 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
 __global__ __launch_bounds__(256) void quant_rows_mxfp4_kernel(const v4i* __restrict__ x, int T, int nch,
                                                               uint32_t* __restrict__ codes,
                                                               uint8_t* __restrict__ scales) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long i = linear_block() * 256 + threadIdx.x;
   const long long end = (long long)T * nch;
   if (i >= end + nch) return;
   const v4i v = i < end ? x[i] : (v4i){0, 0, 0, 0};
@@ -157,7 +157,7 @@ hipError_t launch_quant_rows_mxfp4(const uint16_t* x, int T, int K, uint8_t* cod
                                    hipStream_t stream) {
   const int nch = K / 8;
   const long long blocks = (((long long)T + 1) * nch + 255) / 256;
-  hipLaunchKernelGGL(quant_rows_mxfp4_kernel, dim3((unsigned)blocks), dim3(256), 0, stream,
+  hipLaunchKernelGGL(quant_rows_mxfp4_kernel, linear_grid(blocks), dim3(256), 0, stream,
                      reinterpret_cast<const v4i*>(x), T, nch, reinterpret_cast<uint32_t*>(codes), scales);
   return hipGetLastError();
 }

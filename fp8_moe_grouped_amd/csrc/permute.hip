@@ -24,7 +24,7 @@ namespace {
 __global__ __launch_bounds__(256) void permute_kernel(const v4i* __restrict__ x, const int* __restrict__ row_of_slot,
                                                       int T, int k, int R, int nch, int pieces,
                                                       v4i* __restrict__ out) {
-  const long long unit = (long long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const long long unit = linear_block() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = (int)(unit / pieces);
   if (t >= T) return;
   const int c = (int)(unit % pieces) * 64 + (threadIdx.x & 63);
@@ -92,7 +92,7 @@ template <bool WEIGHTED>
 __global__ __launch_bounds__(256) void combine_kernel(const v4i* __restrict__ y, const int* __restrict__ row_of_slot,
                                                       const float* __restrict__ weights, int T, int k, int R, int nch,
                                                       int pieces, v4i* __restrict__ out) {
-  const long long unit = (long long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const long long unit = linear_block() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = (int)(unit / pieces);
   if (t >= T) return;
   const int c = (int)(unit % pieces) * 64 + (threadIdx.x & 63);
@@ -177,14 +177,14 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const v4i* __restrict_
   }
 }
 
-unsigned blocks_of(long long units) { return (unsigned)((units + 3) / 4); }
+long long blocks_of(long long units) { return (units + 3) / 4; }
 
 }  // namespace
 
 hipError_t launch_permute(const uint16_t* x, const int* row_of_slot, int T, int k, int R, int H, uint16_t* out,
                           hipStream_t stream) {
   const int nch = H / 8, pieces = (nch + 63) / 64;
-  hipLaunchKernelGGL(permute_kernel, dim3(blocks_of((long long)T * pieces)), dim3(256), 0, stream,
+  hipLaunchKernelGGL(permute_kernel, linear_grid(blocks_of((long long)T * pieces)), dim3(256), 0, stream,
                      reinterpret_cast<const v4i*>(x), row_of_slot, T, k, R, nch, pieces, reinterpret_cast<v4i*>(out));
   return hipGetLastError();
 }
@@ -193,7 +193,7 @@ hipError_t launch_permute_fp8(const uint16_t* x, const int* row_of_slot, int T, 
                               float* scales, hipStream_t stream) {
   const int cpl = (H / 8 + 63) / 64;
 #define PLAUNCH(C)                                                                                               \
-  hipLaunchKernelGGL(permute_fp8_kernel<C>, dim3(blocks_of(T)), dim3(256), 0, stream, x, row_of_slot, T, k, R, H, \
+  hipLaunchKernelGGL(permute_fp8_kernel<C>, dim3((unsigned)blocks_of(T)), dim3(256), 0, stream, x, row_of_slot, T, k, R, H, \
                      codes, scales)
   if (cpl <= 1) PLAUNCH(1);
   else if (cpl <= 2) PLAUNCH(2);
@@ -209,7 +209,7 @@ hipError_t launch_permute_fp8(const uint16_t* x, const int* row_of_slot, int T, 
 hipError_t launch_combine(const uint16_t* y, const int* row_of_slot, const float* weights, int T, int k, int R, int H,
                           uint16_t* out, hipStream_t stream) {
   const int nch = H / 8, pieces = (nch + 63) / 64;
-  const dim3 grid(blocks_of((long long)T * pieces));
+  const dim3 grid = linear_grid(blocks_of((long long)T * pieces));
   const v4i* yv = reinterpret_cast<const v4i*>(y);
   v4i* ov = reinterpret_cast<v4i*>(out);
   if (weights)

@@ -167,3 +167,20 @@ def test_rows_past_four_gigabytes():
     dy = torch.zeros_like(y)
     G.moe_combine_bwd(x, y, rows, torch.ones((2, 2), device="cuda"), dy=dy)
     assert torch.equal(dy, y)
+
+
+def test_more_threads_than_a_launch_dimension():
+    """2^24 - 1 tokens in five pieces each: more than 2^32 threads.  All slots but a few are masked."""
+    import fp8_moe_grouped_amd as G
+    T, H, R = 2 ** 24 - 1, 2176, 8
+    rows = torch.full((T, 1), -1, dtype=torch.int32, device="cuda")
+    at = torch.tensor([0, 1, T // 2, 13_421_772, 13_421_773, T - 3, T - 2, T - 1], device="cuda")
+    rows[at, 0] = torch.arange(R, dtype=torch.int32, device="cuda")
+    small = torch.randn((R, H), device="cuda").to(torch.bfloat16)
+    big = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    big[at] = small
+    assert torch.equal(G.moe_permute(big, rows, out=torch.empty_like(small)), small)
+    big[at - 1] = 7.0
+    G.moe_combine(small, rows, out=big)
+    assert torch.equal(big[at], small)
+    assert not bool(big[T - 5:T - 3].any()) and not bool(big[2:100].any())
