@@ -173,15 +173,15 @@ __global__ __launch_bounds__(256, 2) void gmm_mxfp4_stream_kernel(
                                                (uint32_t)p * kLine, 0, kCpolStream);
     dma4(rsb, slot + (BM + BN) * kLine + 1024 + wave * 256, vsb, (uint32_t)p * (uint32_t)N * 8u);
   };
-  copy_weights(0, smem);
-
-  // a wave copies 8 * MI rows; rows past the tile's end repeat its last
+  // A wave brings 8 * MI rows; rows past the tile's end repeat its last.  Loads return in order, so the slots are
+  // asked for before the weights.
   const int row = row0 + min(8 * MI * wave + min(lane, 8 * MI - 1), rows - 1);
+  const int slot_in = slot_of_row ? slot_of_row[row] : row;
+  sched_fence();
+  copy_weights(0, smem);
+  sched_fence();
   int token = row;
-  if (slot_of_row) {
-    const int slot = slot_of_row[row];
-    token = slot < 0 ? T : min(slot / topk, T);     // row T of the quantized activations is zero
-  }
+  if (slot_of_row) token = slot_in < 0 ? T : min(slot_in / topk, T);   // row T of the quantized activations is zero
   const uint8_t* va[MI];
 #pragma unroll
   for (int j = 0; j < MI; ++j) {
@@ -207,11 +207,13 @@ __global__ __launch_bounds__(256, 2) void gmm_mxfp4_stream_kernel(
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
   int cur = 0, ahead = R - 1;                       // slots of pair p and of pair p + R - 1
-  for (int p = 0; p < np; ++p) {
-    if (R == 3 && p + 1 < np) wait_vmem_lds<kLoads>();   // pair p is there, pair p + 1 on its way
+  // LEFT: pairs after this one, 2 standing for more.
+  auto step = [&](int p, auto left_c) __attribute__((always_inline)) {
+    constexpr int LEFT = decltype(left_c)::value;
+    if (R == 3 && LEFT > 0) wait_vmem_lds<kLoads>();     // pair p is there, pair p + 1 on its way
     else wait_vmem_lds<0>();
     barrier_only();                                 // and every wave has read pair p - 1
-    if (p + R - 1 < np) {
+    if (LEFT > R - 2) {
       copy_weights(p + R - 1, smem + ahead * kSlot);
       copy_rows(p + R - 1, smem + ahead * kSlot);
     }
@@ -239,7 +241,11 @@ __global__ __launch_bounds__(256, 2) void gmm_mxfp4_stream_kernel(
     }
     cur = cur == R - 1 ? 0 : cur + 1;
     ahead = ahead == R - 1 ? 0 : ahead + 1;
-  }
+  };
+  int p = 0;
+  for (; p + 2 < np; ++p) step(p, std::integral_constant<int, 2>{});
+  if (p + 1 < np) step(p++, std::integral_constant<int, 1>{});
+  step(p, std::integral_constant<int, 0>{});
 
   // a lane holds row 32 i + r32, columns 8q + 4h + 0..3 of its wave's 32
   constexpr int COLS = SWIGLU ? 64 : 128;
@@ -323,11 +329,12 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
   const BufRsrc rsa = make_rsrc(ascale, (uint32_t)(T + 1) * sbytes);
   const BufRsrc rb = make_rsrc(codes + (size_t)g * N * abytes, (uint32_t)N * abytes);
   const BufRsrc rsb = make_rsrc(wscale + (size_t)g * kw * N * 4, (uint32_t)kw * (uint32_t)N * 4u);
-  auto token_of = [&](int r) {                      // rows past the tile's end repeat its last
+  auto slot_of = [&](int r) {                       // rows past the tile's end repeat its last
     const int row = row0 + min(r, rows - 1);
-    if (!slot_of_row) return row;
-    const int slot = slot_of_row[row];
-    return slot < 0 ? T : min(slot / topk, T);
+    return slot_of_row ? slot_of_row[row] : row;
+  };
+  auto token_of = [&](int slot) {
+    return !slot_of_row ? slot : slot < 0 ? T : min(slot / topk, T);
   };
   auto column = [&](int c) {                        // column of tile column c (past N: past the buffer's end)
     return SWIGLU ? (c < BN / 2 ? nt * (BN / 2) + c : half + nt * (BN / 2) + c - BN / 2) : nt * BN + c;
@@ -337,29 +344,36 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
     constexpr int MI = decltype(mi_c)::value;       // the tile has up to 64 * MI rows, a wave 32 * MI
     constexpr int kLoads = 2 * MI + 8;              // a wave's copies of a pair, without the scales
     uint32_t va[2 * MI], vb[8], vsa, vsb;
-    const int mine = token_of(16 * MI * wave + min(lane, 16 * MI - 1));      // a lane has a row's token
-#pragma unroll
-    for (int j = 0; j < 2 * MI; ++j) {
-      const int r = (2 * MI * wave + j) * 8 + (lane >> 3);
-      va[j] = (uint32_t)__shfl(mine, 8 * j + (lane >> 3)) * abytes + (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) << 4);
-    }
+    // Loads return in order: the slots are asked for first, and the first columns copied while they come.
+    const int slot_copy = slot_of(16 * MI * wave + min(lane, 16 * MI - 1)), slot_scale = slot_of(64 * wave + lane);
+    sched_fence();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = (8 * wave + j) * 8 + (lane >> 3);
       vb[j] = (uint32_t)column(c) * abytes + (uint32_t)(((lane & 7) ^ ((c >> 1) & 7)) << 4);
     }
-    vsa = (uint32_t)token_of(64 * wave + lane) * sbytes;
     vsb = ((uint32_t)wave * (uint32_t)N + (uint32_t)column(4 * lane)) * 4u;
     auto copy = [&](int p, int u, int q) __attribute__((always_inline)) {    // copy q of pair p into slot u
       uint8_t* const s = smem + u * kSlotBytes;
       if (q < 2 * MI) dma16(ra, s + (2 * MI * wave + q) * 1024, va[q], (uint32_t)p * kLine);
       else dma16(rb, s + BM * kLine + (8 * wave + q - 2 * MI) * 1024, vb[q - 2 * MI], (uint32_t)p * kLine);
     };
-    auto copy_scales = [&](int ks) __attribute__((always_inline)) {          // of stages ks .. ks + 3, ks a multiple of 4
-      uint8_t* const s = smem + kRingBytes + ((ks >> 2) & 1) * kScaleSlot;
-      dma16(rsa, s + wave * 1024, vsa, (uint32_t)ks * 4u);
-      dma16(rsb, s + BM * 16 + wave * 1024, vsb, (uint32_t)ks * (uint32_t)N * 4u);
+    auto copy_scales = [&](int ks, bool rows_, bool columns) __attribute__((always_inline)) {
+      uint8_t* const s = smem + kRingBytes + ((ks >> 2) & 1) * kScaleSlot;   // of stages ks .. ks + 3, ks a multiple of 4
+      if (rows_) dma16(rsa, s + wave * 1024, vsa, (uint32_t)ks * 4u);
+      if (columns) dma16(rsb, s + BM * 16 + wave * 1024, vsb, (uint32_t)ks * (uint32_t)N * 4u);
     };
+    copy_scales(0, false, true);
+#pragma unroll
+    for (int q = 2 * MI; q < kLoads; ++q) copy(0, 0, q);
+    sched_fence();
+    const int mine = token_of(slot_copy);           // a lane has a row's token
+#pragma unroll
+    for (int j = 0; j < 2 * MI; ++j) {
+      const int r = (2 * MI * wave + j) * 8 + (lane >> 3);
+      va[j] = (uint32_t)__shfl(mine, 8 * j + (lane >> 3)) * abytes + (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) << 4);
+    }
+    vsa = (uint32_t)token_of(slot_scale) * sbytes;
 
     const int h = lane >> 5, r32 = lane & 31;
     int arow[MI], bcol[4];
@@ -395,9 +409,9 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
     // ---- prologue: pairs 0 and 1 in flight, stage 0 in registers
-    copy_scales(0);
+    copy_scales(0, true, false);
 #pragma unroll
-    for (int q = 0; q < kLoads; ++q) copy(0, 0, q);
+    for (int q = 0; q < 2 * MI; ++q) copy(0, 0, q);
     if (nk > 2) {
 #pragma unroll
       for (int q = 0; q < kLoads; ++q) copy(1, 1, q);
@@ -441,7 +455,7 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
 #pragma unroll
           for (int o = t * kOut / (6 * MI); o < min((t + 1) * kOut / (6 * MI), kOut); ++o) {
             if (o < kLoads) copy((ks + 3) >> 1, U >> 1, o);
-            else if (o == kLoads) copy_scales(ks + 3);
+            else if (o == kLoads) copy_scales(ks + 3, true, true);
           }
         }
         if (more) {
