@@ -251,3 +251,63 @@ def test_refusals():
         G.gmm_mxfp4_fwd(x, codes, scales, sizes, topk=0)
     assert e.value.status == G.ERR_SHAPE
     assert G.gmm_mxfp4_fwd(x[:0], codes, scales, sizes).shape == (0, 256)
+
+
+# K of 1024 and more with 64 rows an expert and more: the large tiles.  Counts of 128 k: 8, 9, 10, 11, 17, 13.
+LARGE = [(700, 1, 3, 1024, 256), (333, 3, 2, 1152, 512), (500, 2, 5, 1280, 768), (64, 1, 1, 1408, 1024),
+         (900, 1, 4, 2176, 256), (2600, 1, 7, 1664, 2304)]
+
+
+@pytest.mark.parametrize("T,k,G_,K,N", LARGE)
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_product_large_tiles(T, k, G_, K, N, swiglu):
+    test_product(T, k, G_, K, N, swiglu)
+
+
+@pytest.mark.parametrize("M,K,N", [(300, 1024, 128), (700, 1152, 640), (900, 2048, 1152), (200, 640, 1152), (40, 384, 1152)])
+def test_product_columns_off_the_tile(M, K, N):
+    """N a multiple of 128 that ends inside a tile of 256 columns, in each kind of kernel."""
+    import fp8_moe_grouped_amd as G
+    x = activations(M, K, 3)
+    code, byte = weights(3, N, K, 4)
+    codes, scales = P.pack_weights(code, byte)
+    sizes = sizes_of(M, 3, 7)
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    G.gmm_mxfp4_fwd(x.cuda(), codes.cuda(), scales.cuda(), sizes.cuda(), out=out)
+    check(out, *product(x, code, byte, sizes.tolist(), torch.arange(M)), K, False)
+
+
+@pytest.mark.parametrize("rows", [[1], [5, 3], [0, 40, 0, 24], [64, 1, 63, 65, 128, 0, 2], [257, 255, 256, 1]])
+@pytest.mark.parametrize("K", [256, 1024])
+def test_product_row_counts(rows, K):
+    """Experts whose rows end at, before and past a tile's edge; more experts than a wave has lanes."""
+    import fp8_moe_grouped_amd as G
+    N, M = 256, sum(rows)
+    for lead in (0, 70):                             # experts without rows before the others
+        sizes = [0] * lead + rows
+        x = activations(M, K, K)
+        code, byte = weights(len(rows), N, K, 2)
+        codes, scales = P.pack_weights(code, byte)
+        codes = torch.cat((codes[:1].expand(lead, -1, -1), codes)).contiguous()
+        scales = torch.cat((scales[:1].expand(lead, -1, -1, -1), scales)).contiguous()
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = G.gmm_mxfp4_fwd(x.cuda(), codes.cuda(), scales.cuda(), torch.tensor(sizes, dtype=torch.int32).cuda(),
+                              dev_status=st)
+        check(out, *product(x, code, byte, rows, torch.arange(M)), K, False)
+        assert int(st) == 0
+
+
+def test_product_tokens_past_four_gigabytes():
+    """Quantized rows of 4 GiB and more: tokens at both ends of them."""
+    import fp8_moe_grouped_amd as G
+    T, K, N, M = 524_300, 16384, 128, 64
+    at = torch.cat((torch.arange(32), T - 32 + torch.arange(32)))
+    few = activations(M, K, 1)
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device="cuda")
+    x[at.cuda()] = few.cuda()
+    code, byte = weights(1, N, K, 2)
+    codes, scales = P.pack_weights(code, byte)
+    out = G.gmm_mxfp4_fwd(x, codes.cuda(), scales.cuda(), torch.tensor([M], dtype=torch.int32).cuda(),
+                          slot_of_row=at.int().cuda())
+    del x
+    check(out, *product(few, code, byte, [M], torch.arange(M)), K, False)
