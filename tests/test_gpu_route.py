@@ -171,3 +171,55 @@ def test_route_graph_and_stream():
     side.synchronize()
     for a, b in zip(tuple(s), eager[2]):
         assert torch.equal(a, b)
+
+
+# every way a token's logits can lie in lanes: rows of 16 or the wave, 4 to 16 logits a lane, whole 16-byte
+# chunks or not, and lists of 8 keys or all of a lane's
+LANES = [(61, 16, 16), (61, 31, 9), (200, 64, 8), (130, 100, 12), (70, 128, 16), (129, 255, 13), (66, 256, 16),
+         (40, 256, 17), (40, 60, 20), (67, 257, 8), (129, 512, 8), (30, 500, 16), (64, 384, 7), (33, 1023, 3),
+         (50, 1024, 9)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,k", LANES)
+def test_route_lanes(T, E, k, dtype):
+    import fp8_moe_grouped_amd as G
+    x = logits_of(T, E, dtype, T + E + k, coarse=k % 2 == 0, masked=E % 2 == 0).cuda()
+    g = torch.Generator().manual_seed(k)
+    for renorm in (True, False):
+        r = G.moe_route(x, k, renormalize=renorm)
+        check_route(x, k, renorm, r)
+        dw = torch.randn((T, k), generator=g)
+        got = G.moe_route_bwd(dw.cuda(), x, r.ids, r.weights, renormalize=renorm).cpu()
+        want, mag = P.route_bwd(dw, x.cpu(), r.ids.cpu(), r.weights.cpu(), renorm)
+        tol = mag * U32 * (2 * 104 + 64) + 2.0 ** -140       # as in test_route_gradient
+        if dtype == torch.bfloat16:
+            tol = tol + want.abs() * 2.0 ** -8 + 2.0 ** -133
+        assert bool(((got.double() - want).abs() <= tol).all())
+
+
+def test_route_one_expert_takes_every_token():
+    """All tokens prefer the same experts: the longest runs of ranks within waves, blocks and the batch."""
+    import fp8_moe_grouped_amd as G
+    T, E, k = 9001, 256, 4
+    x = torch.zeros((T, E))
+    x[:, [200, 3, 77, 150]] = torch.tensor([4.0, 3.0, 2.0, 1.0])
+    got = G.moe_route(x.cuda(), k)
+    assert torch.equal(got.ids.cpu(), torch.tensor([[200, 3, 77, 150]], dtype=torch.int32).expand(T, k))
+    sizes = torch.zeros(E, dtype=torch.int32)
+    sizes[[3, 77, 150, 200]] = T
+    assert torch.equal(got.group_sizes.cpu(), sizes)
+    t = torch.arange(T, dtype=torch.int32)
+    rows = torch.stack((3 * T + t, t, T + t, 2 * T + t), dim=1)
+    assert torch.equal(got.row_of_slot.cpu(), rows)
+
+
+def test_route_outputs_of_two_calls_are_apart():
+    import fp8_moe_grouped_amd as G
+    x = logits_of(100, 32, torch.float32, 1).cuda()
+    a = G.moe_route(x, 4)
+    kept = [t.clone() for t in a]
+    b = G.moe_route(-x, 4)
+    for t, old, new in zip(a, kept, b):
+        assert torch.equal(t, old) and not torch.equal(t, new)
+    assert a.weights.is_contiguous() and a.row_of_slot.is_contiguous() and a.slot_of_row.shape == (400,)
