@@ -158,7 +158,7 @@ def _req(t, name, dtype, ndim):
 def _same_device(*ts):
     dev = None
     for t in ts:
-        if t is None:
+        if not isinstance(t, torch.Tensor):         # None, or refused by its own check
             continue
         if dev is None:
             dev = t.device
@@ -624,9 +624,9 @@ def _req_logits(logits):
     _req(logits, "logits", getattr(logits, "dtype", None), 2)
 
 
-def _req_slots(t, name, dtype, T=None, k=None):
+def _req_slots(t, name, dtype, T, k):
     _req(t, name, dtype, 2)
-    if T is not None and tuple(t.shape) != (T, k):
+    if t.shape != (T, k):
         raise ValueError(f"{name} must be [{T}, {k}], got {tuple(t.shape)}")
 
 
@@ -656,7 +656,7 @@ def moe_route_bwd(dweights, logits, ids, weights, *, renormalize=True, out=None)
     [T, E], from dweights [T, k] and the call's logits, ids and weights."""
     _req_logits(logits)
     T, E = logits.shape
-    _req_slots(ids, "ids", torch.int32)
+    _req(ids, "ids", torch.int32, 2)
     k = ids.shape[1]
     if ids.shape[0] != T:
         raise ValueError(f"ids must be [{T}, k], got {tuple(ids.shape)}")
@@ -669,24 +669,28 @@ def moe_route_bwd(dweights, logits, ids, weights, *, renormalize=True, out=None)
     return out
 
 
-def _slots(x, name, row_of_slot, rows):
+def _slots(x, name, row_of_slot, rows, *others):
+    """(device, T, k, H) of bf16 rows x and the map; `rows` if x has a row a
+    token.  All tensors given are on the device."""
     _req(x, name, torch.bfloat16, 2)
-    _req_slots(row_of_slot, "row_of_slot", torch.int32)
+    _req(row_of_slot, "row_of_slot", torch.int32, 2)
     T, k = row_of_slot.shape
-    if rows is not None and x.shape[0] != T:
+    R, H = x.shape
+    if rows and R != T:
         raise ValueError(f"{name} must have the {T} rows of row_of_slot, got {tuple(x.shape)}")
-    return _same_device(x, row_of_slot), T, k, x.shape[1]
+    return _same_device(x, row_of_slot, *others), T, k, H
 
 
 def moe_permute(x, row_of_slot, *, out=None):
     """bf16 [R, H]: row row_of_slot[t, j] is x[t] (R = T * k, or the rows of
     ``out``); rows that no slot names are left as they are."""
-    dev, T, k, H = _slots(x, "x", row_of_slot, True)
+    dev, T, k, H = _slots(x, "x", row_of_slot, True, out)
     if out is None:
         out = torch.empty((T * k, H), dtype=torch.bfloat16, device=dev)
-    _req(out, "out", torch.bfloat16, 2)
-    if out.shape[1] != H or out.device != dev:
-        raise ValueError(f"out must be [R, {H}] on {dev}, got {tuple(out.shape)} on {out.device}")
+    else:
+        _req(out, "out", torch.bfloat16, 2)
+        if out.shape[1] != H:
+            raise ValueError(f"out must be [R, {H}], got {tuple(out.shape)}")
     _launch(dev, "moe_permute", _ptr(x), _ptr(row_of_slot), T, k, out.shape[0], H, _ptr(out))
     return out
 
@@ -695,11 +699,10 @@ def moe_permute_fp8(x, row_of_slot, *, codes=None, scales=None):
     """e4m3 codes [R, H] and f32 row scales [R] of moe_permute's rows, as
     quantize_rows_fp8 gives them: the operands of gmm_fp8_fwd_q and
     gmm_silu_fp8_q."""
-    dev, T, k, H = _slots(x, "x", row_of_slot, True)
+    dev, T, k, H = _slots(x, "x", row_of_slot, True, codes, scales)
     R = T * k if codes is None else codes.shape[0]
     codes = _out(codes, (R, H), torch.uint8, dev, "codes")
     scales = _out(scales, (R,), torch.float32, dev, "scales")
-    _same_device(x, codes, scales)
     _launch(dev, "moe_permute_fp8", _ptr(x), _ptr(row_of_slot), T, k, R, H, _ptr(codes), _ptr(scales))
     return codes, scales
 
@@ -707,11 +710,10 @@ def moe_permute_fp8(x, row_of_slot, *, codes=None, scales=None):
 def moe_combine(y, row_of_slot, weights=None, *, out=None):
     """bf16 [T, H]: the sum of each token's rows of y [R, H] with its weights
     [T, k]; without weights the plain sum, moe_permute's gradient."""
-    dev, T, k, H = _slots(y, "y", row_of_slot, None)
+    dev, T, k, H = _slots(y, "y", row_of_slot, False, weights, out)
     if weights is not None:
         _req_slots(weights, "weights", torch.float32, T, k)
     out = _out(out, (T, H), torch.bfloat16, dev, "out")
-    _same_device(y, weights, out)
     _launch(dev, "moe_combine", _ptr(y), _ptr(row_of_slot), _ptr(weights), T, k, y.shape[0], H, _ptr(out))
     return out
 
@@ -719,14 +721,13 @@ def moe_combine(y, row_of_slot, weights=None, *, out=None):
 def moe_combine_bwd(dout, y, row_of_slot, weights, *, dy=None, dweights=None):
     """moe_combine's gradients from dout [T, H]: (dy bf16 [R, H], dweights f32
     [T, k]).  Rows of dy that no slot names are left as they are."""
-    dev, T, k, H = _slots(dout, "dout", row_of_slot, True)
+    dev, T, k, H = _slots(dout, "dout", row_of_slot, True, y, weights, dy, dweights)
     _req(y, "y", torch.bfloat16, 2)
     if y.shape[1] != H:
         raise ValueError(f"y must be [R, {H}], got {tuple(y.shape)}")
     _req_slots(weights, "weights", torch.float32, T, k)
     dy = _out(dy, tuple(y.shape), torch.bfloat16, dev, "dy")
     dweights = _out(dweights, (T, k), torch.float32, dev, "dweights")
-    _same_device(dout, y, weights, dy, dweights)
     _launch(dev, "moe_combine_bwd", _ptr(dout), _ptr(y), _ptr(row_of_slot), _ptr(weights), T, k, y.shape[0], H, _ptr(dy),
             _ptr(dweights))
     return dy, dweights

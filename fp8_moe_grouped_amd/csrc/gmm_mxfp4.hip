@@ -195,7 +195,7 @@ __global__ __launch_bounds__(256, 2) void gmm_mxfp4_stream_kernel(
     copy4(vsa + 8 * p, slot + (BM + BN) * kLine + wave * 256);
   };
   copy_rows(0, smem);
-  if (R == 3 && np > 1) {
+  if (np > 1) {
     copy_weights(1, smem + kSlot);
     copy_rows(1, smem + kSlot);
   }
@@ -206,17 +206,18 @@ __global__ __launch_bounds__(256, 2) void gmm_mxfp4_stream_kernel(
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
-  int cur = 0, ahead = R - 1;                       // slots of pair p and of pair p + R - 1
+  int cur = 0, ahead = 2 % R;                       // slots of pair p and of pair p + 2
   // LEFT: pairs after this one, 2 standing for more.
   auto step = [&](int p, auto left_c) __attribute__((always_inline)) {
     constexpr int LEFT = decltype(left_c)::value;
-    if (R == 3 && LEFT > 0) wait_vmem_lds<kLoads>();     // pair p is there, pair p + 1 on its way
+    if (LEFT > 0) wait_vmem_lds<kLoads>();          // pair p is there, pair p + 1 on its way
     else wait_vmem_lds<0>();
     barrier_only();                                 // and every wave has read pair p - 1
-    if (LEFT > R - 2) {
-      copy_weights(p + R - 1, smem + ahead * kSlot);
-      copy_rows(p + R - 1, smem + ahead * kSlot);
-    }
+    auto copy_ahead = [&]() __attribute__((always_inline)) {
+      copy_weights(p + 2, smem + ahead * kSlot);
+      copy_rows(p + 2, smem + ahead * kSlot);
+    };
+    if (R == 3 && LEFT > 1) copy_ahead();
     const uint8_t* const slot = smem + cur * kSlot;
     const uint8_t* const sc = slot + (BM + BN) * kLine;
 #pragma unroll
@@ -239,6 +240,11 @@ __global__ __launch_bounds__(256, 2) void gmm_mxfp4_stream_kernel(
 #pragma unroll
       for (int i = 0; i < MI; ++i) acc[i] = mfma_mxfp4_32<2>(b[1], a[i][1], acc[i], xb, xa[i]);
     }
+    if (R == 2 && LEFT > 1) {                       // the slot that was just read
+      wait_vmem_lds<63>();
+      barrier_only();
+      copy_ahead();
+    }
     cur = cur == R - 1 ? 0 : cur + 1;
     ahead = ahead == R - 1 ? 0 : ahead + 1;
   };
@@ -249,7 +255,7 @@ __global__ __launch_bounds__(256, 2) void gmm_mxfp4_stream_kernel(
 
   // a lane holds row 32 i + r32, columns 8q + 4h + 0..3 of its wave's 32
   constexpr int COLS = SWIGLU ? 64 : 128;
-  static_assert(BM * kOutRow<COLS> <= R * kSlot, "the results fit the ring");
+  static_assert(BM * kOutRow<COLS> <= kSlot, "the results fit one slot");
   wait_vmem_lds<0>();
   barrier_only();                                   // every wave has read the last pair
 #pragma unroll
@@ -527,7 +533,7 @@ static hipError_t launch_stream(const uint8_t* aq, const uint8_t* ascale, const 
                                 int N, bool swiglu, uint16_t* out, int* status, hipStream_t stream) {
   const long long tiles = std::min<long long>(M, ((long long)M + 32 * MI - 1) / (32 * MI) + G);
   const dim3 grid((unsigned)(tiles * (N / 128)));
-  const size_t lds = kRing<MI> * ((32 * MI + 128) * kLine + 2048);
+  const size_t lds = std::min(kRing<MI>, (K + 255) / 256) * ((32 * MI + 128) * kLine + 2048);   // a slot a pair at most
   if (swiglu)
     hipLaunchKernelGGL((gmm_mxfp4_stream_kernel<MI, true>), grid, dim3(256), lds, stream, aq, ascale, codes, wscale,
                        group_sizes, slot_of_row, topk, T, G, M, K, N, out, status);
