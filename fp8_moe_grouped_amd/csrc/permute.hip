@@ -11,7 +11,10 @@
 //
 // A row outside [0, R) (a masked choice holds -1) is neither read nor written
 // and counts as zero.  All are bound by HBM: every token's row is read once and
-// every expert row is touched once, in 16-byte chunks.
+// every expert row is touched once, in 16-byte chunks, with the streaming policy on
+// the k times larger side, which is not read again before it has left the caches:
+// 4096 x 7168, k = 8: permute 91 us (5.8 TB/s; 106 without the policy), combine 90
+// (5.9 TB/s; 104), its gradient 188 (5.3 TB/s; 200).
 #include "common.hpp"
 #include "launch.hpp"
 

@@ -20,7 +20,7 @@
 // A lane sorts its keys once with a network; k times the largest head over the
 // lanes is taken and its lane's list moves up.  (Searching all keys k times, one
 // token a wave, was bound by its instructions: 18 us for 16384 x 256 bf16, k = 8,
-// against 8.1 us now, of which 2 us are the bytes.)
+// against 7.3 us now, of which 2 us are the bytes.)
 //
 // A token's choices are distinct, so a wave counts them into its LDS histogram
 // without conflicts, and the count before the increment is the slot's rank among
@@ -376,9 +376,10 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const int* __rest
   }
 }
 
-// Gradient.  Lanes share tokens as above: lane j < k holds choice j and puts its
-// term into the token's row in LDS (the wave's own, so no barrier), which the lanes
-// then read as their chunks.
+// Gradient: 16384 x 160 f32 in 7.2 us, 4.1 us of them bytes (one token a wave with
+// comparisons for each choice: 11.4).  Lanes share tokens as above: lane j < k holds
+// choice j and puts its term into the token's row in LDS (the wave's own, so no
+// barrier), which the lanes then read as their chunks.
 template <int L, int V, typename TX>
 __global__ __launch_bounds__(256) void route_bwd_kernel(const float* __restrict__ dweights,
                                                         const TX* __restrict__ logits, const int* __restrict__ ids,
