@@ -8,12 +8,18 @@ point of the same name on the current HIP stream.  Every step of the
 computation runs in the library's HIP kernels; there is no fallback.  If the
 shared library is missing the first call raises.
 
+The calls around the products (routing, dispatch, combine, 4-bit) first hand
+their arguments to a small extension (csrc/calls.cpp), which makes the same C
+call without the interpreter's checks where the arguments are the plain ones;
+it answers None otherwise, and the function here checks, calls and reports.
+
 The C contract of every call is documented in include/fp8_moe_grouped.h.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
 import os
 import re
 from typing import NamedTuple
@@ -22,6 +28,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8_moe_grouped.so")
+CALLS_PATH = os.path.join(_HERE, "_calls.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "fp8_moe_grouped.h")
 
 OK = 0
@@ -82,6 +89,22 @@ _SIGNATURES = {
 }
 
 _lib = None
+_calls = None
+
+
+def _plain():
+    """The extension of csrc/calls.cpp on the library's entry points."""
+    global _calls
+    if _calls is None:
+        L = lib()
+        if not os.path.exists(CALLS_PATH):
+            raise RuntimeError(f"{CALLS_PATH} is missing: build it first (python -m fp8_moe_grouped_amd.build)")
+        spec = importlib.util.spec_from_file_location("fp8_moe_grouped_amd._calls", CALLS_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.bind(*(ctypes.cast(getattr(L, name), _P).value for name in m.names()))
+        _calls = m
+    return _calls
 
 
 def lib() -> ctypes.CDLL:
@@ -120,10 +143,10 @@ def workspace_bytes(op: int, M: int, K: int, N: int, G: int, tile_m: int = 512) 
 
 # --------------------------------------------------------------------------- marshalling
 
-# A decoded token's call runs for a few microseconds on the GPU, so what a call
-# costs the host counts: plain integers for pointers, the current stream's handle
-# without a Stream object (0.1 us, not 2), and no device switch where the device
-# is the current one already (0.2 us, not 1.4).
+# What a call costs the host counts beside kernels of a few microseconds: plain
+# integers for pointers, the current stream's handle without a Stream object
+# (0.1 us, not 2), and no device switch where the device is the current one
+# already (0.2 us, not 1.4).
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
@@ -635,10 +658,14 @@ def moe_route(logits, k, *, renormalize=True, workspace=None):
     -inf masks an expert), their softmax weights (over the chosen experts, or
     over all without ``renormalize``) and the slots' stable sort by expert:
     a MoeRouting."""
+    k = int(k)
+    if workspace is None:
+        r = (_calls or _plain()).route(logits, k, renormalize)
+        if r is not None:
+            return MoeRouting._make(r)
     _req_logits(logits)
     dev = logits.device
     T, E = logits.shape
-    k = int(k)
     if not 1 <= k <= E:
         raise ValueError(f"k must be between 1 and the {E} experts, got {k}")
     # one allocation for the four outputs of a slot (a view costs the host less than a tensor)
@@ -654,6 +681,10 @@ def moe_route(logits, k, *, renormalize=True, workspace=None):
 def moe_route_bwd(dweights, logits, ids, weights, *, renormalize=True, out=None):
     """The gradient of moe_route's weights by its logits, in the logits' type
     [T, E], from dweights [T, k] and the call's logits, ids and weights."""
+    if out is None:
+        out = (_calls or _plain()).route_bwd(dweights, logits, ids, weights, renormalize)
+        if out is not None:
+            return out
     _req_logits(logits)
     T, E = logits.shape
     _req(ids, "ids", torch.int32, 2)
@@ -684,6 +715,10 @@ def _slots(x, name, row_of_slot, rows, *others):
 def moe_permute(x, row_of_slot, *, out=None):
     """bf16 [R, H]: row row_of_slot[t, j] is x[t] (R = T * k, or the rows of
     ``out``); rows that no slot names are left as they are."""
+    if out is None:
+        out = (_calls or _plain()).permute(x, row_of_slot)
+        if out is not None:
+            return out
     dev, T, k, H = _slots(x, "x", row_of_slot, True, out)
     if out is None:
         out = torch.empty((T * k, H), dtype=torch.bfloat16, device=dev)
@@ -699,6 +734,10 @@ def moe_permute_fp8(x, row_of_slot, *, codes=None, scales=None):
     """e4m3 codes [R, H] and f32 row scales [R] of moe_permute's rows, as
     quantize_rows_fp8 gives them: the operands of gmm_fp8_fwd_q and
     gmm_silu_fp8_q."""
+    if codes is None and scales is None:
+        r = (_calls or _plain()).permute_fp8(x, row_of_slot)
+        if r is not None:
+            return r
     dev, T, k, H = _slots(x, "x", row_of_slot, True, codes, scales)
     R = T * k if codes is None else codes.shape[0]
     codes = _out(codes, (R, H), torch.uint8, dev, "codes")
@@ -710,6 +749,10 @@ def moe_permute_fp8(x, row_of_slot, *, codes=None, scales=None):
 def moe_combine(y, row_of_slot, weights=None, *, out=None):
     """bf16 [T, H]: the sum of each token's rows of y [R, H] with its weights
     [T, k]; without weights the plain sum, moe_permute's gradient."""
+    if out is None:
+        out = (_calls or _plain()).combine(y, row_of_slot, weights)
+        if out is not None:
+            return out
     dev, T, k, H = _slots(y, "y", row_of_slot, False, weights, out)
     if weights is not None:
         _req_slots(weights, "weights", torch.float32, T, k)
@@ -721,6 +764,10 @@ def moe_combine(y, row_of_slot, weights=None, *, out=None):
 def moe_combine_bwd(dout, y, row_of_slot, weights, *, dy=None, dweights=None):
     """moe_combine's gradients from dout [T, H]: (dy bf16 [R, H], dweights f32
     [T, k]).  Rows of dy that no slot names are left as they are."""
+    if dy is None and dweights is None:
+        r = (_calls or _plain()).combine_bwd(dout, y, row_of_slot, weights)
+        if r is not None:
+            return r
     dev, T, k, H = _slots(dout, "dout", row_of_slot, True, y, weights, dy, dweights)
     _req(y, "y", torch.bfloat16, 2)
     if y.shape[1] != H:
@@ -738,6 +785,10 @@ def moe_combine_bwd(dout, y, row_of_slot, weights, *, dy=None, dweights=None):
 def quantize_mxfp4_weights(w, *, codes=None, scales=None):
     """MXFP4 codes u8 [G, N, K/2] and scales u8 [G, K/128, N, 4] of weights
     w bf16 [G, K, N], in blocks of 32 along K."""
+    if codes is None and scales is None:
+        r = (_calls or _plain()).quantize_weights(w)
+        if r is not None:
+            return r
     _req(w, "w", torch.bfloat16, 3)
     G, K, N = w.shape
     dev = w.device
@@ -762,6 +813,10 @@ def _mxfp4_shapes(codes, scales):
 def dequantize_mxfp4(codes, scales, *, out=None):
     """The values bf16 [G, N, K] of MXFP4 codes [G, N, K/2] and scales
     [G, K/128, N, 4]."""
+    if out is None:
+        out = (_calls or _plain()).values(codes, scales)
+        if out is not None:
+            return out
     G, K, N = _mxfp4_shapes(codes, scales)
     dev = _same_device(codes, scales)
     out = _out(out, (G, N, K), torch.bfloat16, dev, "out")
@@ -771,6 +826,11 @@ def dequantize_mxfp4(codes, scales, *, out=None):
 
 
 def _mxfp4_product(name, x, codes, scales, group_sizes, slot_of_row, topk, out, dev_status, workspace, swiglu):
+    topk = int(topk)
+    if out is None and workspace is None and dev_status is None:
+        out = (_calls or _plain()).product(x, codes, scales, group_sizes, slot_of_row, topk, swiglu)
+        if out is not None:
+            return out
     _req(x, "x", torch.bfloat16, 2)
     G, K, N = _mxfp4_shapes(codes, scales)
     _req(group_sizes, "group_sizes", torch.int32, 1)
@@ -786,7 +846,7 @@ def _mxfp4_product(name, x, codes, scales, group_sizes, slot_of_row, topk, out, 
     out = _out(out, (M, N // 2 if swiglu else N), torch.bfloat16, dev, "out")
     _same_device(x, out)
     ws, need = _workspace(OP_MXFP4, T, K, N, G, dev, tile_m=0, workspace=workspace)
-    _launch(dev, name, _ptr(x), _ptr(codes), _ptr(scales), _ptr(group_sizes), _ptr(slot_of_row), int(topk), T, M, K, N, G,
+    _launch(dev, name, _ptr(x), _ptr(codes), _ptr(scales), _ptr(group_sizes), _ptr(slot_of_row), topk, T, M, K, N, G,
             _ptr(out), _ptr(ws), need, _ptr(dev_status))
     return out
 
