@@ -41,6 +41,9 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kTokensPerWave = 4;
 constexpr int kTokensPerBlock = kWaves * kTokensPerWave;   // per chunk
 constexpr int kMaxBlocks = 512;                     // longer batches give a block several chunks
+constexpr int kByteChunks = 3;                      // 192 tokens
+static_assert(kByteChunks * kTokensPerBlock < 256, "a block's count fits a byte");
+__host__ __device__ constexpr int hist_row(int E) { return (E + 15) & ~15; }
 
 // The wave's lanes see each other's LDS writes past this point: LDS serves a wave in order, and
 // the compiler may neither move nor forward accesses across it.
@@ -198,15 +201,15 @@ __device__ __forceinline__ void choose(const float (&x)[V], int E, int k, bool r
   w = id >= 0 ? e / total : 0.f;
 }
 
-// hist holds a block's slots per expert as 16 bits (a block has fewer than 2^16
-// tokens, and a token chooses an expert once): [blocks][Ep], Ep = E rounded up to 8.
+// hist holds a block's slots per expert, at most one a token: bytes for up to
+// kByteChunks chunks a block, 16 bits beyond; a row of 16-byte multiples a block.
 // ONE: the grid is one block, of as many waves as its tokens need, which places the
 // slots itself.
 template <int L, int V, int D, typename TX, bool ONE>
 __global__ __launch_bounds__(kThreads) void route_topk_kernel(const TX* __restrict__ logits, int T, int E, int k,
                                                              int renorm, int chunks, int* __restrict__ ids,
                                                              float* __restrict__ weights, int* __restrict__ row_of_slot,
-                                                             uint16_t* __restrict__ hist, int* __restrict__ group_sizes,
+                                                             void* __restrict__ hist, int* __restrict__ group_sizes,
                                                              int* __restrict__ slot_of_row) {
   constexpr int kRounds = kTokensPerWave * L / 64;  // tokens of a wave, 64 / L at a time
   extern __shared__ int smem[];
@@ -305,57 +308,102 @@ __global__ __launch_bounds__(kThreads) void route_topk_kernel(const TX* __restri
     }
   }
   if (!ONE) {
-    const int Ep = (E + 7) & ~7;
-    for (int e = tid; e < Ep; e += threads) hist[(size_t)blockIdx.x * Ep + e] = (uint16_t)(e < E ? seen[e] : 0);
+    const int Ep = hist_row(E);
+    for (int e = tid; e < Ep; e += threads) {
+      const int n = e < E ? seen[e] : 0;
+      const size_t at = (size_t)blockIdx.x * Ep + e;
+      if (chunks <= kByteChunks) static_cast<uint8_t*>(hist)[at] = (uint8_t)n;
+      else static_cast<uint16_t*>(hist)[at] = (uint16_t)n;
+    }
   }
 }
 
 // Places the slots of block b: an expert's first row, plus its slots in earlier
 // blocks, plus the rank within the block that route_topk_kernel left in row_of_slot.
-// Every block sums the whole histogram (128 KB at 16384 x 256, from L2) instead of a
-// launch between that would scan it.
-__global__ __launch_bounds__(kThreads) void route_place_kernel(const int* __restrict__ ids,
-                                                              const uint16_t* __restrict__ hist, int T, int E, int k,
-                                                              int chunks, int* __restrict__ group_sizes,
+// Every block sums the whole histogram instead of a launch between that would scan
+// it: 64 KB at 16384 x 256, from L2, in bytes and two counts an addition (as 16 bits,
+// one count an addition and LDS atomics, 6.5 us; now 5.8).
+//
+// Thread (segment, chunk of 16 bytes) adds the rows segment, segment + segments, ..
+template <typename H>
+__global__ __launch_bounds__(kThreads) void route_place_kernel(const int* __restrict__ ids, const H* __restrict__ hist,
+                                                              int T, int E, int k, int chunks, int chunk_lanes,
+                                                              int* __restrict__ group_sizes,
                                                               int* __restrict__ row_of_slot,
                                                               int* __restrict__ slot_of_row) {
-  extern __shared__ int smem[];
-  const int Ep = (E + 7) & ~7, ne = Ep / 8;
-  int* const first = smem;                          // [Ep] slots in earlier blocks, then the block's first rows
-  int* const total = smem + Ep;                     // [Ep]
+  constexpr int C = 16 / (int)sizeof(H);            // counts of a chunk
+  extern __shared__ __attribute__((aligned(16))) int smem[];
+  const int Ep = hist_row(E);
+  int* const first = smem;                          // [Ep] the block's first rows
+  int* const sums = smem + Ep;                      // [partial sums][2][Ep]
   __shared__ int part[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int b = blockIdx.x, nb = gridDim.x;
-  auto place = [&](int e) { return (e & 7) * ne + (e >> 3); };   // eight lanes' experts in different banks
   const int s0 = b * chunks * kTokensPerBlock * k;  // T * k < 2^24, and a block starts below T
   const int s1 = min(s0 + chunks * kTokensPerBlock * k, T * k);
   const int mine = s0 + tid;                        // the first slot's loads run while the histogram is summed
-  int id0 = mine < s1 ? ids[mine] : -1, rank0 = mine < s1 ? row_of_slot[mine] : 0;
-  for (int e = tid; e < 2 * Ep; e += kThreads) smem[e] = 0;
-  __syncthreads();
-  // thread (segment, 8 experts): the histogram's rows segment, segment + nseg, ...
-  const int nseg = kThreads / ne, seg = tid / ne, g8 = tid % ne;
-  if (seg < nseg) {
-    int before[8] = {}, all[8] = {};
-#pragma unroll 8
-    for (int r = seg; r < nb; r += nseg) {
-      const v4i h = *reinterpret_cast<const v4i*>(hist + (size_t)r * Ep + 8 * g8);
+  const int id0 = mine < s1 ? ids[mine] : -1, rank0 = mine < s1 ? row_of_slot[mine] : 0;
+  // chunk_lanes: the chunks of a row, rounded up to a power of two
+  const int g = tid & (chunk_lanes - 1), seg = tid / chunk_lanes, segs = kThreads / chunk_lanes;
+  const bool here = g * C < Ep;
+  // bytes: counts 0 and 2 of a word in acc[2j] and 1 and 3 in acc[2j + 1], 16 bits each (a wave adds at most
+  // 32 rows of 192); 16 bits: one count each
+  uint32_t acc[2][8] = {};                          // rows before b, all rows
+  if (here)
+    for (int r0 = seg; r0 < nb; r0 += 4 * segs) {
+      v4i h[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int n = (int)(((uint32_t)h[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-        all[i] += n;
-        if (r < b) before[i] += n;
+      for (int u = 0; u < 4; ++u) {
+        const int r = r0 + u * segs;
+        h[u] = r < nb ? *reinterpret_cast<const v4i*>(hist + (size_t)r * Ep + C * g) : (v4i){0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t earlier = r0 + u * segs < b ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t w = (uint32_t)h[u][j / 2];
+          const uint32_t c = sizeof(H) == 1 ? (j & 1 ? w >> 8 : w) & 0x00FF00FFu : (j & 1 ? w >> 16 : w & 0xFFFFu);
+          acc[0][j] += c & earlier;
+          acc[1][j] += c;
+        }
       }
     }
+  // segments of a wave, to all its lanes (uniform branches; shuffles through LDS took half of the kernel)
+  auto join = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {                   // sums of whole numbers: any order gives the same
-      if (before[i]) atomicAdd(&first[i * ne + g8], before[i]);
-      if (all[i]) atomicAdd(&total[i * ne + g8], all[i]);
+    for (int i = 0; i < 16; ++i) acc[i / 8][i % 8] += f(acc[i / 8][i % 8]);
+  };
+  if (chunk_lanes <= 8) join([](uint32_t v) { return dpp_row<0x128>(v); });
+  if (chunk_lanes <= 4) join([](uint32_t v) { return dpp_row<0x124>(v); });
+  if (chunk_lanes <= 2) join([](uint32_t v) { return dpp_row<0x122>(v); });
+  if (chunk_lanes <= 1) join([](uint32_t v) { return dpp_row<0x121>(v); });
+  if (chunk_lanes <= 16) join([&](uint32_t v) { return other_rows<16>(v, (lane & 16) != 0); });
+  if (chunk_lanes <= 32) join([&](uint32_t v) { return other_rows<32>(v, (lane & 32) != 0); });
+  const int rows_of_sums = min(segs, kWaves), at = min(seg, tid / 64);
+  if (here && (chunk_lanes >= 64 || lane < chunk_lanes))
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v4i* const out = reinterpret_cast<v4i*>(sums + (2 * at + i) * Ep + C * g);
+      const uint32_t(&a)[8] = acc[i];
+#pragma unroll
+      for (int j = 0; j < C / 4; ++j)
+        out[j] = sizeof(H) == 1 ? (v4i){(int)(a[2 * j] & 0xFFFF), (int)(a[2 * j + 1] & 0xFFFF), (int)(a[2 * j] >> 16),
+                                        (int)(a[2 * j + 1] >> 16)}
+                                : (v4i){(int)a[4 * j % 8], (int)a[(4 * j + 1) % 8], (int)a[(4 * j + 2) % 8],
+                                        (int)a[(4 * j + 3) % 8]};
     }
-  }
   __syncthreads();
-  const int n = tid < E ? total[place(tid)] : 0;    // E <= kThreads
-  if (b == 0 && tid < E) group_sizes[tid] = n;
+  int before = 0, n = 0;
+  if (tid < E) {                                    // E <= kThreads
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+      if (w < rows_of_sums) {
+        before += sums[2 * w * Ep + tid];
+        n += sums[(2 * w + 1) * Ep + tid];
+      }
+    if (b == 0) group_sizes[tid] = n;
+  }
   const int incl = wave_scan_dpp(n);
   if (lane == 63) part[wave] = incl;
   __syncthreads();
@@ -365,11 +413,11 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const int* __rest
     if (v < wave) offset += part[v];
     rows += part[v];
   }
-  if (tid < E) first[place(tid)] += offset + incl - n;
+  if (tid < E) first[tid] = before + offset + incl - n;
   __syncthreads();
   for (int s = mine; s < s1; s += kThreads) {
     const int id = s == mine ? id0 : ids[s], rank = s == mine ? rank0 : row_of_slot[s];
-    const int row = id < 0 ? -1 : first[place(id)] + rank;
+    const int row = id < 0 ? -1 : first[id] + rank;
     row_of_slot[s] = row;
     if (row >= 0) slot_of_row[row] = s;
     if (s >= rows) slot_of_row[s] = -1;             // no slot is placed there
@@ -466,7 +514,7 @@ int route_blocks(int T, int& chunks) {
 
 template <int L, int V, int D, typename TX>
 hipError_t route_impl(const TX* logits, int T, int E, int k, int renorm, int* ids, float* weights, int* group_sizes,
-                      int* row_of_slot, int* slot_of_row, uint16_t* hist, hipStream_t stream) {
+                      int* row_of_slot, int* slot_of_row, void* hist, hipStream_t stream) {
   int chunks;
   const int nb = route_blocks(T, chunks);
   if (nb <= 1) {
@@ -480,15 +528,25 @@ hipError_t route_impl(const TX* logits, int T, int E, int k, int renorm, int* id
                      slot_of_row);
   hipError_t st = hipGetLastError();
   if (st != hipSuccess) return st;
-  hipLaunchKernelGGL(route_place_kernel, dim3(nb), dim3(kThreads), sizeof(int) * 2 * (size_t)((E + 7) & ~7), stream,
-                     ids, hist, T, E, k, chunks, group_sizes, row_of_slot, slot_of_row);
+  const int Ep = hist_row(E), C = chunks <= kByteChunks ? 16 : 8;
+  int chunk_lanes = 1;
+  while (chunk_lanes * C < Ep) chunk_lanes *= 2;
+  const size_t place_lds = sizeof(int) * (size_t)Ep * (1 + 2 * std::min(kThreads / chunk_lanes, kWaves));
+  if (chunks <= kByteChunks)
+    hipLaunchKernelGGL(route_place_kernel<uint8_t>, dim3(nb), dim3(kThreads), place_lds, stream, ids,
+                       static_cast<const uint8_t*>(hist), T, E, k, chunks, chunk_lanes, group_sizes, row_of_slot,
+                       slot_of_row);
+  else
+    hipLaunchKernelGGL(route_place_kernel<uint16_t>, dim3(nb), dim3(kThreads), place_lds, stream, ids,
+                       static_cast<const uint16_t*>(hist), T, E, k, chunks, chunk_lanes, group_sizes, row_of_slot,
+                       slot_of_row);
   return hipGetLastError();
 }
 
 // A lane holds whole 16-byte chunks: 4 logits in f32, 8 in bf16.
 template <typename TX>
 hipError_t route_pick(const TX* logits, int T, int E, int k, int renorm, int* ids, float* weights, int* group_sizes,
-                      int* row_of_slot, int* slot_of_row, uint16_t* hist, hipStream_t stream) {
+                      int* row_of_slot, int* slot_of_row, void* hist, hipStream_t stream) {
   constexpr int C = 16 / (int)sizeof(TX);
 #define ROUTE(L, V)                                                                                                    \
   (k <= 8 ? route_impl<L, V, V < 8 ? V : 8, TX>(logits, T, E, k, renorm, ids, weights, group_sizes, row_of_slot,       \
@@ -528,17 +586,16 @@ hipError_t route_bwd_pick(const float* dweights, const TX* logits, const int* id
 size_t route_workspace_bytes(int T, int E) {
   int chunks;
   const int nb = T > 0 ? route_blocks(T, chunks) : 0;
-  return nb <= 1 ? 0 : sizeof(uint16_t) * (size_t)nb * ((E + 7) & ~7);
+  return nb <= 1 ? 0 : (chunks <= kByteChunks ? 1 : 2) * (size_t)nb * hist_row(E);
 }
 
 hipError_t launch_route(const void* logits, bool bf16, int T, int E, int k, bool renorm, int* ids, float* weights,
                         int* group_sizes, int* row_of_slot, int* slot_of_row, void* ws, hipStream_t stream) {
-  uint16_t* hist = static_cast<uint16_t*>(ws);
   if (bf16)
     return route_pick(static_cast<const uint16_t*>(logits), T, E, k, renorm, ids, weights, group_sizes, row_of_slot,
-                      slot_of_row, hist, stream);
+                      slot_of_row, ws, stream);
   return route_pick(static_cast<const float*>(logits), T, E, k, renorm, ids, weights, group_sizes, row_of_slot,
-                    slot_of_row, hist, stream);
+                    slot_of_row, ws, stream);
 }
 
 hipError_t launch_route_bwd(const float* dweights, const void* logits, bool bf16, const int* ids, const float* weights,

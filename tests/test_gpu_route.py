@@ -223,3 +223,23 @@ def test_route_outputs_of_two_calls_are_apart():
     for t, old, new in zip(a, kept, b):
         assert torch.equal(t, old) and not torch.equal(t, new)
     assert a.weights.is_contiguous() and a.row_of_slot.is_contiguous() and a.slot_of_row.shape == (400,)
+
+
+@pytest.mark.parametrize("T", [65, 32768, 32769, 98304, 98305, 140000])
+def test_route_tokens_a_block(T):
+    """Every size of a block's histogram: one to five chunks of tokens, counts in bytes and in 16 bits."""
+    test_route_many_tokens(T, 40, 2)
+
+
+@pytest.mark.parametrize("E", [5, 17, 250, 600, 1024])
+def test_route_every_token_to_one_expert(E):
+    """The fullest counts, in the first and the last expert, with 16-bit histograms and with bytes."""
+    import fp8_moe_grouped_amd as G
+    for T in (20000, 100000):
+        for e in (0, E - 1):
+            x = torch.zeros((T, E), dtype=torch.bfloat16, device="cuda")
+            x[:, e] = 1
+            got = G.moe_route(x, 1)
+            assert bool((got.ids == e).all()) and int(got.group_sizes[e]) == T and int(got.group_sizes.sum()) == T
+            t = torch.arange(T, dtype=torch.int32, device="cuda")
+            assert torch.equal(got.row_of_slot.view(-1), t) and torch.equal(got.slot_of_row, t)
