@@ -311,3 +311,34 @@ def test_product_tokens_past_four_gigabytes():
                           slot_of_row=at.int().cuda())
     del x
     check(out, *product(few, code, byte, [M], torch.arange(M)), K, False)
+
+
+# enough tiles of 256 x 256 for the kernel that has them; counts of 128 k: 8, 9, 10, 17, 11, 8
+MANY_TILES = [(300, 1, 3, 1024, 15360), (130, 2, 3, 1152, 10240), (500, 2, 5, 1280, 7168), (577, 1, 9, 2176, 6144),
+              (900, 1, 1, 1408, 8192), (4700, 1, 70, 1024, 1024)]
+
+
+@pytest.mark.parametrize("T,k,G_,K,N", MANY_TILES)
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_product_many_tiles(T, k, G_, K, N, swiglu):
+    test_product(T, k, G_, K, N, swiglu)
+
+
+@pytest.mark.parametrize("rows,N", [([257, 255, 256, 1], 10240), ([64, 1, 63, 65, 300, 0, 200], 10240), ([900], 8320),
+                                    ([130, 700, 70], 8320), ([512, 0, 513, 100], 7296)])
+def test_product_many_tiles_ragged(rows, N):
+    """Rows and columns that end inside the large tiles."""
+    import fp8_moe_grouped_amd as G
+    K, M = 1152, sum(rows)
+    x = activations(M, K, N)
+    code, byte = weights(len(rows), N, K, 2)
+    codes, scales = P.pack_weights(code, byte)
+    out = G.gmm_mxfp4_fwd(x.cuda(), codes.cuda(), scales.cuda(), torch.tensor(rows, dtype=torch.int32).cuda())
+    check(out, *product(x, code, byte, rows, torch.arange(M)), K, False)
+
+
+@pytest.mark.parametrize("M,G_,K,N", [(1500, 3, 2048, 1280), (600, 4, 1152, 1792), (2300, 5, 640, 1536), (700, 20, 512, 384)])
+def test_product_between(M, G_, K, N):
+    """Sizes at which tiles of 32, 64 and 128 rows are taken."""
+    test_product(M, 1, G_, K, N, False)
+    test_product(M, 1, G_, K, N, N % 256 == 0)
