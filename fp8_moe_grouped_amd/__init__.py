@@ -178,6 +178,12 @@ def _req(t, name, dtype, ndim):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _req_i32(v, name):
+    """ctypes would keep the low 32 bits."""
+    if v >= 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits, got {v}")
+
+
 def _same_device(*ts):
     dev = None
     for t in ts:
@@ -666,6 +672,10 @@ def moe_route(logits, k, *, renormalize=True, workspace=None):
     _req_logits(logits)
     dev = logits.device
     T, E = logits.shape
+    _req_i32(E, "the number of experts")
+    if workspace is not None:
+        _req(workspace, "workspace", torch.uint8, 1)
+        _same_device(logits, workspace)
     if not 1 <= k <= E:
         raise ValueError(f"k must be between 1 and the {E} experts, got {k}")
     # one allocation for the four outputs of a slot (a view costs the host less than a tensor)
@@ -689,11 +699,12 @@ def moe_route_bwd(dweights, logits, ids, weights, *, renormalize=True, out=None)
     T, E = logits.shape
     _req(ids, "ids", torch.int32, 2)
     k = ids.shape[1]
+    _req_i32(max(E, k), "a side of logits and ids")
     if ids.shape[0] != T:
         raise ValueError(f"ids must be [{T}, k], got {tuple(ids.shape)}")
     _req_slots(weights, "weights", torch.float32, T, k)
     _req_slots(dweights, "dweights", torch.float32, T, k)
-    dev = _same_device(dweights, logits, ids, weights)
+    dev = _same_device(dweights, logits, ids, weights, out)
     out = _out(out, (T, E), logits.dtype, dev, "out")
     _launch(dev, "moe_route_bwd", _ptr(dweights), _ptr(logits), LOGIT_DTYPES[logits.dtype], _ptr(ids), _ptr(weights), T,
             E, k, bool(renormalize), _ptr(out))
@@ -707,6 +718,7 @@ def _slots(x, name, row_of_slot, rows, *others):
     _req(row_of_slot, "row_of_slot", torch.int32, 2)
     T, k = row_of_slot.shape
     R, H = x.shape
+    _req_i32(k, "k")
     if rows and R != T:
         raise ValueError(f"{name} must have the {T} rows of row_of_slot, got {tuple(x.shape)}")
     return _same_device(x, row_of_slot, *others), T, k, H
@@ -791,6 +803,7 @@ def quantize_mxfp4_weights(w, *, codes=None, scales=None):
             return r
     _req(w, "w", torch.bfloat16, 3)
     G, K, N = w.shape
+    _req_i32(G, "the number of experts")
     dev = w.device
     codes = _out(codes, (G, N, K // 2), torch.uint8, dev, "codes")
     scales = _out(scales, (G, K // 128, N, 4), torch.uint8, dev, "scales")
@@ -804,6 +817,7 @@ def _mxfp4_shapes(codes, scales):
     _req(scales, "scales", torch.uint8, 4)
     G, N, half = codes.shape
     K = 2 * half
+    _req_i32(G, "the number of experts")
     if tuple(scales.shape) != (G, K // 128, N, 4):
         raise ValueError(f"scales must be [{G}, {K // 128}, {N}, 4] for codes {tuple(codes.shape)}, "
                          f"got {tuple(scales.shape)}")
@@ -827,6 +841,7 @@ def dequantize_mxfp4(codes, scales, *, out=None):
 
 def _mxfp4_product(name, x, codes, scales, group_sizes, slot_of_row, topk, out, dev_status, workspace, swiglu):
     topk = int(topk)
+    _req_i32(topk, "topk")
     if out is None and workspace is None and dev_status is None:
         out = (_calls or _plain()).product(x, codes, scales, group_sizes, slot_of_row, topk, swiglu)
         if out is not None:
@@ -842,7 +857,13 @@ def _mxfp4_product(name, x, codes, scales, group_sizes, slot_of_row, topk, out, 
     if x.shape[1] != K or group_sizes.shape[0] != G:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)} codes {tuple(codes.shape)} "
                          f"group_sizes {tuple(group_sizes.shape)}")
-    dev = _same_device(x, codes, scales, group_sizes, slot_of_row)
+    if dev_status is not None:
+        _req(dev_status, "dev_status", torch.int32, getattr(dev_status, "ndim", 1))
+        if dev_status.numel() == 0:
+            raise ValueError("dev_status must hold a word")
+    if workspace is not None:
+        _req(workspace, "workspace", torch.uint8, 1)
+    dev = _same_device(x, codes, scales, group_sizes, slot_of_row, dev_status, workspace)
     out = _out(out, (M, N // 2 if swiglu else N), torch.bfloat16, dev, "out")
     _same_device(x, out)
     ws, need = _workspace(OP_MXFP4, T, K, N, G, dev, tile_m=0, workspace=workspace)

@@ -98,6 +98,12 @@ T* ptr(const Tensor& t) {
 }
 bool is(const Tensor& t, int64_t a, int64_t b) { return t.size(0) == a && t.size(1) == b; }
 
+// an integer argument; -1 (which no call takes) for one past 64 bits
+int64_t integer(PyObject* o) {
+  int past;
+  return PyLong_AsLongLongAndOverflow(o, &past);
+}
+
 PyObject* pack(std::initializer_list<Tensor> ts) {
   if (ts.size() == 1) return THPVariable_Wrap(*ts.begin());
   PyObject* out = PyTuple_New((Py_ssize_t)ts.size());
@@ -130,7 +136,8 @@ PyObject* pack(std::initializer_list<Tensor> ts) {
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   BEGIN(3)
   const Tensor* x = in.any(a[0], 2);
-  const int64_t k = PyLong_AsLongLong(a[1]);
+  const int64_t k = integer(a[1]);
+  const int renormalize = PyObject_IsTrue(a[2]);
   if (PyErr_Occurred()) return nullptr;
   PLAIN(in.ok && (x->scalar_type() == kF32 || x->scalar_type() == kBf16))
   const int64_t T = x->size(0), E = x->size(1);
@@ -141,7 +148,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor ws;
   if (need) ws = in.make({(int64_t)need}, kU8);
   PLAIN(lib.moe_route(x->data_ptr(), x->scalar_type() == kBf16 ? FP8GMM_BF16 : FP8GMM_F32, T, (int32_t)E, (int32_t)k,
-                      PyObject_IsTrue(a[2]), ptr<int32_t>(ids), ptr<float>(w), ptr<int32_t>(sizes),
+                      renormalize, ptr<int32_t>(ids), ptr<float>(w), ptr<int32_t>(sizes),
                       ptr<int32_t>(rows), ptr<int32_t>(slots), need ? ws.data_ptr() : nullptr, need,
                       in.stream()) == FP8GMM_OK)
   return pack({ids, w, sizes, rows, slots});
@@ -153,12 +160,14 @@ PyObject* route_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   BEGIN(5)
   const Tensor* x = in.any(a[1], 2);
   const Tensor *dw = in.get(a[0], kF32, 2), *ids = in.get(a[2], kI32, 2), *w = in.get(a[3], kF32, 2);
+  const int renormalize = PyObject_IsTrue(a[4]);
+  if (renormalize < 0) return nullptr;
   PLAIN(in.ok && (x->scalar_type() == kF32 || x->scalar_type() == kBf16))
   const int64_t T = x->size(0), E = x->size(1), k = ids->size(1);
   PLAIN(is(*ids, T, k) && is(*w, T, k) && is(*dw, T, k) && E < (1 << 30) && k < (1 << 30))
   const Tensor out = in.make({T, E}, x->scalar_type());
   PLAIN(lib.moe_route_bwd(ptr<float>(*dw), x->data_ptr(), x->scalar_type() == kBf16 ? FP8GMM_BF16 : FP8GMM_F32,
-                          ptr<int32_t>(*ids), ptr<float>(*w), T, (int32_t)E, (int32_t)k, PyObject_IsTrue(a[4]),
+                          ptr<int32_t>(*ids), ptr<float>(*w), T, (int32_t)E, (int32_t)k, renormalize,
                           out.data_ptr(), in.stream()) == FP8GMM_OK)
   return pack({out});
   END
@@ -259,7 +268,7 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor *x = in.get(a[0], kBf16, 2), *codes = in.get(a[1], kU8, 3), *scales = in.get(a[2], kU8, 4),
                *sizes = in.get(a[3], kI32, 1);
   const Tensor* slots = a[4] == Py_None ? nullptr : in.get(a[4], kI32, 1);
-  const int64_t topk = PyLong_AsLongLong(a[5]);
+  const int64_t topk = integer(a[5]);
   if (PyErr_Occurred()) return nullptr;
   PLAIN(in.ok && four_bit(*codes, *scales) && topk > 0 && topk < (1 << 30))
   const int64_t T = x->size(0), G = codes->size(0), N = codes->size(1), K = 2 * codes->size(2);

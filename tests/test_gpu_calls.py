@@ -132,3 +132,39 @@ def test_side_stream_and_other_threads():
     for t in threads:
         t.join()
     assert len(got) == 3 and all(torch.equal(o, want) for o in got)
+
+
+@pytest.mark.parametrize("way", ["extension", "python"])
+def test_refusals_of_either_way(way, monkeypatch):
+    """Flags without a truth, integers past 32 bits, scratch in host memory: errors, before any launch."""
+    import fp8_moe_grouped_amd as G
+    if way == "python":
+        monkeypatch.setattr(G, "_calls", Nothing())
+    logits = torch.zeros((4, 8), device="cuda")
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    w = torch.zeros((4, 2), device="cuda")
+    x = torch.zeros((4, 128), dtype=torch.bfloat16, device="cuda")
+    codes = torch.zeros((2, 128, 64), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((2, 1, 128, 4), dtype=torch.uint8, device="cuda")
+    sizes = torch.zeros(2, dtype=torch.int32, device="cuda")
+    two = torch.zeros(2)
+    for call in (lambda: G.moe_route(logits, 2, renormalize=two),
+                 lambda: G.moe_route_bwd(w, logits, ids, w, renormalize=two)):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            call()
+    for k in ((1 << 32) + 2, 1 << 70, -(1 << 70)):
+        with pytest.raises(ValueError):
+            G.moe_route(logits, k)
+    for k in ((1 << 32) + 1, 1 << 70):
+        with pytest.raises(ValueError, match="topk"):
+            G.gmm_mxfp4_fwd(x, codes, scales, sizes, topk=k)
+    for bad in (dict(dev_status=torch.zeros(1, dtype=torch.int32)), dict(dev_status=sizes[:0]),
+                dict(workspace=torch.zeros(1 << 16, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            G.gmm_mxfp4_fwd(x, codes, scales, sizes, **bad)
+    for bad in (dict(dev_status=sizes.long()), dict(workspace=torch.zeros(1 << 16, device="cuda"))):
+        with pytest.raises(TypeError):
+            G.gmm_mxfp4_fwd(x, codes, scales, sizes, **bad)
+    with pytest.raises(ValueError):
+        G.moe_route(logits, 2, workspace=torch.zeros(1 << 16, dtype=torch.uint8))
+    torch.cuda.synchronize()
