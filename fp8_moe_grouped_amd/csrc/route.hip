@@ -475,11 +475,12 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const float* __restrict_
     top = lanes_max<L>(top);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      x[i] = expert_of<L, C>(at, i) < E ? expf(x[i] - top) : 0.f;
+      const bool counts = expert_of<L, C>(at, i) < E && x[i] != -__builtin_inff();
+      x[i] = counts ? expf(x[i] - top) : 0.f;
       total += x[i];
     }
     total = lanes_sum<L>(total);
-    const bool some = top != -__builtin_inff();     // a token without experts has no gradient
+    const bool some = total != 0.f;                 // 0: a token without experts, no gradient (NaN with only NaN ones)
     const float share = inner / total;
 #pragma unroll
     for (int i = 0; i < V; ++i) d[i] = some ? d[i] - x[i] * share : 0.f;

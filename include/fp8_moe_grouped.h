@@ -364,8 +364,9 @@ int moe_ffn_fp8_bwd(const void* x, const void* h, const void* preact, const void
  *   renormalize: dlogits[t, ids[t,j]] = weights (dweights - s), 0 elsewhere
  *   otherwise:   dlogits[t, e] = [e = ids[t,j]] weights dweights - softmax(x[t])[e] * s
  * A choice with id -1 adds nothing and its dweights is not read; a token whose
- * logits are all -inf gets zeros.  Sums in f32, rounded once to the logits'
- * type.  logits may be NULL with renormalize.  dlogits [T, E].
+ * logits are all -inf gets zeros, one with a NaN or +inf among its softmax's
+ * logits NaN.  Sums in f32, rounded once to the logits' type.  logits may be NULL
+ * with renormalize.  dlogits [T, E].
  */
 int moe_route(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t renormalize, int32_t* ids,
               float* weights, int32_t* group_sizes, int32_t* row_of_slot, int32_t* slot_of_row, void* ws,

@@ -121,6 +121,30 @@ def test_route_gradient(T, E, k, dtype, renorm):
     assert bool(((got.double() - want).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [5, 64, 1024])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_gradient_of_nan_and_inf(renorm, E, dtype):
+    """A NaN or +inf among a softmax's logits makes its gradients NaN; a token without experts gets zeros."""
+    import fp8_moe_grouped_amd as G
+    x = torch.full((6, E), -INF)
+    x[0, 1] = math.nan                               # nothing but a NaN
+    x[1, 3], x[1, 4] = math.nan, 1.0
+    x[2, 0], x[2, 2] = INF, 1.0
+    x[3, 2] = 0.5                                    # one expert; row 4: none
+    x[5, :] = math.nan
+    x = x.to(dtype).cuda()
+    r = G.moe_route(x, 2, renormalize=renorm)
+    got = G.moe_route_bwd(torch.ones((6, 2), device="cuda"), x, r.ids, r.weights, renormalize=renorm).cpu().float()
+    ids = r.ids.cpu()
+    for t in (0, 1, 2, 5):
+        bad = torch.zeros(E, dtype=torch.bool)
+        bad[ids[t][ids[t] >= 0].long()] = True
+        assert torch.equal(torch.isnan(got[t]), bad if renorm else torch.ones_like(bad)), t
+        assert bool((got[t][~torch.isnan(got[t])] == 0).all())
+    assert bool((got[3:5] == 0).all())               # a weight of 1 does not move
+
+
 def test_route_gradient_by_differences():
     import fp8_moe_grouped_amd as G
     g = torch.Generator().manual_seed(3)
