@@ -12,6 +12,7 @@
 // four consecutive columns of one row.
 #include "common.hpp"
 #include "launch.hpp"
+#include "mxfp4_plan.hpp"
 
 #include <algorithm>
 #include <type_traits>
@@ -328,7 +329,7 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
   map.locate(group_sizes, G, M, mt, g, g0, g1, part);
   // this tile's share of the expert's units of 64 rows
   const int parts = (g1 - g0 + BM - 1) / BM, units = (g1 - g0 + 63) / 64;
-  const int u0 = units * part / parts, u1 = units * (part + 1) / parts;
+  const int u0 = first_unit(units, parts, part), u1 = first_unit(units, parts, part + 1);
   const int row0 = g0 + 64 * u0, rows = min(64 * (u1 - u0), g1 - row0);
 
   const int kw = K / 128, nk = kw;

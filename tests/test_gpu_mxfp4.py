@@ -342,3 +342,27 @@ def test_product_between(M, G_, K, N):
     """Sizes at which tiles of 32, 64 and 128 rows are taken."""
     test_product(M, 1, G_, K, N, False)
     test_product(M, 1, G_, K, N, N % 256 == 0)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("lead,M", [(0, 6_000_001), (3, 2 ** 24 - 1)])
+def test_product_millions_of_rows_an_expert(lead, M, swiglu):
+    """One expert's rows in the large tiles up to the most that a call takes.  Tokens are few: a token's first row
+    against the definition, its other rows against that one (the same sums wherever a row stands)."""
+    import fp8_moe_grouped_amd as G
+    T, K, N = 61, 1024, 256
+    g = torch.Generator().manual_seed(M)
+    x = activations(T, K, 1)
+    code, byte = weights(1 + lead, N, K, 2)
+    codes, scales = P.pack_weights(code, byte)
+    token = torch.randint(0, T, (M,), generator=g, dtype=torch.int32)
+    token[:lead + T] = torch.arange(lead + T, dtype=torch.int32) % T
+    sizes = [1] * lead + [M - lead]
+    f = G.gmm_silu_mxfp4 if swiglu else G.gmm_mxfp4_fwd
+    out = f(x.cuda(), codes.cuda(), scales.cuda(), torch.tensor(sizes, dtype=torch.int32).cuda(), slot_of_row=token.cuda())
+    check(out[:lead + T], *product(x, code, byte, [1] * lead + [T], token[:lead + T].long()), K, swiglu)
+    first = torch.empty((T, out.shape[1]), dtype=out.dtype, device="cuda")
+    first[token[lead:lead + T].cuda().long()] = out[lead:lead + T]
+    for at in range(lead, M, 1 << 21):
+        rows = slice(at, min(at + (1 << 21), M))
+        assert torch.equal(out[rows], first[token[rows].cuda().long()]), at
