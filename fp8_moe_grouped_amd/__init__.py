@@ -180,7 +180,7 @@ def _req(t, name, dtype, ndim):
 
 def _req_i32(v, name):
     """ctypes would keep the low 32 bits."""
-    if v >= 1 << 31:
+    if not -(1 << 31) <= v < 1 << 31:
         raise ValueError(f"{name} must fit 32 bits, got {v}")
 
 

@@ -114,6 +114,16 @@ def test_binding_refusals():
         G.moe_route([[0.0]], 1)
 
 
+@pytest.mark.parametrize("topk", [(1 << 32) + 1, 1 - (1 << 32), -(1 << 31) - 1, -(1 << 70)])
+def test_binding_refuses_topk_past_32_bits(topk):
+    """On either side: ctypes would keep the low 32 bits, 1 of 1 - 2^32."""
+    _lib()
+    x = torch.zeros((4, 128), dtype=torch.bfloat16)
+    codes, scales = torch.zeros((2, 128, 64), dtype=torch.uint8), torch.zeros((2, 1, 128, 4), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="topk"):
+        G.gmm_mxfp4_fwd(x, codes, scales, torch.zeros(2, dtype=torch.int32), topk=topk)
+
+
 # --------------------------------------------------------------------------- the plain definitions
 
 def test_plain_route_by_hand():
