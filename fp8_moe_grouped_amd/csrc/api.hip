@@ -6,7 +6,7 @@
 #include <atomic>
 
 #include "../../include/fp8_moe_grouped.h"
-#include "launch.hpp"
+#include "moe_launch.hpp"
 
 using namespace fp8gmm;
 

@@ -10,8 +10,8 @@
 // accumulates in f32.  A lane's operand is 32 consecutive k of one row, which is one
 // block with one scale byte.  The weight is the first operand, so a lane ends with
 // four consecutive columns of one row.
-#include "common.hpp"
-#include "launch.hpp"
+#include "moe_common.hpp"
+#include "moe_launch.hpp"
 #include "mxfp4_plan.hpp"
 
 #include <algorithm>

@@ -14,8 +14,8 @@
 // Codes [.., rows, K/2] hold the even k of a pair in the low half byte; scales
 // [K/128, rows, 4] of weights put the four blocks of 128 k of a row in one word,
 // which is what a lane of the scaled matrix instructions takes.
-#include "common.hpp"
-#include "launch.hpp"
+#include "moe_common.hpp"
+#include "moe_launch.hpp"
 
 namespace fp8gmm {
 namespace {

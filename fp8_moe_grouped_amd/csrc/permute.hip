@@ -15,8 +15,8 @@
 // the k times larger side, which is not read again before it has left the caches:
 // 4096 x 7168, k = 8: permute 91 us (5.8 TB/s; 106 without the policy), combine 90
 // (5.9 TB/s; 104), its gradient 188 (5.3 TB/s; 200).
-#include "common.hpp"
-#include "launch.hpp"
+#include "moe_common.hpp"
+#include "moe_launch.hpp"
 
 #include <type_traits>
 

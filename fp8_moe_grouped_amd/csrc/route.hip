@@ -26,8 +26,8 @@
 // without conflicts, and the count before the increment is the slot's rank among
 // the wave's slots of that expert.  Waves of a block and then blocks are joined by
 // prefix sums of the histograms: the order of slots never depends on timing.
-#include "common.hpp"
-#include "launch.hpp"
+#include "moe_common.hpp"
+#include "moe_launch.hpp"
 
 #include <algorithm>
 #include <type_traits>
