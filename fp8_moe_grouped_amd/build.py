@@ -68,10 +68,10 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     with ThreadPoolExecutor(jobs) as ex:
         calls = ex.submit(build_calls)
         logs = list(ex.map(compile_one, zip(srcs, objs)))
-        logs.append(calls.result())
-    tmp = LIB + ".tmp"
-    logs.append(_run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]))
-    os.replace(tmp, LIB)
+        tmp = LIB + ".tmp"
+        logs.append(_run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]))
+        os.replace(tmp, LIB)
+        logs.append(calls.result())     # last: the library stands without the extension, whose failure is raised here
     if verbose:
         for l in logs:
             if l.strip():
