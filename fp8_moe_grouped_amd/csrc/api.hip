@@ -564,7 +564,8 @@ static int mxfp4_common(const void* x, const uint8_t* codes, const uint8_t* scal
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   uint8_t* aq = static_cast<uint8_t*>(ws);
   uint8_t* as = aq + align_up((size_t)(T + 1) * (K / 2));
-  if (launch_quant_rows_mxfp4(static_cast<const uint16_t*>(x), (int)T, (int)K, aq, as, s) != hipSuccess ||
+  const int32_t* valid = slot_of_row ? nullptr : group_sizes;   // x is the ragged buffer where there is no map
+  if (launch_quant_rows_mxfp4(static_cast<const uint16_t*>(x), valid, G, (int)T, (int)K, aq, as, s) != hipSuccess ||
       launch_gmm_mxfp4(aq, as, codes, scale, group_sizes, slot_of_row, topk, (int)T, G, (int)M, (int)K, (int)N, swiglu,
                        static_cast<uint16_t*>(out), dev_status, s) != hipSuccess)
     return FP8GMM_ERR_HIP;

@@ -26,9 +26,10 @@ hipError_t launch_combine(const uint16_t* y, const int* row_of_slot, const float
 hipError_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y, const int* row_of_slot, const float* weights,
                               int T, int k, int R, int H, uint16_t* dy, float* dweights, hipStream_t stream);
 
-// MXFP4: quantizers (the activations' codes and scales have T + 1 rows, the last of zeros), values, product.
-hipError_t launch_quant_rows_mxfp4(const uint16_t* x, int T, int K, uint8_t* codes, uint8_t* scales,
-                                   hipStream_t stream);
+// MXFP4: quantizers, values, product.  launch_quant_rows_mxfp4: with group_sizes, the valid rows of the ragged
+// buffer x [T, K]; without, all T tokens and a row of zeros at T (codes and scales have T + 1 rows).
+hipError_t launch_quant_rows_mxfp4(const uint16_t* x, const int* group_sizes, int G, int T, int K, uint8_t* codes,
+                                   uint8_t* scales, hipStream_t stream);
 hipError_t launch_quant_weights_mxfp4(const uint16_t* w, int G, int K, int N, uint8_t* codes, uint8_t* scales,
                                       hipStream_t stream);
 hipError_t launch_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int G, int N, int K, uint16_t* out,

@@ -42,15 +42,20 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
 }
 
-// Activations: one 16-byte chunk (8 values) per lane, four lanes a block.  Row T
-// is written as zeros: the product reads it for rows without a token.  Scale rows
+// Activations: one 16-byte chunk (8 values) per lane, four lanes a block of 32.  Scale rows
 // are padded to 16 bytes.  Bound by HBM: 5000 x 7168 in 18 us, 91 MB at 5 TB/s.
-__global__ __launch_bounds__(256) void quant_rows_mxfp4_kernel(const v4i* __restrict__ x, int T, int nch,
-                                                              uint32_t* __restrict__ codes,
+// ROWS: x is the ragged buffer itself, and rows past the valid prefix are neither read nor
+// written (the sizes cost 0.3 to 0.7 us of a product's call; 19661 valid rows of 32768 in a
+// 2048 x 7168 product 261 -> 257 us).  Otherwise x holds tokens, all of which are quantized, and row T is written as
+// zeros: the product reads it for rows without a token.
+template <bool ROWS>
+__global__ __launch_bounds__(256) void quant_rows_mxfp4_kernel(const v4i* __restrict__ x,
+                                                              const int* __restrict__ group_sizes, int G, int T,
+                                                              int nch, uint32_t* __restrict__ codes,
                                                               uint8_t* __restrict__ scales) {
   const long long i = linear_block() * 256 + threadIdx.x;
-  const long long end = (long long)T * nch;
-  if (i >= end + nch) return;
+  const long long end = (long long)(ROWS ? valid_rows(group_sizes, G, T) : T) * nch;
+  if (i >= (ROWS ? end : end + nch)) return;
   const v4i v = i < end ? x[i] : (v4i){0, 0, 0, 0};
   uint32_t am = 0;
 #pragma unroll
@@ -155,12 +160,18 @@ __global__ __launch_bounds__(256) void dequant_mxfp4_kernel(const uint32_t* __re
 
 }  // namespace
 
-hipError_t launch_quant_rows_mxfp4(const uint16_t* x, int T, int K, uint8_t* codes, uint8_t* scales,
-                                   hipStream_t stream) {
+hipError_t launch_quant_rows_mxfp4(const uint16_t* x, const int* group_sizes, int G, int T, int K, uint8_t* codes,
+                                   uint8_t* scales, hipStream_t stream) {
   const int nch = K / 8;
-  const long long blocks = (((long long)T + 1) * nch + 255) / 256;
-  hipLaunchKernelGGL(quant_rows_mxfp4_kernel, linear_grid(blocks), dim3(256), 0, stream,
-                     reinterpret_cast<const v4i*>(x), T, nch, reinterpret_cast<uint32_t*>(codes), scales);
+  const long long rows = group_sizes ? T : (long long)T + 1;
+  const dim3 grid = linear_grid((rows * nch + 255) / 256);
+  const v4i* xv = reinterpret_cast<const v4i*>(x);
+  uint32_t* cv = reinterpret_cast<uint32_t*>(codes);
+  if (group_sizes)
+    hipLaunchKernelGGL(quant_rows_mxfp4_kernel<true>, grid, dim3(256), 0, stream, xv, group_sizes, G, T, nch, cv, scales);
+  else
+    hipLaunchKernelGGL(quant_rows_mxfp4_kernel<false>, grid, dim3(256), 0, stream, xv, group_sizes, G, T, nch, cv,
+                       scales);
   return hipGetLastError();
 }
 

@@ -420,7 +420,8 @@ int moe_combine_bwd(const void* dout, const void* y, const int32_t* row_of_slot,
  * x bf16 [T, K], or row r itself when slot_of_row is NULL (then T = M).  With
  * q(.) the MXFP4 values of x's blocks and w the weights' values:
  *   out[r, n] = bf16( sum_k q(x)[token, k] * w[g, n, k] )      f32 accumulation
- * out bf16 [M, N]; rows >= sum(group_sizes) are neither read nor written.  A
+ * out bf16 [M, N]; rows >= sum(group_sizes) are neither read nor written (rows of
+ * x, out and slot_of_row; with a map x holds tokens, all of which are quantized).  A
  * slot outside [0, T*topk) gives a row of zeros.
  * gmm_silu_mxfp4: N = 2I columns [gate | up]; out bf16 [M, I] =
  *   bf16( silu(y[r, i]) * y[r, I + i] ) of the f32 products y.  I % 128 == 0.

@@ -366,3 +366,22 @@ def test_product_millions_of_rows_an_expert(lead, M, swiglu):
     for at in range(lead, M, 1 << 21):
         rows = slice(at, min(at + (1 << 21), M))
         assert torch.equal(out[rows], first[token[rows].cuda().long()]), at
+
+
+@pytest.mark.parametrize("M,valid,G_,K,N", [(100, 60, 3, 384, 256), (7, 0, 2, 128, 128), (5000, 3001, 70, 1024, 512), (40, 40, 4, 256, 128)])
+def test_product_leaves_stale_rows_alone(M, valid, G_, K, N):
+    """Without a map the rows past the valid prefix are neither quantized into the workspace nor in the result."""
+    import fp8_moe_grouped_amd as G
+    x = activations(M, K, 1)
+    x[valid:] = math.nan
+    code, byte = weights(G_, N, K, 2)
+    codes, scales = P.pack_weights(code, byte)
+    sizes = sizes_of(valid, G_, 5)
+    ws = torch.full((G.workspace_bytes(G.OP_MXFP4, M, K, N, G_),), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    G.gmm_mxfp4_fwd(x.cuda(), codes.cuda(), scales.cuda(), sizes.cuda(), out=out, workspace=ws)
+    assert bool((out[valid:] == 7.0).all())
+    held = ws[:M * K // 2].view(M, K // 2)           # the rows' codes come first
+    assert bool((held[valid:] == 0xA5).all())
+    if valid:
+        check(out[:valid], *product(x, code, byte, sizes.tolist(), torch.arange(M)), K, False)
