@@ -101,4 +101,11 @@ __device__ __forceinline__ int wave_scan_dpp(int v) {
   return dpp_add<0x143, 0xC>(v);                    // row_bcast 31 into rows 2 and 3
 }
 
+// valid_rows of common.hpp without LDS.  A lane's sum stays at or below M < 2^24, the wave's below 2^30.
+__device__ __forceinline__ int valid_rows_dpp(const int* __restrict__ group_sizes, int G, int M) {
+  int s = 0;
+  for (int g = (int)(threadIdx.x & 63); g < G; g += 64) s = min(s + min(max(group_sizes[g], 0), M), M);
+  return min(__builtin_amdgcn_readlane(wave_scan_dpp(s), 63), M);
+}
+
 }  // namespace fp8gmm

@@ -45,8 +45,8 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
 // Activations: one 16-byte chunk (8 values) per lane, four lanes a block of 32.  Scale rows
 // are padded to 16 bytes.  Bound by HBM: 5000 x 7168 in 18 us, 91 MB at 5 TB/s.
 // ROWS: x is the ragged buffer itself, and rows past the valid prefix are neither read nor
-// written (the sizes cost 0.3 to 0.7 us of a product's call; 19661 valid rows of 32768 in a
-// 2048 x 7168 product 261 -> 257 us).  Otherwise x holds tokens, all of which are quantized, and row T is written as
+// written (the sizes cost 0.1 to 0.5 us of a product's call; 19661 valid rows of 32768 in a
+// 2048 x 7168 product 268 -> 262 us).  Otherwise x holds tokens, all of which are quantized, and row T is written as
 // zeros: the product reads it for rows without a token.
 template <bool ROWS>
 __global__ __launch_bounds__(256) void quant_rows_mxfp4_kernel(const v4i* __restrict__ x,
@@ -54,7 +54,7 @@ __global__ __launch_bounds__(256) void quant_rows_mxfp4_kernel(const v4i* __rest
                                                               int nch, uint32_t* __restrict__ codes,
                                                               uint8_t* __restrict__ scales) {
   const long long i = linear_block() * 256 + threadIdx.x;
-  const long long end = (long long)(ROWS ? valid_rows(group_sizes, G, T) : T) * nch;
+  const long long end = (long long)(ROWS ? valid_rows_dpp(group_sizes, G, T) : T) * nch;
   if (i >= (ROWS ? end : end + nch)) return;
   const v4i v = i < end ? x[i] : (v4i){0, 0, 0, 0};
   uint32_t am = 0;
