@@ -549,24 +549,13 @@ static hipError_t launch_stream(const uint8_t* aq, const uint8_t* ascale, const 
 hipError_t launch_gmm_mxfp4(const uint8_t* aq, const uint8_t* ascale, const uint8_t* codes, const uint8_t* wscale,
                             const int* group_sizes, const int* slot_of_row, int topk, int T, int G, int M, int K,
                             int N, bool swiglu, uint16_t* out, int* status, hipStream_t stream) {
-  // The sizes of the groups are not known here: about M / BM + G / 2 row tiles.  Of 60 shapes measured (us with MI = 1,
-  // 2, 4 and the large tiles; the count of large tiles in brackets):
-  //   7168 x 4096, 32 experts: 4 rows an expert 70 / 74 / 88 / 93, 16 rows 86 / 83 / 92 / 97, 64 rows 172 / 146 / 131 / 133
-  //   few tiles: 697 rows, 4 experts, 4352 x 1792 (42) 21 / 17 / 21 / 33; 1144 rows, 5 experts, 1536 x 3328 (104)
-  //   15 / 16 / 14 / 19; 3092 rows, 5 experts, 3840 x 1536 (90) 43 / 37 / 34 / 35; 2746 rows, 3 experts, 6528 x 2560 (120)
-  //   107 / 77 / 58 / 55; 7143 rows, 8 experts, 5504 x 3584 (448) 315 / 222 / 169 / 103
-  //   two pairs are over before a large tile's loads and stores overlap anything: 5412 rows, 7 experts, 384 x 3840 (375)
-  //   34 / 27 / 25 / 27
-  auto blocks = [&](long long bm, long long bn) { return (M / bm + (G + 1) / 2) * ((N + bn - 1) / bn); };
-  const bool many = M >= 64 * (long long)G;
-  // the large tiles have 32-bit offsets to the rows
-  const bool tile = many && K >= 1024 && blocks(256, 256) >= 120 && (long long)(T + 1) * (K / 2) < (1LL << 32);
 #define STREAM(MI)                                                                                                  \
   launch_stream<MI>(aq, ascale, codes, wscale, group_sizes, slot_of_row, topk, T, G, M, K, N, swiglu, out, status, \
                     stream)
-  if (!tile && many && blocks(128, 128) >= 200) return STREAM(4);
-  if (!tile && M > 24 * (long long)G && blocks(64, 128) >= 100) return STREAM(2);
-  if (!tile) return STREAM(1);
+  const int rows = mxfp4_tile_rows(T, G, M, K, N);
+  if (rows == 32) return STREAM(1);
+  if (rows == 64) return STREAM(2);
+  if (rows == 128) return STREAM(4);
 #undef STREAM
   const long long tiles = std::min<long long>(M, ((long long)M + BM - 1) / BM + G);
   if (swiglu)

@@ -385,3 +385,63 @@ def test_product_leaves_stale_rows_alone(M, valid, G_, K, N):
     assert bool((held[valid:] == 0xA5).all())
     if valid:
         check(out[:valid], *product(x, code, byte, sizes.tolist(), torch.arange(M)), K, False)
+
+
+# 120 large tiles and more, at the K, row counts and odd numbers of experts where few columns give the stream kernel
+# the work; tests/test_mxfp4_plan.py holds these shapes to the kernel that they are meant for
+LARGE_TILES = [(700, 1, 3, 1024, 7680), (333, 3, 2, 1152, 8192), (500, 2, 5, 1280, 5120), (64, 1, 1, 1408, 30720),
+               (900, 1, 4, 2176, 6144), (2600, 1, 7, 1664, 2304)]
+BETWEEN = [(3092, 5, 640, 1536), (1144, 5, 512, 3328), (697, 4, 512, 1792), (70, 4, 256, 512)]
+
+
+@pytest.mark.parametrize("T,k,G_,K,N", LARGE_TILES)
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_product_in_large_tiles(T, k, G_, K, N, swiglu):
+    test_product(T, k, G_, K, N, swiglu)
+
+
+@pytest.mark.parametrize("M,G_,K,N", BETWEEN)
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_product_in_tiles_of_32_to_128_rows(M, G_, K, N, swiglu):
+    test_product(M, 1, G_, K, N, swiglu)
+
+
+@pytest.mark.parametrize("M,K,N", [(300, 1024, 15488), (700, 1152, 7552), (900, 2048, 7808)])
+def test_large_tiles_with_columns_off_the_tile(M, K, N):
+    test_product_columns_off_the_tile(M, K, N)
+
+
+@pytest.mark.parametrize("T", [524_286, 524_287, 524_300])
+def test_product_at_four_gigabytes_of_tokens(T):
+    """Enough columns for the large tiles: quantized tokens just below 4 GiB go through them, from there on the stream
+    kernel takes over.  Tokens at both ends, the last ones and none; 240 copies of 128 columns."""
+    import fp8_moe_grouped_amd as G
+    K, N, M = 16384, 30720, 64
+    at = torch.cat((torch.arange(30), torch.tensor([-1, T]), T - 32 + torch.arange(32)))
+    few = activations(M, K, 1)
+    few[30:32] = 0                                   # the slots without a token
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device="cuda")
+    named = (at >= 0) & (at < T)
+    x[at[named].cuda()] = few[named].cuda()
+    code, byte = weights(1, 128, K, 2)
+    codes, scales = P.pack_weights(code, byte)
+    out = G.gmm_mxfp4_fwd(x, codes.repeat(1, N // 128, 1).cuda(), scales.repeat(1, 1, N // 128, 1).cuda(),
+                          torch.tensor([M], dtype=torch.int32).cuda(), slot_of_row=at.int().cuda())
+    del x
+    y, mag = product(few, code, byte, [M], torch.arange(M))
+    check(out, y.repeat(1, N // 128), mag.repeat(1, N // 128), K, False)
+
+
+def test_product_of_zero_codes_by_nan_scales():
+    """A scale byte of 255 makes values of zero codes NaN too, of weights and of activations; in each kernel."""
+    import fp8_moe_grouped_amd as G
+    for M, K, N in ((20, 256, 256), (300, 1024, 15360)):
+        code, byte = torch.zeros((1, N, K), dtype=torch.uint8), torch.full((1, N, K // 32), 120, dtype=torch.uint8)
+        byte[0, 7, K // 32 - 1] = 255
+        codes, scales = P.pack_weights(code, byte)
+        x = torch.zeros((M, K), dtype=torch.bfloat16)
+        x[11, 33] = math.inf
+        out = G.gmm_mxfp4_fwd(x.cuda(), codes.cuda(), scales.cuda(), torch.tensor([M], dtype=torch.int32).cuda()).cpu()
+        want = torch.zeros((M, N), dtype=torch.bool)
+        want[11], want[:, 7] = True, True
+        assert torch.equal(torch.isnan(out), want) and bool((out[~want] == 0).all())
