@@ -421,13 +421,9 @@ void gmm_mxfp4_tile_kernel(const uint8_t* __restrict__ aq, const uint8_t* __rest
     copy_scales(0, true, false);
 #pragma unroll
     for (int q = 0; q < 2 * MI; ++q) copy(0, 0, q);
-    if (nk > 2) {
 #pragma unroll
-      for (int q = 0; q < kLoads; ++q) copy(1, 1, q);
-      wait_vmem_lds<kLoads>();
-    } else {
-      wait_vmem_lds<0>();
-    }
+    for (int q = 0; q < kLoads; ++q) copy(1, 1, q);  // K >= 1024 here: four pairs or more
+    wait_vmem_lds<kLoads>();
     barrier_only();
 #pragma unroll
     for (int q = 0; q < kReads; ++q) read(std::integral_constant<int, 0>{}, 0, q);
