@@ -25,7 +25,8 @@ namespace {
 // The experts' rows and tiles of BM rows, 64 experts at a time, one a lane.  Every
 // wave finds its own tile in registers: the LDS table of build_group_table (one
 // wave's shuffles, a barrier, a binary search) took 9400 cycles from the block's
-// start to its tile's first address, this takes 3900.
+// start to its tile's first address, this takes 3900 with up to 64 experts; with more,
+// locate walks the sizes again.
 template <int BM>
 struct TileMap {
   int start, end, first, tiles;                     // the lane's expert: rows, first tile, tiles
@@ -116,8 +117,8 @@ __device__ __forceinline__ float silu_mul(float gate, float up) {   // hardware 
 // Bound by the weights' bytes: a block streams 128 columns of one expert (SwiGLU: 64
 // gate and the matching 64 up) past up to 32 * MI of its rows.  Copies to LDS, a pair
 // a row (contiguous lines, streaming policy for the weights: 7.1 TB/s alone, where
-// operand loads of 16 rows x 64 bytes reach 6.1), into a ring of three slots: two
-// pairs in flight a block, two blocks a CU.  A wave multiplies 32 columns, SwiGLU 16
+// operand loads of 16 rows x 64 bytes reach 6.1), into a ring of three slots (two
+// with 128 rows, so that two blocks still share a CU).  A wave multiplies 32 columns, SwiGLU 16
 // gate and their 16 up in one fragment, so that a lane ends with both.
 template <int MI>
 constexpr int kRing = MI <= 2 ? 3 : 2;

@@ -43,6 +43,8 @@ constexpr int kTokensPerBlock = kWaves * kTokensPerWave;   // per chunk
 constexpr int kMaxBlocks = 512;                     // longer batches give a block several chunks
 constexpr int kByteChunks = 3;                      // 192 tokens
 static_assert(kByteChunks * kTokensPerBlock < 256, "a block's count fits a byte");
+// A wave of route_place_kernel joins its share of the rows, up to 32 of 512, or a row a lane where a row is one chunk.
+static_assert(64 * kByteChunks * kTokensPerBlock < 65536, "a wave's sums of bytes fit 16 bits");
 __host__ __device__ constexpr int hist_row(int E) { return (E + 15) & ~15; }
 
 // The wave's lanes see each other's LDS writes past this point: LDS serves a wave in order, and
@@ -346,8 +348,7 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(const int* __rest
   // chunk_lanes: the chunks of a row, rounded up to a power of two
   const int g = tid & (chunk_lanes - 1), seg = tid / chunk_lanes, segs = kThreads / chunk_lanes;
   const bool here = g * C < Ep;
-  // bytes: counts 0 and 2 of a word in acc[2j] and 1 and 3 in acc[2j + 1], 16 bits each (a wave adds at most
-  // 32 rows of 192); 16 bits: one count each
+  // bytes: counts 0 and 2 of a word in acc[2j] and 1 and 3 in acc[2j + 1], 16 bits each; 16 bits: one count each
   uint32_t acc[2][8] = {};                          // rows before b, all rows
   if (here)
     for (int r0 = seg; r0 < nb; r0 += 4 * segs) {
