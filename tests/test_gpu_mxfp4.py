@@ -389,7 +389,7 @@ def test_product_leaves_stale_rows_alone(M, valid, G_, K, N):
 
 # 120 large tiles and more, at the K, row counts and odd numbers of experts where few columns give the stream kernel
 # the work; tests/test_mxfp4_plan.py holds these shapes to the kernel that they are meant for
-LARGE_TILES = [(700, 1, 3, 1024, 7680), (333, 3, 2, 1152, 8192), (500, 2, 5, 1280, 5120), (64, 1, 1, 1408, 30720),
+LARGE_TILES = [(700, 1, 3, 1024, 7680), (333, 3, 2, 1152, 8192), (500, 2, 5, 1280, 5120), (64, 1, 1, 1408, 30976),
                (900, 1, 4, 2176, 6144), (2600, 1, 7, 1664, 2304)]
 BETWEEN = [(3092, 5, 640, 1536), (1144, 5, 512, 3328), (697, 4, 512, 1792), (70, 4, 256, 512)]
 
@@ -414,9 +414,9 @@ def test_large_tiles_with_columns_off_the_tile(M, K, N):
 @pytest.mark.parametrize("T", [524_286, 524_287, 524_300])
 def test_product_at_four_gigabytes_of_tokens(T):
     """Enough columns for the large tiles: quantized tokens just below 4 GiB go through them, from there on the stream
-    kernel takes over.  Tokens at both ends, the last ones and none; 240 copies of 128 columns."""
+    kernel takes over.  Tokens at both ends, the last ones and none; 242 copies of 128 columns."""
     import fp8_moe_grouped_amd as G
-    K, N, M = 16384, 30720, 64
+    K, N, M = 16384, 30976, 64
     at = torch.cat((torch.arange(30), torch.tensor([-1, T]), T - 32 + torch.arange(32)))
     few = activations(M, K, 1)
     few[30:32] = 0                                   # the slots without a token

@@ -36,7 +36,7 @@ def test_row_offsets_of_the_large_tiles_fit_32_bits(check):
         T = 2 ** 32 // (K // 2) - 2                  # the last row of zeros included, the most below 4 GiB
         T += ((T + 2) * (K // 2) < 2 ** 32)
         assert (T + 1) * (K // 2) < 2 ** 32 <= (T + 2) * (K // 2)
-        assert tile_rows(check, T, 1, 64, K, 30720) == 256 and tile_rows(check, T + 1, 1, 64, K, 30720) == 128
+        assert tile_rows(check, T, 1, 64, K, 30976) == 256 and tile_rows(check, T + 1, 1, 64, K, 30976) == 128
     assert tile_rows(check, 2 ** 24 - 1, 1, 2 ** 24 - 1, 1024, 65536) == 128
 
 
