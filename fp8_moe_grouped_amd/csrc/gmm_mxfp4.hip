@@ -290,7 +290,7 @@ __global__ __launch_bounds__(256, 2) void gmm_mxfp4_stream_kernel(
 // count (MI fragments of 32 rows): at K = 7168 a loop of 84000 cycles for 256 rows
 // and 66000, the copies' time, for 64.
 //
-// 20000 x 7168 x 4096 over 32 skewed experts: 350 to 380 us with the quantizer, 3.1
+// 20000 x 7168 x 4096 over 32 skewed experts: 360 to 375 us with the quantizer, 3.1
 // to 3.3 PFLOP/s.  A stage takes 1475 cycles at a clock that the power limit holds
 // near 1.9 GHz; its matrix instructions alone take 1140, its copies alone 1040 when
 // all lines are in L2.

@@ -20,7 +20,7 @@
 // A lane sorts its keys once with a network; k times the largest head over the
 // lanes is taken and its lane's list moves up.  (Searching all keys k times, one
 // token a wave, was bound by its instructions: 18 us for 16384 x 256 bf16, k = 8,
-// against 7.3 us now, of which 2 us are the bytes.)
+// against 7.2 us now, of which 2 us are the bytes.)
 //
 // A token's choices are distinct, so a wave counts them into its LDS histogram
 // without conflicts, and the count before the increment is the slot's rank among
@@ -324,7 +324,7 @@ __global__ __launch_bounds__(kThreads) void route_topk_kernel(const TX* __restri
 // blocks, plus the rank within the block that route_topk_kernel left in row_of_slot.
 // Every block sums the whole histogram instead of a launch between that would scan
 // it: 64 KB at 16384 x 256, from L2, in bytes and two counts an addition (as 16 bits,
-// one count an addition and LDS atomics, 6.5 us; now 5.8).
+// one count an addition and LDS atomics, at least 6.5 us in a kernel trace; now 6.0).
 //
 // Thread (segment, chunk of 16 bytes) adds the rows segment, segment + segments, ..
 template <typename H>
