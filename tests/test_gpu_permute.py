@@ -184,3 +184,22 @@ def test_more_threads_than_a_launch_dimension():
     G.moe_combine(small, rows, out=big)
     assert torch.equal(big[at], small)
     assert not bool(big[T - 5:T - 3].any()) and not bool(big[2:100].any())
+
+
+def test_permuted_codes_feed_the_forward():
+    """moe_permute_fp8's codes and scales in gmm_silu_fp8_q and gmm_fp8_fwd_q: the same bits as the bf16 rows through
+    the calls that quantize."""
+    import fp8_moe_grouped_amd as G
+    T, k, E, H, N = 77, 3, 5, 384, 512
+    g = torch.Generator().manual_seed(2)
+    x = normal((T, H), 1).cuda()
+    r = G.moe_route(torch.randn((T, E), generator=g).masked_fill(torch.rand((T, E), generator=g) < 0.5, -math.inf).cuda(), k)
+    n = int(r.group_sizes.sum())
+    assert 0 < n < T * k                             # some choices are masked
+    codes = torch.randn((E, H, N), generator=g).clamp(-4, 4).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    scale = (0.01 + torch.rand((E, N), generator=g)).cuda()
+    aq, ascale = G.moe_permute_fp8(x, r.row_of_slot)
+    xs = G.moe_permute(x, r.row_of_slot)
+    for from_codes, from_rows in ((G.gmm_silu_fp8_q, G.gmm_silu_fp8), (G.gmm_fp8_fwd_q, G.gmm_fp8_fwd)):
+        a, b = from_codes(aq, ascale, codes, scale, r.group_sizes), from_rows(xs, codes, scale, r.group_sizes)
+        assert torch.equal(a[:n], b[:n]) and bool(torch.isfinite(a[:n]).all())
