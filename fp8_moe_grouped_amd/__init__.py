@@ -8,8 +8,8 @@ point of the same name on the current HIP stream.  Every step of the
 computation runs in the library's HIP kernels; there is no fallback.  If the
 shared library is missing the first call raises.
 
-The calls around the products (routing, dispatch, combine, 4-bit) first hand
-their arguments to a small extension (csrc/calls.cpp), which makes the same C
+The calls around the products (routing, balance losses, dispatch, combine, weight
+quantizers, AdamW, 4-bit) first hand their arguments to a small extension (csrc/calls.cpp), which makes the same C
 call without the interpreter's checks where the arguments are the plain ones;
 it answers None otherwise, and the function here checks, calls and reports.
 
@@ -33,11 +33,12 @@ HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "fp8_moe_grouped.h
 
 OK = 0
 ERR_NULL, ERR_SHAPE, ERR_UNSUPPORTED, ERR_ALIGN, ERR_WORKSPACE, ERR_HIP, ERR_SCRATCH = -1, -2, -3, -4, -5, -6, -7
+ERR_OVERLAP = -8
 NOALLOC_SCRATCH_BYTES = 32 << 20
 DEV_SUM_CLAMPED, DEV_NEGATIVE_SIZE = 1, 2
 E4M3, E5M2 = 0, 1
 (OP_FWD, OP_SILU, OP_DLHS, OP_TGMM, OP_BF16_FWD, OP_BF16_DLHS, OP_FFN_FWD, OP_FFN_BWD, OP_FWD_VARIANT,
- OP_TGMM_DENSE, OP_ROUTE, OP_MXFP4) = range(12)
+ OP_TGMM_DENSE, OP_ROUTE, OP_MXFP4, OP_BALANCE) = range(13)
 LHS_SCALE_BF16, ACC_BF16, RHS_SCALE_FIRST = 1, 2, 4
 GRAD_DTYPES = {"e4m3": E4M3, "e5m2": E5M2}
 F32, BF16 = 0, 1
@@ -55,6 +56,7 @@ class Fp8GmmError(RuntimeError):
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
+_U64 = ctypes.c_uint64
 _SZ = ctypes.c_size_t
 
 _SIGNATURES = {
@@ -82,6 +84,11 @@ _SIGNATURES = {
     "moe_permute_fp8": [_P, _P, _I64, _I32, _I64, _I64, _P, _P, _P],
     "moe_combine": [_P, _P, _P, _I64, _I32, _I64, _I64, _P, _P],
     "moe_combine_bwd": [_P, _P, _P, _P, _I64, _I32, _I64, _I64, _P, _P, _P],
+    "moe_balance_loss": [_P, _I32, _P, _I64, _I32, _I32, _P, _P, _P, _P, _P, _SZ, _P],
+    "moe_balance_loss_bwd": [_P, _P, _I32, _P, _P, _I64, _I32, _P, _P, _P],
+    "adamw_step": [_I32, _P, _P, _I32, _P, _I32, _P, _P, _P, _P],
+    "adamw_step_8bit": [_I32, _P, _P, _I32, _P, _I32, _P, _P, _P, _P, _U64, _P, _P],
+    "quantize_fp8_weights": [_P, _I32, _I64, _I64, _I32, _P, _P, _P],
     "quantize_mxfp4_weights": [_P, _I64, _I64, _I32, _P, _P, _P],
     "dequantize_mxfp4": [_P, _P, _I64, _I64, _I32, _P, _P],
     "gmm_mxfp4_fwd": [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, _I32, _P, _P, _SZ, _P, _P],
@@ -790,6 +797,223 @@ def moe_combine_bwd(dout, y, row_of_slot, weights, *, dy=None, dweights=None):
     _launch(dev, "moe_combine_bwd", _ptr(dout), _ptr(y), _ptr(row_of_slot), _ptr(weights), T, k, y.shape[0], H, _ptr(dy),
             _ptr(dweights))
     return dy, dweights
+
+
+# --------------------------------------------------------------------------- balance losses
+
+class MoeBalance(NamedTuple):
+    """What moe_balance_loss returns."""
+    losses: torch.Tensor       # float32 [2]: balance (1 for an even load), mean square of the logits' log-sum-exp
+    counts: torch.Tensor       # int32 [E]
+    probs: torch.Tensor        # float32 [E], mean over the tokens that count
+    tokens: torch.Tensor       # int32 [1], how many count
+
+
+def _req_vector(t, name, dtype, n):
+    _req(t, name, dtype, 1)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+
+
+def moe_balance_loss(logits, ids=None, *, counts=None, workspace=None):
+    """The balance losses of router logits [T, E] (float32 or bfloat16; a token
+    whose logits are all -inf does not count): a MoeBalance.  The experts' loads
+    are counted from ``ids`` [T, k] (moe_route's), or given as ``counts`` int32
+    [E], for example moe_route's group_sizes summed over several ranks."""
+    if workspace is None:
+        r = (_calls or _plain()).balance(logits, ids, counts)
+        if r is not None:
+            return MoeBalance._make(r)
+    _req_logits(logits)
+    T, E = logits.shape
+    _req_i32(E, "the number of experts")
+    if (ids is None) == (counts is None):
+        raise ValueError("either ids or counts must be given")
+    if workspace is not None:
+        _req(workspace, "workspace", torch.uint8, 1)
+    dev = _same_device(logits, ids, counts, workspace)
+    k = 1
+    if ids is None:
+        _req_vector(counts, "counts", torch.int32, E)
+    else:
+        _req(ids, "ids", torch.int32, 2)
+        k = ids.shape[1]
+        _req_i32(k, "k")
+        if ids.shape[0] != T:
+            raise ValueError(f"ids must be [{T}, k], got {tuple(ids.shape)}")
+        counts = torch.empty((E,), dtype=torch.int32, device=dev)
+    losses, probs = torch.empty((2,), device=dev), torch.empty((E,), device=dev)
+    tokens = torch.empty((1,), dtype=torch.int32, device=dev)
+    ws, need = _workspace(OP_BALANCE, T, E, k, 1, dev, tile_m=0, workspace=workspace)
+    # an empty tensor's pointer is NULL, which would make counts an input: any other stands for no ids
+    ids_ptr = None if ids is None else _ptr(ids) or _ptr(tokens)
+    _launch(dev, "moe_balance_loss", _ptr(logits), LOGIT_DTYPES[logits.dtype], ids_ptr, T, E, k, _ptr(losses),
+            _ptr(counts), _ptr(probs), _ptr(tokens), _ptr(ws), need)
+    return MoeBalance(losses, counts, probs, tokens)
+
+
+def moe_balance_loss_bwd(dlosses, logits, counts, tokens, *, add=None, out=None):
+    """The logits' gradient, in their type [T, E], of moe_balance_loss's losses
+    weighted by dlosses float32 [2], from the forward's counts and tokens.
+    ``add`` (for example moe_route_bwd's result) is added before the rounding;
+    ``out`` may be ``add`` itself."""
+    if out is None:
+        r = (_calls or _plain()).balance_bwd(dlosses, logits, counts, tokens, add)
+        if r is not None:
+            return r
+    _req_logits(logits)
+    T, E = logits.shape
+    _req_i32(E, "the number of experts")
+    _req_vector(dlosses, "dlosses", torch.float32, 2)
+    _req_vector(counts, "counts", torch.int32, E)
+    _req_vector(tokens, "tokens", torch.int32, 1)
+    dev = _same_device(dlosses, logits, counts, tokens, add, out)
+    if add is not None:
+        add = _out(add, (T, E), logits.dtype, dev, "add")
+    out = _out(out, (T, E), logits.dtype, dev, "out")
+    _launch(dev, "moe_balance_loss_bwd", _ptr(dlosses), _ptr(logits), LOGIT_DTYPES[logits.dtype], _ptr(counts),
+            _ptr(tokens), T, E, _ptr(add), _ptr(out))
+    return out
+
+
+# --------------------------------------------------------------------------- AdamW, weight codes
+
+class _AdamW(ctypes.Structure):
+    """fp8gmm_adamw of the header."""
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
+        [("step", _I64), ("lr_dev", _P), ("step_dev", _P), ("grad_scale", _P)]
+
+
+STATE_BLOCK = 256      # consecutive elements that share one scale of an 8-bit state
+
+
+def adamw_8bit_states(params):
+    """Zero states of adamw_step_8bit for a list of parameters: two lists of
+    (codes uint8 of the parameter's shape, scales float32 [ceil(size / 256)])."""
+    def zeros(p):
+        return (torch.zeros(p.shape, dtype=torch.uint8, device=p.device),
+                torch.zeros(-(-p.numel() // STATE_BLOCK), device=p.device))
+    return [zeros(p) for p in params], [zeros(p) for p in params]
+
+
+def _number_or_device(v, name, dtype, dev):
+    """(host number, device pointer) of a number or a tensor of one."""
+    if not isinstance(v, torch.Tensor):
+        return v, None
+    if v.dtype != dtype:
+        raise TypeError(f"{name} must be a number or a {dtype} tensor, got {v.dtype}")
+    if v.numel() != 1:
+        raise ValueError(f"{name} must hold one number, got shape {tuple(v.shape)}")
+    if v.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {v.device}")
+    return 0, v.data_ptr()
+
+
+def _adamw(name, params, grads, states, held, lr, step, betas, eps, weight_decay, grad_scale, seed):
+    lists = [list(params), list(grads)] + [list(s) for s in states]
+    n = len(lists[0])
+    if any(len(l) != n for l in lists):
+        raise ValueError(f"the lists must have one length, got {[len(l) for l in lists]}")
+    if n == 0:
+        return
+    columns, named = lists[:2], ["params", "grads"]
+    if held:
+        for l, what in zip(lists[2:], ("exp_avgs", "exp_avg_roots")):
+            if any(not isinstance(s, (tuple, list)) or len(s) != 2 for s in l):
+                raise TypeError(f"{what} must hold pairs (codes, scales)")
+            columns, named = columns + [[s[0] for s in l], [s[1] for s in l]], named + [what + " codes", what + " scales"]
+    else:
+        columns, named = lists, named + ["exp_avgs", "exp_avg_sqs"]
+    for l, what in zip(columns, named):
+        for t in l:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{what} must hold torch.Tensors")
+            if what in ("params", "grads"):
+                if t.dtype not in LOGIT_DTYPES or t.dtype != l[0].dtype:
+                    raise TypeError(f"{what} must all be float32 or all bfloat16, got {t.dtype}")
+                dtype = t.dtype
+            else:
+                dtype = torch.uint8 if what.endswith("codes") else torch.float32
+            _req(t, what, dtype, t.dim())
+    for i, p in enumerate(columns[0]):
+        for l, what in zip(columns[1:], named[1:]):
+            want = (-(-p.numel() // STATE_BLOCK),) if what.endswith("scales") else tuple(p.shape)
+            if tuple(l[i].shape) != want:
+                raise ValueError(f"{what}[{i}] must be {want}, got {tuple(l[i].shape)}")
+    dev = _same_device(*(t for l in columns for t in l))
+    how = _AdamW(beta1=float(betas[0]), beta2=float(betas[1]), eps=float(eps), weight_decay=float(weight_decay))
+    lr, how.lr_dev = _number_or_device(lr, "lr", torch.float32, dev)
+    step, how.step_dev = _number_or_device(step, "step", torch.int64, dev)
+    if grad_scale is not None:
+        if not isinstance(grad_scale, torch.Tensor):
+            raise TypeError("grad_scale must be a torch.Tensor")
+        _, how.grad_scale = _number_or_device(grad_scale, "grad_scale", torch.float32, dev)
+    how.lr, step = float(lr), int(step)
+    if how.step_dev is None and not 1 <= step < 1 << 63:
+        raise ValueError(f"step must be at least 1, got {step}")
+    how.step = step
+    rates = [how.lr, how.eps, how.weight_decay]
+    if not all(0 <= v < float("inf") for v in rates) or not all(0 <= b < 1 for b in (how.beta1, how.beta2)):
+        raise ValueError(f"lr, eps and weight_decay must be finite and not negative, betas in [0, 1): got {rates}, {betas}")
+    if held and not 0 <= seed < 1 << 64:
+        raise ValueError(f"seed must fit 64 bits without a sign, got {seed}")
+    pointers = [(_P * n)(*(t.data_ptr() for t in l)) for l in columns]
+    sizes = (_I64 * n)(*(p.numel() for p in columns[0]))
+    p, g = LOGIT_DTYPES[columns[0][0].dtype], LOGIT_DTYPES[columns[1][0].dtype]
+    _launch(dev, name, n, sizes, pointers[0], p, pointers[1], g, *pointers[2:], *((seed,) if held else ()),
+            ctypes.byref(how))
+
+
+def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+               grad_scale=None):
+    """One AdamW step over lists of tensors, in place: parameters and gradients
+    float32 or bfloat16, states float32.  ``step`` counts from 1.  ``lr`` and
+    ``step`` may be tensors of one number on the device (float32, int64), read
+    when the kernels run, for captured graphs; ``grad_scale`` is such a float32
+    tensor that multiplies the gradients.  A tensor may be listed once."""
+    st = (_calls or _plain()).adamw(params, grads, exp_avgs, exp_avg_sqs, lr, step, *betas, eps, weight_decay,
+                                    grad_scale)
+    if st is None:
+        _adamw("adamw_step", params, grads, (exp_avgs, exp_avg_sqs), False, lr, step, betas, eps, weight_decay,
+               grad_scale, 0)
+    elif st != OK:
+        raise Fp8GmmError("adamw_step", st)
+
+
+def adamw_step_8bit(params, grads, exp_avgs, exp_avg_roots, *, lr, step, betas=(0.9, 0.999), eps=1e-8,
+                    weight_decay=0.01, grad_scale=None, seed=0):
+    """adamw_step with states in 8 bits: lists of (codes, scales) as
+    adamw_8bit_states makes them, of the first moment and of the second one's
+    square root.  Codes are rounded up or down by chance, as ``seed`` and
+    ``step`` decide: the same call on the same tensors gives the same bits."""
+    seed = int(seed)
+    st = (_calls or _plain()).adamw8(params, grads, exp_avgs, exp_avg_roots, lr, step, *betas, eps, weight_decay,
+                                     grad_scale, seed)
+    if st is None:
+        _adamw("adamw_step_8bit", params, grads, (exp_avgs, exp_avg_roots), True, lr, step, betas, eps, weight_decay,
+               grad_scale, seed)
+    elif st != OK:
+        raise Fp8GmmError("adamw_step_8bit", st)
+
+
+def quantize_fp8_weights(w, *, codes=None, scales=None):
+    """e4m3 codes u8 [G, K, N] and f32 scales [G, N], one per output channel over
+    all K, of master weights w [G, K, N] (float32 or bfloat16): what the FP8
+    calls read."""
+    if codes is None and scales is None:
+        r = (_calls or _plain()).quantize_fp8(w)
+        if r is not None:
+            return r
+    if isinstance(w, torch.Tensor) and w.dtype not in LOGIT_DTYPES:
+        raise TypeError(f"w must be float32 or bfloat16, got {w.dtype}")
+    _req(w, "w", getattr(w, "dtype", None), 3)
+    G, K, N = w.shape
+    _req_i32(G, "the number of experts")
+    dev = _same_device(w, codes, scales)
+    codes = _out(codes, (G, K, N), torch.uint8, dev, "codes")
+    scales = _out(scales, (G, N), torch.float32, dev, "scales")
+    _launch(dev, "quantize_fp8_weights", _ptr(w), LOGIT_DTYPES[w.dtype], K, N, G, _ptr(codes), _ptr(scales))
+    return codes, scales
 
 
 # --------------------------------------------------------------------------- MXFP4

@@ -20,8 +20,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8_moe_grouped.so")
 CALLS = os.path.join(PKG, "_calls.so")
 
-SOURCES = ["quant.hip", "gmm_fwd.hip", "dlhs.hip", "tgmm.hip", "dequant.hip", "route.hip", "permute.hip", "mxfp4.hip",
-           "gmm_mxfp4.hip", "api.hip"]
+SOURCES = ["quant.hip", "gmm_fwd.hip", "dlhs.hip", "tgmm.hip", "dequant.hip", "route.hip", "balance.hip", "permute.hip",
+           "quant_weights.hip", "mxfp4.hip", "gmm_mxfp4.hip", "adamw.hip", "api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -3,7 +3,10 @@
 // entry point are in include/fp8_moe_grouped.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
+#include <vector>
 
 #include "../../include/fp8_moe_grouped.h"
 #include "moe_launch.hpp"
@@ -87,6 +90,76 @@ int current_scratch(void** out) {
   }
   *out = p;
   return FP8GMM_OK;
+}
+
+}  // namespace
+
+namespace {
+
+constexpr int64_t kMaxElements = 1LL << 35;         // of an AdamW tensor: 2^23 blocks
+
+// A buffer of an AdamW call.
+struct Range {
+  uintptr_t begin, end;
+  bool written;
+};
+
+// Whether a written buffer overlaps another one.
+bool overlap(std::vector<Range>& all) {
+  std::sort(all.begin(), all.end(), [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t any = 0, written = 0;                   // where the buffers so far end
+  for (const Range& r : all) {
+    if (r.begin < (r.written ? any : written)) return true;
+    any = std::max(any, r.end);
+    if (r.written) written = std::max(written, r.end);
+  }
+  return false;
+}
+
+// What both AdamW calls check; buffers(i, size, put) names a tensor's state as put(pointer, bytes).
+template <typename F>
+int check_adamw(int32_t tensors, const int64_t* sizes, void* const* params, int32_t param_dtype,
+                const void* const* grads, int32_t grad_dtype, bool states, const fp8gmm_adamw* how, F buffers) {
+  if (tensors < 0) return FP8GMM_ERR_SHAPE;
+  if (!how || (tensors > 0 && (!sizes || !params || !grads || !states))) return FP8GMM_ERR_NULL;
+  for (int32_t d : {param_dtype, grad_dtype})
+    if (d != FP8GMM_F32 && d != FP8GMM_BF16) return FP8GMM_ERR_UNSUPPORTED;
+  const auto rate = [](double v) { return v >= 0.0 && std::isfinite(v); };
+  const auto beta = [](double v) { return v >= 0.0 && v < 1.0; };
+  if ((!how->lr_dev && !rate(how->lr)) || !rate(how->eps) || !rate(how->weight_decay) || !beta(how->beta1) ||
+      !beta(how->beta2) || (!how->step_dev && how->step < 1))
+    return FP8GMM_ERR_UNSUPPORTED;
+  try {
+    std::vector<Range> all;
+    all.reserve((size_t)tensors * 6);
+    int st = FP8GMM_OK;
+    for (int32_t i = 0; i < tensors && st == FP8GMM_OK; ++i) {
+      const int64_t n = sizes[i];
+      if (n < 0 || n > kMaxElements) return FP8GMM_ERR_SHAPE;
+      if (n == 0) continue;
+      const auto put = [&](const void* p, int64_t bytes, uintptr_t align = 16, bool written = true) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        if (!p) st = FP8GMM_ERR_NULL;
+        else if (at % align != 0 && st == FP8GMM_OK) st = FP8GMM_ERR_ALIGN;
+        all.push_back({at, at + (uintptr_t)bytes, written});
+      };
+      put(params[i], n * (param_dtype == FP8GMM_F32 ? 4 : 2));
+      put(grads[i], n * (grad_dtype == FP8GMM_F32 ? 4 : 2), 16, false);
+      buffers(i, n, put);
+    }
+    if (st != FP8GMM_OK) return st;
+    return overlap(all) ? FP8GMM_ERR_OVERLAP : FP8GMM_OK;
+  } catch (...) {                                   // host memory: nothing passes the C boundary
+    return FP8GMM_ERR_UNSUPPORTED;
+  }
+}
+
+AdamW adamw_of(const fp8gmm_adamw& h) {
+  AdamW a{h.lr, h.beta1, h.beta2, h.eps, h.weight_decay, h.lr * h.weight_decay, 0.0, 0.0, h.step,
+          h.lr_dev, h.step_dev, h.grad_scale};
+  a.up = h.lr / (1.0 - std::pow(h.beta1, (double)h.step));
+  a.root = 1.0 / std::sqrt(1.0 - std::pow(h.beta2, (double)h.step));
+  return a;
 }
 
 }  // namespace
@@ -447,6 +520,43 @@ int moe_route_bwd(const float* dweights, const void* logits, int32_t dtype, cons
   return FP8GMM_OK;
 }
 
+static int check_balance(int64_t T, int64_t E, int64_t k) {
+  if (T < 0 || E <= 0 || k <= 0 || T > kMaxRows / k) return FP8GMM_ERR_SHAPE;
+  if (E > kMaxGroups || k > kMaxTopk) return FP8GMM_ERR_UNSUPPORTED;
+  return FP8GMM_OK;
+}
+
+int moe_balance_loss(const void* logits, int32_t dtype, const int32_t* ids, int64_t T, int32_t E, int32_t k,
+                     float* losses, int32_t* counts, float* probs, int32_t* tokens, void* ws, size_t ws_bytes,
+                     void* stream) {
+  if (!losses || !counts || !probs || !tokens) return FP8GMM_ERR_NULL;
+  if (!ids) k = 1;
+  int st = check_balance(T, E, k);
+  if (st != FP8GMM_OK) return st;
+  if (T > 0 && !logits) return FP8GMM_ERR_NULL;
+  if (dtype != FP8GMM_F32 && dtype != FP8GMM_BF16) return FP8GMM_ERR_UNSUPPORTED;
+  if (!aligned16(logits) || !aligned16(ws)) return FP8GMM_ERR_ALIGN;
+  const size_t need = balance_workspace_bytes((int)T, E);
+  if (need > 0 && (!ws || ws_bytes < need)) return FP8GMM_ERR_WORKSPACE;
+  if (launch_balance(logits, dtype == FP8GMM_BF16, ids, (int)T, E, k, losses, counts, probs, tokens, ws,
+                     reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+int moe_balance_loss_bwd(const float* dlosses, const void* logits, int32_t dtype, const int32_t* counts,
+                         const int32_t* tokens, int64_t T, int32_t E, const void* add, void* dlogits, void* stream) {
+  int st = check_balance(T, E, 1);
+  if (st != FP8GMM_OK) return st;
+  if (!dlosses || !counts || !tokens || (T > 0 && (!logits || !dlogits))) return FP8GMM_ERR_NULL;
+  if (dtype != FP8GMM_F32 && dtype != FP8GMM_BF16) return FP8GMM_ERR_UNSUPPORTED;
+  if (!aligned16(logits) || !aligned16(add) || !aligned16(dlogits)) return FP8GMM_ERR_ALIGN;
+  if (launch_balance_bwd(dlosses, logits, dtype == FP8GMM_BF16, counts, tokens, (int)T, E, add, dlogits,
+                         reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
 // T tokens of width H with k choices each, R buffer rows.
 static int check_slots(int64_t T, int64_t k, int64_t R, int64_t H) {
   if (T < 0 || k <= 0 || R < 0 || R > kMaxRows || H <= 0 || T > kMaxRows / k) return FP8GMM_ERR_SHAPE;
@@ -503,6 +613,54 @@ int moe_combine_bwd(const void* dout, const void* y, const int32_t* row_of_slot,
   if (launch_combine_bwd(static_cast<const uint16_t*>(dout), static_cast<const uint16_t*>(y), row_of_slot, weights,
                          (int)T, k, (int)R, (int)H, static_cast<uint16_t*>(dy), dweights,
                          reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+int quantize_fp8_weights(const void* w, int32_t dtype, int64_t K, int64_t N, int32_t G, uint8_t* codes_out,
+                         float* scale_out, void* stream) {
+  int st = check_common(0, K, N, G);
+  if (st != FP8GMM_OK) return st;
+  if (dtype != FP8GMM_F32 && dtype != FP8GMM_BF16) return FP8GMM_ERR_UNSUPPORTED;
+  if (!w || !codes_out || !scale_out) return FP8GMM_ERR_NULL;
+  if (!aligned16(w) || !aligned16(codes_out) || !aligned16(scale_out)) return FP8GMM_ERR_ALIGN;
+  if (launch_quant_weights_fp8(w, dtype == FP8GMM_BF16, G, (int)K, (int)N, codes_out, scale_out,
+                               reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+int adamw_step(int32_t tensors, const int64_t* sizes, void* const* params, int32_t param_dtype,
+               const void* const* grads, int32_t grad_dtype, float* const* exp_avgs, float* const* exp_avg_sqs,
+               const fp8gmm_adamw* how, void* stream) {
+  const int st = check_adamw(tensors, sizes, params, param_dtype, grads, grad_dtype, exp_avgs && exp_avg_sqs, how,
+                             [&](int32_t i, int64_t n, const auto& put) {
+                               put(exp_avgs[i], 4 * n);
+                               put(exp_avg_sqs[i], 4 * n);
+                             });
+  if (st != FP8GMM_OK) return st;
+  if (launch_adamw(tensors, sizes, params, param_dtype == FP8GMM_BF16, grads, grad_dtype == FP8GMM_BF16, exp_avgs,
+                   exp_avg_sqs, adamw_of(*how), reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return FP8GMM_ERR_HIP;
+  return FP8GMM_OK;
+}
+
+int adamw_step_8bit(int32_t tensors, const int64_t* sizes, void* const* params, int32_t param_dtype,
+                    const void* const* grads, int32_t grad_dtype, uint8_t* const* m_codes, float* const* m_scales,
+                    uint8_t* const* r_codes, float* const* r_scales, uint64_t seed, const fp8gmm_adamw* how,
+                    void* stream) {
+  const int st = check_adamw(tensors, sizes, params, param_dtype, grads, grad_dtype,
+                             m_codes && m_scales && r_codes && r_scales, how,
+                             [&](int32_t i, int64_t n, const auto& put) {
+                               put(m_codes[i], n);
+                               put(r_codes[i], n);
+                               put(m_scales[i], (n + 255) / 256 * 4, 4);
+                               put(r_scales[i], (n + 255) / 256 * 4, 4);
+                             });
+  if (st != FP8GMM_OK) return st;
+  if (launch_adamw8(tensors, sizes, params, param_dtype == FP8GMM_BF16, grads, grad_dtype == FP8GMM_BF16, m_codes,
+                    m_scales, r_codes, r_scales, seed, adamw_of(*how), reinterpret_cast<hipStream_t>(stream)) !=
+      hipSuccess)
     return FP8GMM_ERR_HIP;
   return FP8GMM_OK;
 }
@@ -587,6 +745,8 @@ int gmm_silu_mxfp4(const void* x, const uint8_t* codes, const uint8_t* scale, co
 }
 
 size_t fp8gmm_workspace_bytes(int32_t op, int64_t M, int64_t K, int64_t N, int32_t G, int32_t tile_m) {
+  if (op == FP8GMM_OP_BALANCE)
+    return check_balance(M, K, N) == FP8GMM_OK ? balance_workspace_bytes((int)M, (int)K) : 0;
   if (op == FP8GMM_OP_ROUTE) return check_route(M, K, N) == FP8GMM_OK ? route_workspace_bytes((int)M, (int)K) : 0;
   if (check_common(M, K, N, G) != FP8GMM_OK) return 0;
   switch (op) {
@@ -620,6 +780,7 @@ const char* fp8gmm_status_string(int32_t status) {
     case FP8GMM_ERR_WORKSPACE: return "workspace missing or too small";
     case FP8GMM_ERR_HIP: return "a HIP kernel launch failed";
     case FP8GMM_ERR_SCRATCH: return "the input does not fit the fixed scratch of the allocation-free entry point";
+    case FP8GMM_ERR_OVERLAP: return "a buffer that the call writes overlaps another of its buffers";
     default: return "unknown status";
   }
 }

@@ -1,5 +1,5 @@
-// The plain case of the routing, dispatch, combine and 4-bit calls without the
-// interpreter: tensors on the current device, contiguous and of the right types and
+// The plain case of the routing, dispatch, combine, 4-bit, balance, AdamW and weight quantizer
+// calls without the interpreter: tensors on the current device, contiguous and of the right types and
 // sizes, outputs and workspace allocated here.  Anything else (other arguments, a
 // non-zero status) returns None, and the Python function of the same name checks,
 // converts, calls and reports.  A decoded token's kernels run for a few microseconds,
@@ -16,6 +16,9 @@
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 
+#include <cmath>
+#include <vector>
+
 #include "../../include/fp8_moe_grouped.h"
 
 namespace {
@@ -24,7 +27,8 @@ using at::Tensor;
 
 #define CALLS(X)                                                                                                 \
   X(moe_route) X(moe_route_bwd) X(moe_permute) X(moe_permute_fp8) X(moe_combine) X(moe_combine_bwd)               \
-  X(quantize_mxfp4_weights) X(dequantize_mxfp4) X(gmm_mxfp4_fwd) X(gmm_silu_mxfp4) X(fp8gmm_workspace_bytes)
+  X(quantize_mxfp4_weights) X(dequantize_mxfp4) X(gmm_mxfp4_fwd) X(gmm_silu_mxfp4) X(fp8gmm_workspace_bytes)     \
+  X(moe_balance_loss) X(moe_balance_loss_bwd) X(quantize_fp8_weights) X(adamw_step) X(adamw_step_8bit)
 
 struct Library {
 #define X(name) decltype(&::name) name = nullptr;
@@ -287,13 +291,190 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END
 }
 
+bool logits_type(const Tensor& t) { return t.scalar_type() == kF32 || t.scalar_type() == kBf16; }
+int32_t type_of(const Tensor& t) { return t.scalar_type() == kBf16 ? FP8GMM_BF16 : FP8GMM_F32; }
+
+// (logits, ids or None, counts or None)
+PyObject* balance(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BEGIN(3)
+  const Tensor* x = in.any(a[0], 2);
+  const Tensor* ids = a[1] == Py_None ? nullptr : in.get(a[1], kI32, 2);
+  const Tensor* given = a[2] == Py_None ? nullptr : in.get(a[2], kI32, 1);
+  PLAIN(in.ok && logits_type(*x) && !ids != !given)
+  const int64_t T = x->size(0), E = x->size(1), k = ids ? ids->size(1) : 1;
+  PLAIN(T > 0 && E < (1 << 30) && k < (1 << 30) && (!ids || ids->size(0) == T) && (!given || given->size(0) == E))
+  const Tensor losses = in.make({2}, kF32), probs = in.make({E}, kF32), tokens = in.make({1}, kI32);
+  const Tensor counts = given ? *given : in.make({E}, kI32);
+  const size_t need = lib.fp8gmm_workspace_bytes(FP8GMM_OP_BALANCE, T, E, k, 1, 0);
+  Tensor ws;
+  if (need) ws = in.make({(int64_t)need}, kU8);
+  PLAIN(lib.moe_balance_loss(x->data_ptr(), type_of(*x), ids ? ptr<int32_t>(*ids) : nullptr, T, (int32_t)E,
+                             (int32_t)k, ptr<float>(losses), ptr<int32_t>(counts), ptr<float>(probs),
+                             ptr<int32_t>(tokens), need ? ws.data_ptr() : nullptr, need, in.stream()) == FP8GMM_OK)
+  return pack({losses, counts, probs, tokens});
+  END
+}
+
+// (dlosses, logits, counts, tokens, add or None)
+PyObject* balance_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BEGIN(5)
+  const Tensor* x = in.any(a[1], 2);
+  const Tensor *d = in.get(a[0], kF32, 1), *counts = in.get(a[2], kI32, 1), *tokens = in.get(a[3], kI32, 1);
+  PLAIN(in.ok && logits_type(*x))
+  const Tensor* add = a[4] == Py_None ? nullptr : in.get(a[4], x->scalar_type(), 2);
+  const int64_t T = x->size(0), E = x->size(1);
+  PLAIN(in.ok && d->size(0) == 2 && counts->size(0) == E && tokens->size(0) == 1 && (!add || is(*add, T, E)) &&
+        E < (1 << 30))
+  const Tensor out = in.make({T, E}, x->scalar_type());
+  PLAIN(lib.moe_balance_loss_bwd(ptr<float>(*d), x->data_ptr(), type_of(*x), ptr<int32_t>(*counts),
+                                 ptr<int32_t>(*tokens), T, (int32_t)E, add ? add->data_ptr() : nullptr,
+                                 out.data_ptr(), in.stream()) == FP8GMM_OK)
+  return pack({out});
+  END
+}
+
+// (w)
+PyObject* quantize_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BEGIN(1)
+  const Tensor* w = in.any(a[0], 3);
+  PLAIN(in.ok && logits_type(*w))
+  const int64_t G = w->size(0), K = w->size(1), N = w->size(2);
+  PLAIN(G < (1 << 30))
+  const Tensor codes = in.make({G, K, N}, kU8), scales = in.make({G, N}, kF32);
+  PLAIN(lib.quantize_fp8_weights(w->data_ptr(), type_of(*w), K, N, (int32_t)G, ptr<uint8_t>(codes),
+                                 ptr<float>(scales), in.stream()) == FP8GMM_OK)
+  return pack({codes, scales});
+  END
+}
+
+// A list of tensors with as many members as the call's other lists.
+struct List {
+  PyObject* fast = nullptr;
+  Py_ssize_t n = 0;
+  explicit List(PyObject* o) {
+    if (!PyList_Check(o) && !PyTuple_Check(o)) return;
+    fast = PySequence_Fast(o, "");
+    if (fast) n = PySequence_Fast_GET_SIZE(fast);
+  }
+  ~List() { Py_XDECREF(fast); }
+  List(const List&) = delete;
+  PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(fast, i); }
+};
+
+// A number, or a tensor of one element of this type on the device.
+bool number(Args& in, PyObject* o, at::ScalarType type, double* value, const void** device) {
+  if (THPVariable_Check(o)) {
+    const Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda() || t.scalar_type() != type || t.numel() != 1 || (in.dev >= 0 && t.get_device() != in.dev))
+      return false;
+    *device = t.data_ptr();
+    return true;
+  }
+  if (!value || !PyFloat_Check(o)) return false;
+  *value = PyFloat_AS_DOUBLE(o);
+  return true;
+}
+
+// Tensors of any shape, contiguous, on one device, the current one.
+const Tensor* member(Args& in, PyObject* o) {
+  if (!THPVariable_Check(o)) return in.fail();
+  return in.any(o, THPVariable_Unpack(o).dim());
+}
+
+// (params, grads, m, second state, lr, step, beta1, beta2, eps, weight_decay, grad_scale or None[, seed]): with a
+// seed the states are pairs of codes and scales.  Answers the status.
+PyObject* adamw_call(PyObject* const* a, bool held) {
+  HANDLE_TH_ERRORS
+  Args in;
+  const List p(a[0]), g(a[1]), m(a[2]), v(a[3]);
+  PLAIN(p.fast && g.fast && m.fast && v.fast && p.n == g.n && p.n == m.n && p.n == v.n && p.n > 0 && p.n < (1 << 24))
+  std::vector<int64_t> sizes((size_t)p.n);
+  std::vector<void*> at((size_t)p.n * 6);
+  void** const cols = at.data();                    // params, grads, then the states' buffers
+  at::ScalarType types[2] = {kF32, kF32};
+  for (Py_ssize_t i = 0; i < p.n; ++i) {
+    const Tensor *pt = member(in, p[i]), *gt = member(in, g[i]);
+    PLAIN(in.ok && logits_type(*pt) && logits_type(*gt))
+    if (i == 0) {
+      types[0] = pt->scalar_type();
+      types[1] = gt->scalar_type();
+    }
+    const int64_t size = pt->numel();
+    PLAIN(pt->scalar_type() == types[0] && gt->scalar_type() == types[1] && gt->sizes() == pt->sizes())
+    sizes[(size_t)i] = size;
+    cols[i] = pt->data_ptr();
+    cols[p.n + i] = gt->data_ptr();
+    PyObject* const states[2] = {m[i], v[i]};
+    for (int s = 0; s < 2; ++s) {
+      if (held) {
+        PLAIN(PyTuple_Check(states[s]) && PyTuple_GET_SIZE(states[s]) == 2)
+        const Tensor* codes = member(in, PyTuple_GET_ITEM(states[s], 0));
+        const Tensor* scales = in.get(PyTuple_GET_ITEM(states[s], 1), kF32, 1);
+        PLAIN(in.ok && codes->scalar_type() == kU8 && codes->sizes() == pt->sizes() &&
+              scales->numel() == (size + 255) / 256)
+        cols[(2 + 2 * s) * p.n + i] = codes->data_ptr();
+        cols[(3 + 2 * s) * p.n + i] = scales->data_ptr();
+      } else {
+        const Tensor* t = member(in, states[s]);
+        PLAIN(in.ok && t->scalar_type() == kF32 && t->sizes() == pt->sizes())
+        cols[(2 + s) * p.n + i] = t->data_ptr();
+      }
+    }
+  }
+  fp8gmm_adamw how = {};
+  const void *lr = nullptr, *step = nullptr, *scale = nullptr;
+  PLAIN(number(in, a[4], kF32, &how.lr, &lr))
+  if (PyLong_Check(a[5])) how.step = integer(a[5]);
+  else PLAIN(number(in, a[5], at::kLong, nullptr, &step))
+  double* const rates[4] = {&how.beta1, &how.beta2, &how.eps, &how.weight_decay};
+  for (int i = 0; i < 4; ++i) {
+    PLAIN(PyFloat_Check(a[6 + i]))
+    *rates[i] = PyFloat_AS_DOUBLE(a[6 + i]);
+  }
+  PLAIN(a[10] == Py_None || number(in, a[10], kF32, nullptr, &scale))
+  how.lr_dev = static_cast<const float*>(lr);
+  how.step_dev = static_cast<const int64_t*>(step);
+  how.grad_scale = static_cast<const float*>(scale);
+  const int32_t n = (int32_t)p.n, pd = types[0] == kBf16, gd = types[1] == kBf16;
+  const void* const* const grads = cols + p.n;
+  int st;
+  if (held) {
+    const unsigned long long seed = PyLong_Check(a[11]) ? PyLong_AsUnsignedLongLong(a[11]) : 0;
+    if (PyErr_Occurred() || !PyLong_Check(a[11])) {
+      PyErr_Clear();
+      Py_RETURN_NONE;
+    }
+    st = lib.adamw_step_8bit(n, sizes.data(), cols, pd, grads, gd, reinterpret_cast<uint8_t**>(cols + 2 * p.n),
+                             reinterpret_cast<float**>(cols + 3 * p.n), reinterpret_cast<uint8_t**>(cols + 4 * p.n),
+                             reinterpret_cast<float**>(cols + 5 * p.n), seed, &how, in.stream());
+  } else {
+    st = lib.adamw_step(n, sizes.data(), cols, pd, grads, gd, reinterpret_cast<float**>(cols + 2 * p.n),
+                        reinterpret_cast<float**>(cols + 3 * p.n), &how, in.stream());
+  }
+  // not left to Python after a launch, which has changed some tensors already
+  PLAIN(st == FP8GMM_OK || st == FP8GMM_ERR_HIP)
+  return PyLong_FromLong(st);
+  END
+}
+PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n == 11) return adamw_call(a, false);
+  PyErr_SetString(PyExc_TypeError, "argument count");
+  return nullptr;
+}
+PyObject* adamw8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n == 12) return adamw_call(a, true);
+  PyErr_SetString(PyExc_TypeError, "argument count");
+  return nullptr;
+}
+
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(bind),     {"names", names, METH_NOARGS, nullptr},
                          METHOD(route),    METHOD(route_bwd),
                          METHOD(permute),  METHOD(permute_fp8),
                          METHOD(combine),  METHOD(combine_bwd),
                          METHOD(quantize_weights), METHOD(values),
-                         METHOD(product),  {nullptr, nullptr, 0, nullptr}};
+                         METHOD(product),  METHOD(balance), METHOD(balance_bwd),
+                         METHOD(quantize_fp8), METHOD(adamw), METHOD(adamw8), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods};
 
 }  // namespace

@@ -16,6 +16,13 @@ hipError_t launch_route(const void* logits, bool bf16, int T, int E, int k, bool
 hipError_t launch_route_bwd(const float* dweights, const void* logits, bool bf16, const int* ids, const float* weights,
                             int T, int E, int k, bool renorm, void* dlogits, hipStream_t stream);
 
+// Balance losses (ids NULL: counts is an input) and the logits' gradient (add may be NULL or dlogits).
+size_t balance_workspace_bytes(int T, int E);
+hipError_t launch_balance(const void* logits, bool bf16, const int* ids, int T, int E, int k, float* losses,
+                          int* counts, float* probs, int* tokens, void* ws, hipStream_t stream);
+hipError_t launch_balance_bwd(const float* dlosses, const void* logits, bool bf16, const int* counts,
+                              const int* tokens, int T, int E, const void* add, void* dlogits, hipStream_t stream);
+
 // Tokens to the ragged buffer's R rows and back.
 hipError_t launch_permute(const uint16_t* x, const int* row_of_slot, int T, int k, int R, int H, uint16_t* out,
                           hipStream_t stream);
@@ -37,5 +44,26 @@ hipError_t launch_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int
 hipError_t launch_gmm_mxfp4(const uint8_t* aq, const uint8_t* ascale, const uint8_t* codes, const uint8_t* wscale,
                             const int* group_sizes, const int* slot_of_row, int topk, int T, int G, int M, int K,
                             int N, bool swiglu, uint16_t* out, int* status, hipStream_t stream);
+
+// Master weights to e4m3 codes and a scale per output channel.
+hipError_t launch_quant_weights_fp8(const void* w, bool bf16, int G, int K, int N, uint8_t* codes, float* scales,
+                                    hipStream_t stream);
+
+// AdamW.  decay, up and root are lr * weight_decay, lr / (1 - beta1^step) and 1 / sqrt(1 - beta2^step); lr_dev and
+// step_dev replace lr and step.
+struct AdamW {
+  double lr, beta1, beta2, eps, weight_decay, decay, up, root;
+  int64_t step;
+  const float* lr_dev;
+  const int64_t* step_dev;
+  const float* grad_scale;
+};
+hipError_t launch_adamw(int tensors, const int64_t* sizes, void* const* params, bool param_bf16,
+                        const void* const* grads, bool grad_bf16, float* const* m, float* const* v, const AdamW& how,
+                        hipStream_t stream);
+hipError_t launch_adamw8(int tensors, const int64_t* sizes, void* const* params, bool param_bf16,
+                         const void* const* grads, bool grad_bf16, uint8_t* const* m_codes, float* const* m_scales,
+                         uint8_t* const* r_codes, float* const* r_scales, uint64_t seed, const AdamW& how,
+                         hipStream_t stream);
 
 }  // namespace fp8gmm

@@ -26,7 +26,7 @@
 // without conflicts, and the count before the increment is the slot's rank among
 // the wave's slots of that expert.  Waves of a block and then blocks are joined by
 // prefix sums of the histograms: the order of slots never depends on timing.
-#include "moe_common.hpp"
+#include "logits.hpp"
 #include "moe_launch.hpp"
 
 #include <algorithm>
@@ -53,9 +53,6 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 }
-
-__device__ __forceinline__ float load_logit(const float* x) { return *x; }
-__device__ __forceinline__ float load_logit(const uint16_t* x) { return __uint_as_float((uint32_t)*x << 16); }
 
 // Keys: larger for the larger logit, then for the lower expert.  -0 equals +0, NaN is above +inf;
 // a masked logit (-inf) is at or below kMasked, a place past the experts is kNone.
@@ -131,32 +128,6 @@ __device__ __forceinline__ void sort_down(typename O::Key (&s)[V], std::integer_
     y = small;
   };
   (exchange(s[w.a[I]], s[w.b[I]]), ...);
-}
-
-// Lane `at` of the L that share a token holds the experts of chunks at, at + L, ..: C logits each (16 bytes).
-template <int L, int C>
-__device__ __forceinline__ int expert_of(int at, int i) { return (i / C * L + at) * C + i % C; }
-
-template <int L, int V, typename TX>
-__device__ __forceinline__ void load_logits(const TX* row, int E, int at, bool here, bool wide, float (&x)[V]) {
-  constexpr int C = 16 / (int)sizeof(TX);
-  if (wide) {                                       // E is a multiple of C: a chunk is inside or outside
-#pragma unroll
-    for (int i = 0; i < V; i += C) {
-      const int e = expert_of<L, C>(at, i);
-      const v4i w = here && e < E ? *reinterpret_cast<const v4i*>(row + e) : (v4i){0, 0, 0, 0};
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        x[i + c] = C == 4 ? __uint_as_float((uint32_t)w[c % 4])
-                          : (c & 1 ? bf16_hi((uint32_t)w[c / 2 % 4]) : bf16_lo((uint32_t)w[c / 2 % 4]));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = expert_of<L, C>(at, i);
-      x[i] = here && e < E ? load_logit(row + e) : 0.f;
-    }
-  }
 }
 
 // The k choices of a token: lane j < k of its lanes returns choice j.  A lane's list never moves up
@@ -487,25 +458,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const float* __restrict_
     for (int i = 0; i < V; ++i) d[i] = some ? d[i] - x[i] * share : 0.f;
   }
   if (!here) return;
-  TX* const out = dlogits + (size_t)t * E;
-#pragma unroll
-  for (int i = 0; i < V; i += C) {
-    const int e = expert_of<L, C>(at, i);
-    uint32_t o[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      o[c] = C == 4 ? __float_as_uint(d[i + c]) : pack_bf16x2(d[i + C / 4 * c], d[i + C / 4 * c + 1]);
-    if (wide) {
-      if (e < E) *reinterpret_cast<v4i*>(out + e) = (v4i){(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
-    } else {
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (e + c < E) {
-          if constexpr (C == 4) out[e + c] = d[i + c];
-          else out[e + c] = (TX)(o[c / 2] >> (16 * (c & 1)));
-        }
-    }
-  }
+  store_logits<L, V>(dlogits + (size_t)t * E, E, at, wide, d);
 }
 
 int route_blocks(int T, int& chunks) {

@@ -7,8 +7,8 @@
  *   conversation page, and "MoE fp8 backward: in-kernel drhs operand
  *   quantization + configurable gradient dtype" (maxtext PR #4971).
  * Each declaration names the page and the section it follows.  The calls around
- * that path (moe_route to moe_combine_bwd, and the MXFP4 calls) are defined by
- * their formulas alone.
+ * that path (moe_route to moe_combine_bwd, the balance losses, AdamW, the weight
+ * quantizers and the MXFP4 calls) are defined by their formulas alone.
  *
  * Common conventions
  * ------------------
@@ -54,6 +54,7 @@ extern "C" {
 #define FP8GMM_ERR_WORKSPACE (-5)   /* workspace NULL or smaller than fp8gmm_workspace_bytes */
 #define FP8GMM_ERR_HIP (-6)         /* a kernel launch failed */
 #define FP8GMM_ERR_SCRATCH (-7)     /* input larger than gmm_fp8_fwd_noalloc's fixed scratch */
+#define FP8GMM_ERR_OVERLAP (-8)     /* adamw_step: a buffer that the call writes overlaps another */
 
 /* bits of *dev_status */
 #define FP8GMM_DEV_SUM_CLAMPED 1    /* sum(group_sizes) > M, clamped */
@@ -76,8 +77,9 @@ extern "C" {
 #define FP8GMM_OP_TGMM_DENSE 9  /* tgmm_dense_quant */
 #define FP8GMM_OP_ROUTE 10      /* moe_route: pass M = T, K = E, N = k, G = 1 */
 #define FP8GMM_OP_MXFP4 11      /* gmm_mxfp4_fwd, gmm_silu_mxfp4: pass M = T (rows of x) */
+#define FP8GMM_OP_BALANCE 12    /* moe_balance_loss: pass M = T, K = E, N = k (1 without ids), G = 1 */
 
-/* types of the router's logits */
+/* types of the router's logits, of AdamW's parameters and gradients, of master weights */
 #define FP8GMM_F32 0
 #define FP8GMM_BF16 1
 
@@ -400,6 +402,104 @@ int moe_combine(const void* y, const int32_t* row_of_slot, const float* weights,
                 int64_t H, void* out, void* stream);
 int moe_combine_bwd(const void* dout, const void* y, const int32_t* row_of_slot, const float* weights, int64_t T,
                     int32_t k, int64_t R, int64_t H, void* dy, float* dweights, void* stream);
+
+/*
+ * Balance losses of a router: how evenly its tokens fall on the experts, and how
+ * large its logits grow.  A token counts unless all its logits are -inf (padding);
+ * n is the number of those, p[t, :] the softmax of a token's E logits (zeros for
+ * one that does not count), lse[t] the logarithm of the sum of their exponentials.
+ *
+ * moe_balance_loss:
+ *   counts[e] number of ids equal to e (ids outside [0, E), as of masked choices,
+ *             are not counted), S their sum.  With ids NULL counts is an input: the
+ *             group_sizes of moe_route, or their sum over several ranks or batches
+ *   probs[e]  sum_t p[t, e] / n                                  f32
+ *   losses[0] E * sum_e (counts[e] / S) * probs[e], 1 for an even load; 0 if S or n is 0
+ *   losses[1] sum_t lse[t]^2 / n; 0 if n is 0                    f32
+ *   tokens[0] n                                                  i32
+ * A NaN or +inf among a token's logits makes probs and both losses NaN.  Only -inf masks:
+ * logits of the type's lowest value are numbers, whose squares make losses[1] inf.
+ * logits f32 or bf16 [T, E], ids i32 [T, k] or NULL, losses f32 [2], counts i32 [E],
+ * probs f32 [E], tokens i32 [1].  1 <= k <= 32, E <= 1024, T*k < 2^24; k does not
+ * matter without ids.  Sums in f32 and f64, in an order that the sizes alone decide.
+ * ws: fp8gmm_workspace_bytes(FP8GMM_OP_BALANCE, T, E, k, 1, 0) bytes (0 for few tokens).
+ *
+ * moe_balance_loss_bwd -- the logits' gradient of dlosses[0] * losses[0] +
+ *   dlosses[1] * losses[1], with the counts held fixed:
+ *   dlogits[t, e] = p[t, e] * ( dlosses[0] * E / (n S) * (counts[e] - sum_f p[t, f] counts[f])
+ *                               + dlosses[1] * 2 / n * lse[t] ) + add[t, e]
+ * add (or NULL) has dlogits' type and shape, for example moe_route_bwd's result, and
+ * may be dlogits itself.  A token that does not count has the gradient 0, one with a
+ * NaN or +inf NaN.  dlosses f32 [2]; tokens i32 [1] and counts as the forward left them
+ * (a negative count is 0).  Rounded once to the logits' type.
+ */
+int moe_balance_loss(const void* logits, int32_t dtype, const int32_t* ids, int64_t T, int32_t E, int32_t k,
+                     float* losses, int32_t* counts, float* probs, int32_t* tokens, void* ws, size_t ws_bytes,
+                     void* stream);
+int moe_balance_loss_bwd(const float* dlosses, const void* logits, int32_t dtype, const int32_t* counts,
+                         const int32_t* tokens, int64_t T, int32_t E, const void* add, void* dlogits, void* stream);
+
+/*
+ * AdamW over many tensors at once.  tensors is the number of tensors; sizes
+ * (elements, 0 <= size <= 2^35) and the arrays of device pointers are host arrays of
+ * that length, read before the call returns.  With t the step (from 1), every
+ * element of every tensor:
+ *   g  = grad * grad_scale[0]               grad_scale f32 [1], or NULL for 1
+ *   m' = beta1 m + (1 - beta1) g
+ *   v' = beta2 v + (1 - beta2) g^2
+ *   p' = p - ( lr wd p + lr / (1 - beta1^t) * m' / ( sqrt(v') / sqrt(1 - beta2^t) + eps ) )
+ * in f32, in place, p' rounded once to p's type.  Parameters and gradients are f32 or
+ * bf16 each (FP8GMM_F32 / FP8GMM_BF16, one type for all of a call's tensors).  The
+ * coefficients are computed in f64 and rounded to f32.  lr_dev (f32 [1]) and step_dev
+ * (i64 [1], values below 1 count as 1) replace lr and step where they are not NULL, for
+ * captured graphs; they and grad_scale are device memory.  lr, wd and eps are finite
+ * and not negative, the betas in [0, 1), step at least 1.  No buffer that the call
+ * writes may overlap another of its buffers (FP8GMM_ERR_OVERLAP): a tensor is listed
+ * once.  Buffers of empty tensors may be NULL.
+ *
+ * adamw_step: m and v f32, of the parameter's size.
+ * adamw_step_8bit: m and r = sqrt(v) as e4m3 codes u8 of the parameter's size, one f32
+ *   scale for each block of 256 consecutive elements (ceil(size / 256) scales, 4-byte
+ *   aligned, the last block may be shorter): m = code * scale.  After the step a block's new scale is
+ *   max|m'| / 448, and its codes round m' / scale up or down by chance: with d the
+ *   distance of e4m3's numbers at |q|,
+ *     |q| -> min( d * floor( |q| / d + u ), 448 ),   u = (b + 1/2) / 2^16,
+ *   b 16 bits of a 32-bit hash of (seed, t, place of the tensor in the list, place of
+ *   the element): the low half for m, the high half for r.  The mean of the code is the
+ *   value, so that changes far below d (0.05 % of r a step with beta2 = 0.999) are not
+ *   lost.  An r' above 0 gets the smallest code at least: it divides the next update.
+ *   Blocks with an Inf or NaN get a NaN scale.  Zero states are zero codes and scales.
+ *   The hash, modulo 2^32, with mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15;
+ *   x *= 0xBB67AE85; x ^= x >> 16, lo and hi the halves of seed, t modulo 2^32:
+ *     key  = mix( mix( lo + mix( hi + mix(t) ) ) + tensor )
+ *     hash = mix( mix( key + element / 256 ) + 0x9E3779B9 * (element % 256) )
+ */
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  const float* lr_dev;
+  const int64_t* step_dev;
+  const float* grad_scale;
+} fp8gmm_adamw;
+int adamw_step(int32_t tensors, const int64_t* sizes, void* const* params, int32_t param_dtype,
+               const void* const* grads, int32_t grad_dtype, float* const* exp_avgs, float* const* exp_avg_sqs,
+               const fp8gmm_adamw* how, void* stream);
+int adamw_step_8bit(int32_t tensors, const int64_t* sizes, void* const* params, int32_t param_dtype,
+                    const void* const* grads, int32_t grad_dtype, uint8_t* const* m_codes, float* const* m_scales,
+                    uint8_t* const* r_codes, float* const* r_scales, uint64_t seed, const fp8gmm_adamw* how,
+                    void* stream);
+
+/*
+ * quantize_fp8_weights -- the weight codes and scales that the FP8 calls read, from
+ * master weights w [G, K, N], f32 or bf16 (dtype FP8GMM_F32 / FP8GMM_BF16), one scale
+ * per output channel over all K:
+ *   scale_out[g,n]   = f32( max(max_k |w[g,k,n]|, 1e-12) / 448 )
+ *   codes_out[g,k,n] = e4m3fn( f32(w[g,k,n] / scale_out[g,n]) )   round to nearest even
+ * NaN gets a NaN code and does not count for the scale; a column with an Inf has the
+ * scale Inf, NaN codes where it is infinite and zeros elsewhere.
+ */
+int quantize_fp8_weights(const void* w, int32_t dtype, int64_t K, int64_t N, int32_t G, uint8_t* codes_out,
+                         float* scale_out, void* stream);
 
 /*
  * MXFP4: 4-bit e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) in
