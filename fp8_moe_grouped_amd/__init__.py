@@ -38,7 +38,7 @@ NOALLOC_SCRATCH_BYTES = 32 << 20
 DEV_SUM_CLAMPED, DEV_NEGATIVE_SIZE = 1, 2
 E4M3, E5M2 = 0, 1
 (OP_FWD, OP_SILU, OP_DLHS, OP_TGMM, OP_BF16_FWD, OP_BF16_DLHS, OP_FFN_FWD, OP_FFN_BWD, OP_FWD_VARIANT,
- OP_TGMM_DENSE, OP_ROUTE, OP_MXFP4, OP_BALANCE) = range(13)
+ OP_TGMM_DENSE, OP_ROUTE, OP_MXFP4, OP_BALANCE, OP_QUANT_WEIGHTS) = range(14)
 LHS_SCALE_BF16, ACC_BF16, RHS_SCALE_FIRST = 1, 2, 4
 GRAD_DTYPES = {"e4m3": E4M3, "e5m2": E5M2}
 F32, BF16 = 0, 1
@@ -88,7 +88,7 @@ _SIGNATURES = {
     "moe_balance_loss_bwd": [_P, _P, _I32, _P, _P, _I64, _I32, _P, _P, _P],
     "adamw_step": [_I32, _P, _P, _I32, _P, _I32, _P, _P, _P, _P],
     "adamw_step_8bit": [_I32, _P, _P, _I32, _P, _I32, _P, _P, _P, _P, _U64, _P, _P],
-    "quantize_fp8_weights": [_P, _I32, _I64, _I64, _I32, _P, _P, _P],
+    "quantize_fp8_weights": [_P, _I32, _I64, _I64, _I32, _P, _P, _P, _SZ, _P],
     "quantize_mxfp4_weights": [_P, _I64, _I64, _I32, _P, _P, _P],
     "dequantize_mxfp4": [_P, _P, _I64, _I64, _I32, _P, _P],
     "gmm_mxfp4_fwd": [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, _I32, _P, _P, _SZ, _P, _P],
@@ -996,11 +996,11 @@ def adamw_step_8bit(params, grads, exp_avgs, exp_avg_roots, *, lr, step, betas=(
         raise Fp8GmmError("adamw_step_8bit", st)
 
 
-def quantize_fp8_weights(w, *, codes=None, scales=None):
+def quantize_fp8_weights(w, *, codes=None, scales=None, workspace=None):
     """e4m3 codes u8 [G, K, N] and f32 scales [G, N], one per output channel over
     all K, of master weights w [G, K, N] (float32 or bfloat16): what the FP8
     calls read."""
-    if codes is None and scales is None:
+    if codes is None and scales is None and workspace is None:
         r = (_calls or _plain()).quantize_fp8(w)
         if r is not None:
             return r
@@ -1009,10 +1009,14 @@ def quantize_fp8_weights(w, *, codes=None, scales=None):
     _req(w, "w", getattr(w, "dtype", None), 3)
     G, K, N = w.shape
     _req_i32(G, "the number of experts")
-    dev = _same_device(w, codes, scales)
+    if workspace is not None:
+        _req(workspace, "workspace", torch.uint8, 1)
+    dev = _same_device(w, codes, scales, workspace)
     codes = _out(codes, (G, K, N), torch.uint8, dev, "codes")
     scales = _out(scales, (G, N), torch.float32, dev, "scales")
-    _launch(dev, "quantize_fp8_weights", _ptr(w), LOGIT_DTYPES[w.dtype], K, N, G, _ptr(codes), _ptr(scales))
+    ws, need = _workspace(OP_QUANT_WEIGHTS, 0, K, N, G, dev, tile_m=LOGIT_DTYPES[w.dtype], workspace=workspace)
+    _launch(dev, "quantize_fp8_weights", _ptr(w), LOGIT_DTYPES[w.dtype], K, N, G, _ptr(codes), _ptr(scales), _ptr(ws),
+            need)
     return codes, scales
 
 

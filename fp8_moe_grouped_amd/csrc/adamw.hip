@@ -121,12 +121,20 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int64_t j, int64_t n, ui
     if (j + i < n) p[j + i] = (uint8_t)(w >> (8 * i));
 }
 
-// One element: p, m, v become their next values.
-__device__ __forceinline__ void update(const Rates& a, float g, float& p, float& m, float& v) {
-  g *= a.scale;
+// One element: p, m, v become their next values.  old_v is b2 * v.  Every product
+// and sum rounds by itself: a step of another program in f32 then chooses the same codes, which would otherwise part
+// by a whole step of theirs wherever a sum's last bit decides.
+__device__ __forceinline__ void update(const Rates& a, float g, float old_v, float& p, float& m, float& v, float& r) {
+#pragma clang fp contract(off)
+  g = g * a.scale;
   m = a.b1 * m + a.c1 * g;
-  v = a.b2 * v + a.c2 * g * g;
-  p -= a.decay * p + a.up * m / (sqrtf(v) * a.root + a.eps);
+  v = old_v + a.c2 * g * g;
+  r = sqrtf(v);
+  p = p - (a.decay * p + a.up * m / (r * a.root + a.eps));
+}
+__device__ __forceinline__ float square(float b2, float r) {
+#pragma clang fp contract(off)
+  return b2 * r * r;
 }
 
 // The tensor of a block and the block's place in it.
@@ -159,8 +167,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Tensors<State32> 
     v4f pv = load_some(p, j, n), gv = load_some(g, j, n), mv = load_some(m, j, n), vv = load_some(v, j, n);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      float pe = pv[c], me = mv[c], ve = vv[c];
-      update(a, gv[c], pe, me, ve);
+      float pe = pv[c], me = mv[c], ve, re;
+      update(a, gv[c], a.b2 * vv[c], pe, me, ve, re);
       pv[c] = pe;
       mv[c] = me;
       vv[c] = ve;
@@ -195,12 +203,14 @@ __device__ __forceinline__ uint32_t hold(const v4f x, const uint32_t (&bits)[4],
 #pragma unroll
   for (int c = 0; c < 4; ++c) top = max(top, __float_as_uint(x[c]) & 0x7FFFFFFFu);
   top = reduce<64>(top, [](uint32_t a, uint32_t b) { return max(a, b); });
-  scale = top < 0x7F800000u ? __uint_as_float(top) / kE4M3Max : __builtin_nanf("");
+  scale = top < 0x7F800000u ? __uint_as_float(top) * (1.f / kE4M3Max) : __builtin_nanf("");
   const bool some = scale > 0.f;
+  const float inverse = 1.f / scale;
+  const bool normal = inverse < __builtin_inff();   // of a scale below 2^-128 it is not
   float q[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    q[c] = some ? by_chance(__builtin_fminf(__builtin_fabsf(x[c]) / scale, kE4M3Max), bits[c]) : 0.f;
+    q[c] = some ? by_chance(__builtin_fminf(normal ? __builtin_fabsf(x[c]) * inverse : __builtin_fabsf(x[c]) / scale, kE4M3Max), bits[c]) : 0.f;
     if (POSITIVE) q[c] = some && x[c] > 0.f ? __builtin_fmaxf(q[c], 0x1p-9f) : q[c];
     else q[c] = __builtin_copysignf(q[c], x[c]);
   }
@@ -240,11 +250,11 @@ __global__ __launch_bounds__(kThreads) void adamw8_kernel(const Tensors<State8> 
       const uint32_t h = mix(kb + 0x9E3779B9u * (uint32_t)(lane * kVec + c));
       low[c] = h & 0xFFFFu;
       high[c] = h >> 16;
-      float pe = pv[c], me = mv[c], ve = rv[c] * rv[c];
-      update(a, gv[c], pe, me, ve);
+      float pe = pv[c], me = mv[c], ve, re;
+      update(a, gv[c], square(a.b2, rv[c]), pe, me, ve, re);
       pv[c] = pe;
       mv[c] = me;
-      rv[c] = sqrtf(ve);
+      rv[c] = re;
     }
     store_some(p, j, n, pv);
     float mscale, rscale;

@@ -617,14 +617,22 @@ int moe_combine_bwd(const void* dout, const void* y, const int32_t* row_of_slot,
   return FP8GMM_OK;
 }
 
-int quantize_fp8_weights(const void* w, int32_t dtype, int64_t K, int64_t N, int32_t G, uint8_t* codes_out,
-                         float* scale_out, void* stream) {
+static int check_quant_weights(int32_t dtype, int64_t K, int64_t N, int32_t G) {
   int st = check_common(0, K, N, G);
   if (st != FP8GMM_OK) return st;
-  if (dtype != FP8GMM_F32 && dtype != FP8GMM_BF16) return FP8GMM_ERR_UNSUPPORTED;
+  if (K > kMaxK || (dtype != FP8GMM_F32 && dtype != FP8GMM_BF16)) return FP8GMM_ERR_UNSUPPORTED;
+  return FP8GMM_OK;
+}
+
+int quantize_fp8_weights(const void* w, int32_t dtype, int64_t K, int64_t N, int32_t G, uint8_t* codes_out,
+                         float* scale_out, void* ws, size_t ws_bytes, void* stream) {
+  int st = check_quant_weights(dtype, K, N, G);
+  if (st != FP8GMM_OK) return st;
   if (!w || !codes_out || !scale_out) return FP8GMM_ERR_NULL;
-  if (!aligned16(w) || !aligned16(codes_out) || !aligned16(scale_out)) return FP8GMM_ERR_ALIGN;
-  if (launch_quant_weights_fp8(w, dtype == FP8GMM_BF16, G, (int)K, (int)N, codes_out, scale_out,
+  if (!aligned16(w) || !aligned16(codes_out) || !aligned16(scale_out) || !aligned16(ws)) return FP8GMM_ERR_ALIGN;
+  const size_t need = quant_weights_workspace_bytes(dtype == FP8GMM_BF16, G, (int)K, (int)N);
+  if (need > 0 && (!ws || ws_bytes < need)) return FP8GMM_ERR_WORKSPACE;
+  if (launch_quant_weights_fp8(w, dtype == FP8GMM_BF16, G, (int)K, (int)N, codes_out, scale_out, ws, kQuantPolls,
                                reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
     return FP8GMM_ERR_HIP;
   return FP8GMM_OK;
@@ -750,6 +758,9 @@ size_t fp8gmm_workspace_bytes(int32_t op, int64_t M, int64_t K, int64_t N, int32
   if (op == FP8GMM_OP_ROUTE) return check_route(M, K, N) == FP8GMM_OK ? route_workspace_bytes((int)M, (int)K) : 0;
   if (check_common(M, K, N, G) != FP8GMM_OK) return 0;
   switch (op) {
+    case FP8GMM_OP_QUANT_WEIGHTS:
+      return check_quant_weights(tile_m, K, N, G) == FP8GMM_OK
+                 ? quant_weights_workspace_bytes(tile_m == FP8GMM_BF16, G, (int)K, (int)N) : 0;
     case FP8GMM_OP_MXFP4:
       return check_mxfp4(M, M, K, N, G) == FP8GMM_OK ? mxfp4_ws(M, K) : 0;
     case FP8GMM_OP_FWD:

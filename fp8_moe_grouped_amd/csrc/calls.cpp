@@ -341,8 +341,11 @@ PyObject* quantize_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t G = w->size(0), K = w->size(1), N = w->size(2);
   PLAIN(G < (1 << 30))
   const Tensor codes = in.make({G, K, N}, kU8), scales = in.make({G, N}, kF32);
-  PLAIN(lib.quantize_fp8_weights(w->data_ptr(), type_of(*w), K, N, (int32_t)G, ptr<uint8_t>(codes),
-                                 ptr<float>(scales), in.stream()) == FP8GMM_OK)
+  const size_t need = lib.fp8gmm_workspace_bytes(FP8GMM_OP_QUANT_WEIGHTS, 0, K, N, (int32_t)G, type_of(*w));
+  Tensor ws;
+  if (need) ws = in.make({(int64_t)need}, kU8);
+  PLAIN(lib.quantize_fp8_weights(w->data_ptr(), type_of(*w), K, N, (int32_t)G, ptr<uint8_t>(codes), ptr<float>(scales),
+                                 need ? ws.data_ptr() : nullptr, need, in.stream()) == FP8GMM_OK)
   return pack({codes, scales});
   END
 }

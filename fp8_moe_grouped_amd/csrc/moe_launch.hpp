@@ -45,9 +45,12 @@ hipError_t launch_gmm_mxfp4(const uint8_t* aq, const uint8_t* ascale, const uint
                             const int* group_sizes, const int* slot_of_row, int topk, int T, int G, int M, int K,
                             int N, bool swiglu, uint16_t* out, int* status, hipStream_t stream);
 
-// Master weights to e4m3 codes and a scale per output channel.
+// Master weights to e4m3 codes and a scale per output channel.  polls: how often a block looks for another one's
+// maxima before it computes them itself, some microsecond each.
+constexpr int kQuantPolls = 20000;
+size_t quant_weights_workspace_bytes(bool bf16, int G, int K, int N);
 hipError_t launch_quant_weights_fp8(const void* w, bool bf16, int G, int K, int N, uint8_t* codes, float* scales,
-                                    hipStream_t stream);
+                                    void* ws, int polls, hipStream_t stream);
 
 // AdamW.  decay, up and root are lr * weight_decay, lr / (1 - beta1^step) and 1 / sqrt(1 - beta2^step); lr_dev and
 // step_dev replace lr and step.

@@ -4,67 +4,238 @@
 //
 // The quotient never passes 448 by more than a rounding, which the conversion brings back,
 // so nothing is clamped and a NaN stays one.
+//
+// Bound by HBM: 5 bytes an element in f32.  A strip of 64 columns keeps reads and codes in
+// whole half-lines or more: with 16 columns the codes' 16-byte pieces took as long as half of
+// the reads (8 x 7168 x 4096 f32: 357 us, 228 without the stores).  64 columns of 7168 rows are
+// 1.8 MB, four times a CU's registers, so a strip's rows are shared by blocks that exchange
+// their maxima (250 us, 4.7 TB/s; two passes over the weights 960).
 #include "moe_common.hpp"
 #include "moe_launch.hpp"
+
+#include <type_traits>
 
 namespace fp8gmm {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kColumns = 128;                       // a block's strip
-constexpr int kRows = kThreads * 4 / kColumns;
+// x / s, correctly rounded, from r = 1/s: two corrections, each with the exact remainder (the first brings the
+// quotient within a step of the truth, where the second rounds it as a division would).  s is finite and at least
+// 1e-12 / 448; remainders are subnormal only where the code is 0 whatever they are.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  float q = x * r;
+  q = __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
+  return __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
+}
 
-__device__ __forceinline__ v4f load4(const float* p) { return *reinterpret_cast<const v4f*>(p); }
-__device__ __forceinline__ v4f load4(const uint16_t* p) {
-  const v2i w = *reinterpret_cast<const v2i*>(p);
-  return (v4f){bf16_lo((uint32_t)w[0]), bf16_hi((uint32_t)w[0]), bf16_lo((uint32_t)w[1]), bf16_hi((uint32_t)w[1])};
+typedef uint16_t v8u __attribute__((ext_vector_type(8)));
+
+// A chunk of 16 bytes: 4 f32 or 8 bf16.
+template <typename TW>
+__device__ __forceinline__ float element(const v4i& w, int c) {
+  if constexpr (sizeof(TW) == 4) return __uint_as_float((uint32_t)w[c]);
+  else return c & 1 ? bf16_hi((uint32_t)w[c / 2]) : bf16_lo((uint32_t)w[c / 2]);
+}
+
+// Largest magnitude over the lanes that hold the same chunk of a row: every LPR-th of the wave.
+template <int LPR>
+__device__ __forceinline__ float same_columns_max(float v) {
+  const auto f = [](float a, float b) { return __builtin_fmaxf(a, b); };
+  if (LPR <= 4) v = f(v, dpp_row<0x124>(v));        // rotations by 4 and 8 within 16 lanes
+  if (LPR <= 8) v = f(v, dpp_row<0x128>(v));
+  if (LPR <= 16) v = f(v, other_rows<16>(v, (threadIdx.x & 16) != 0));
+  if (LPR <= 32) v = f(v, other_rows<32>(v, (threadIdx.x & 32) != 0));
+  return v;
+}
+
+// A block keeps M chunks a thread, a strip of LPR chunks x kRows * M rows, in its registers, so that the weights are
+// read once.  Where that is not all of K (parts > 1), the strip's blocks tell each other their columns' largest
+// magnitudes through `words` [total][parts][columns], zero at first: the magnitude's bits below a one, published and
+// read as one 64-bit word, so that no other order matters.  The blocks of a strip follow each other on one XCD and
+// run at the same time; one that waits longer than `polls` reads the rows of the others instead, so every wait ends.
+template <typename TW, int THREADS, int LPR, int M>
+__global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW* __restrict__ w, int K, int N, int strips,
+                                                                       int total, int parts, int polls,
+                                                                       uint64_t* __restrict__ words,
+                                                                       uint8_t* __restrict__ codes,
+                                                                       float* __restrict__ scales) {
+  constexpr int C = 16 / (int)sizeof(TW), kRows = THREADS / LPR, kWaves = THREADS / 64, kColumns = LPR * C;
+  __shared__ __attribute__((aligned(16))) float tops[kWaves][kColumns];
+  const int tid = threadIdx.x, col = tid % LPR * C, wave = tid >> 6;
+  // a strip is a part of whole cache lines, whose other parts go to the same XCD at about the same time
+  const long long b = linear_block();
+  const int per = (total + 7) / 8, slot = (int)(b / 8), strip = (int)(b % 8) * per + slot / parts, part = slot % parts;
+  if (slot / parts >= per || strip >= total) return;
+  const int g = strip / strips, n = strip % strips * kColumns + col;
+  const int first = part * (kRows * M), end = min(K, first + kRows * M);
+  // A wave's rows are inside or outside together.  Its addresses are a uniform part and 32 bits of each lane
+  // (at most 16 rows of N < 2^24), so that M of them need no registers.
+  const int row = first + tid / LPR, wave_row = __builtin_amdgcn_readfirstlane(row);
+  const size_t base = (size_t)g * K * N + (size_t)wave_row * N + (n - col);
+  const uint32_t lane_at = (uint32_t)(row - wave_row) * (uint32_t)N + (uint32_t)col;
+  const char* const from = reinterpret_cast<const char*>(w + base);
+  v4i x[M];
+#pragma unroll
+  for (int i = 0; i < M; ++i)
+    if (wave_row + i * kRows < end)
+      x[i] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(from + (size_t)i * kRows * N * sizeof(TW) +
+                                                                     lane_at * (uint32_t)sizeof(TW)));
+    else
+      x[i] = (v4i){0, 0, 0, 0};
+  float top[C] = {};
+  const auto largest = [&] {
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+      for (int c = 0; c < C; ++c) top[c] = __builtin_fmaxf(top[c], __builtin_fabsf(element<TW>(x[i], c)));
+  };
+  if constexpr (C == 4) {
+    largest();
+  } else {                                          // magnitudes are ordered as their bits are, two at a time
+    v8u t = {};
+    const v8u most = 0x7F80;
+#pragma unroll
+    for (int i = 0; i < M; ++i) t = __builtin_elementwise_max(t, __builtin_bit_cast(v8u, x[i]) & (uint16_t)0x7FFF);
+    bool nan = false;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      nan = nan || t[c] > most[c];
+      top[c] = __uint_as_float((uint32_t)t[c] << 16);
+    }
+    if (nan) {                                      // which does not count
+#pragma unroll
+      for (int c = 0; c < C; ++c) top[c] = 0.f;
+      largest();
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    top[c] = same_columns_max<LPR>(top[c]);
+    if ((tid & 63) < LPR) tops[wave][col + c] = top[c];
+  }
+  __syncthreads();
+  if (parts > 1) {
+    float most = 0.f;
+    if (tid < kColumns) {
+#pragma unroll
+      for (int v = 0; v < kWaves; ++v) most = __builtin_fmaxf(most, tops[v][tid]);
+      uint64_t* const mine = words + (size_t)strip * parts * kColumns + tid;
+      __hip_atomic_store(mine + part * kColumns, 1ull << 32 | __float_as_uint(most), __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+      for (int o = 1; o < parts; ++o) {
+        const int q = (part + o) % parts;
+        uint64_t word = 0;
+        for (int tries = 0; tries < polls && !word; ++tries) {
+          word = __hip_atomic_load(mine + q * kColumns, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          if (!word) __builtin_amdgcn_s_sleep(4);
+        }
+        if (word) {
+          most = __builtin_fmaxf(most, __uint_as_float((uint32_t)word));
+        } else {
+          const TW* const others = w + (size_t)g * K * N + (n - col) + tid;
+          const int stop = min(K, (q + 1) * kRows * M);
+          for (int k = q * kRows * M; k < stop; ++k) {
+            float v;
+            if constexpr (C == 4) v = others[(size_t)k * N];
+            else v = __uint_as_float((uint32_t)others[(size_t)k * N] << 16);
+            most = __builtin_fmaxf(most, __builtin_fabsf(v));
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (tid < kColumns) tops[0][tid] = most;
+    __syncthreads();
+  }
+  float scale[C], inverse[C];
+  bool finite = true;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float t = __builtin_fmaxf(kAmaxFloor, tops[0][col + c]);
+    if (parts == 1)
+#pragma unroll
+      for (int v = 1; v < kWaves; ++v) t = __builtin_fmaxf(t, tops[v][col + c]);
+    scale[c] = t / kE4M3Max;
+    inverse[c] = 1.f / scale[c];
+    finite = finite && __builtin_isfinite(scale[c]);
+    if (row == 0) scales[(size_t)g * N + n + c] = scale[c];
+  }
+  const auto put = [&](auto fast) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      if (wave_row + i * kRows >= end) continue;
+      int q[C / 4];
+#pragma unroll
+      for (int c = 0; c < C; c += 4) {
+        float e[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const float v = element<TW>(x[i], c + d);
+          e[d] = decltype(fast)::value ? quotient(v, scale[c + d], inverse[c + d]) : v / scale[c + d];
+        }
+        const int low = __builtin_amdgcn_cvt_pk_fp8_f32(e[0], e[1], 0, false);
+        q[c / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(e[2], e[3], low, true);
+      }
+      uint8_t* const to = codes + base + (size_t)i * kRows * N + lane_at;
+      if constexpr (C == 4) *reinterpret_cast<int*>(to) = q[0];
+      else *reinterpret_cast<v2i*>(to) = (v2i){q[0], q[C / 4 - 1]};
+    }
+  };
+  if (finite) put(std::true_type{});
+  else put(std::false_type{});
+}
+
+__global__ __launch_bounds__(256) void clear_words_kernel(v4i* __restrict__ words, long long n) {
+  const long long i = linear_block() * 256 + threadIdx.x;
+  if (i < n) words[i] = (v4i){0, 0, 0, 0};
+}
+
+// Rows of a block, f32 or bf16: 24 or 16 chunks a thread.  16 in f32 takes 274 us for 8 x 7168 x 4096 (24: 256), 24 in
+// bf16 the same 173 as 16 there and 16.7 instead of 13.2 for 8 x 768 x 2048.
+__host__ __device__ constexpr int part_rows(bool bf16) { return bf16 ? 1024 : 768; }
+constexpr int kThreads = 512;
+
+template <typename TW, int LPR>
+void strips_of(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint64_t* words,
+               hipStream_t stream) {
+  constexpr int kRows = part_rows(sizeof(TW) == 2);
+  const int strips = N / (LPR * 16 / (int)sizeof(TW)), total = strips * G, parts = (K + kRows - 1) / kRows;
+  hipLaunchKernelGGL((quant_weights_fp8_kernel<TW, kThreads, LPR, kRows * LPR / kThreads>),
+                     linear_grid((long long)((total + 7) / 8 * 8) * parts), dim3(kThreads), 0, stream, w, K, N, strips,
+                     total, parts, polls, words, codes, scales);
 }
 
 template <typename TW>
-__global__ __launch_bounds__(kThreads) void quant_weights_fp8_kernel(const TW* __restrict__ w, int K, int N,
-                                                                     uint8_t* __restrict__ codes,
-                                                                     float* __restrict__ scales) {
-  __shared__ __attribute__((aligned(16))) float tops[kRows][kColumns];
-  const int tid = threadIdx.x, col = tid % (kColumns / 4) * 4, row = tid / (kColumns / 4);
-  const int n = blockIdx.x * kColumns + col;
-  const size_t base = (size_t)blockIdx.y * K * N + n;
-  v4f top = {0.f, 0.f, 0.f, 0.f};
-  for (int k = row; k < K; k += kRows) {
-    const v4f x = load4(w + base + (size_t)k * N);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) top[c] = __builtin_fmaxf(top[c], __builtin_fabsf(x[c]));
+hipError_t quantize(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint64_t* words,
+                    hipStream_t stream) {
+  constexpr int kWide = 64 * (int)sizeof(TW) / 16;  // lanes of 64 columns
+  const long long parts = (K + part_rows(sizeof(TW) == 2) - 1) / part_rows(sizeof(TW) == 2);
+  if (parts > 1) {
+    const long long n = (long long)G * N * parts / 2;
+    hipLaunchKernelGGL(clear_words_kernel, linear_grid((n + 255) / 256), dim3(256), 0, stream,
+                       reinterpret_cast<v4i*>(words), n);
+    const hipError_t st = hipGetLastError();
+    if (st != hipSuccess) return st;
   }
-  *reinterpret_cast<v4f*>(&tops[row][col]) = top;
-  __syncthreads();
-  v4f scale;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float t = kAmaxFloor;
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) t = __builtin_fmaxf(t, tops[r][col + c]);
-    scale[c] = t / kE4M3Max;
-  }
-  if (row == 0) *reinterpret_cast<v4f*>(scales + (size_t)blockIdx.y * N + n) = scale;
-  for (int k = row; k < K; k += kRows) {
-    const v4f x = load4(w + base + (size_t)k * N);
-    int q = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] / scale[0], x[1] / scale[1], 0, false);
-    q = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] / scale[2], x[3] / scale[3], q, true);
-    *reinterpret_cast<int*>(codes + base + (size_t)k * N) = q;
-  }
+  // half the columns where that leaves CUs without a block: 512 x 4096 f32 5.7 us, with 64 columns 7.4
+  if ((long long)G * (N / 64) * parts < device_cu_count())
+    strips_of<TW, kWide / 2>(w, G, K, N, polls, codes, scales, words, stream);
+  else
+    strips_of<TW, kWide>(w, G, K, N, polls, codes, scales, words, stream);
+  return hipGetLastError();
 }
 
 }  // namespace
 
+size_t quant_weights_workspace_bytes(bool bf16, int G, int K, int N) {
+  const size_t parts = (K + part_rows(bf16) - 1) / part_rows(bf16);
+  return parts > 1 ? 8 * (size_t)G * N * parts : 0;
+}
+
 hipError_t launch_quant_weights_fp8(const void* w, bool bf16, int G, int K, int N, uint8_t* codes, float* scales,
-                                    hipStream_t stream) {
-  const dim3 grid(N / kColumns, G);
-  if (bf16)
-    hipLaunchKernelGGL(quant_weights_fp8_kernel<uint16_t>, grid, dim3(kThreads), 0, stream,
-                       static_cast<const uint16_t*>(w), K, N, codes, scales);
-  else
-    hipLaunchKernelGGL(quant_weights_fp8_kernel<float>, grid, dim3(kThreads), 0, stream, static_cast<const float*>(w),
-                       K, N, codes, scales);
-  return hipGetLastError();
+                                    void* ws, int polls, hipStream_t stream) {
+  uint64_t* const words = static_cast<uint64_t*>(ws);
+  if (bf16) return quantize(static_cast<const uint16_t*>(w), G, K, N, polls, codes, scales, words, stream);
+  return quantize(static_cast<const float*>(w), G, K, N, polls, codes, scales, words, stream);
 }
 
 }  // namespace fp8gmm

@@ -78,6 +78,7 @@ extern "C" {
 #define FP8GMM_OP_ROUTE 10      /* moe_route: pass M = T, K = E, N = k, G = 1 */
 #define FP8GMM_OP_MXFP4 11      /* gmm_mxfp4_fwd, gmm_silu_mxfp4: pass M = T (rows of x) */
 #define FP8GMM_OP_BALANCE 12    /* moe_balance_loss: pass M = T, K = E, N = k (1 without ids), G = 1 */
+#define FP8GMM_OP_QUANT_WEIGHTS 13 /* quantize_fp8_weights: pass M = 0 and the dtype as tile_m */
 
 /* types of the router's logits, of AdamW's parameters and gradients, of master weights */
 #define FP8GMM_F32 0
@@ -496,10 +497,11 @@ int adamw_step_8bit(int32_t tensors, const int64_t* sizes, void* const* params, 
  *   scale_out[g,n]   = f32( max(max_k |w[g,k,n]|, 1e-12) / 448 )
  *   codes_out[g,k,n] = e4m3fn( f32(w[g,k,n] / scale_out[g,n]) )   round to nearest even
  * NaN gets a NaN code and does not count for the scale; a column with an Inf has the
- * scale Inf, NaN codes where it is infinite and zeros elsewhere.
+ * scale Inf, NaN codes where it is infinite and zeros elsewhere.  K <= 16384.
+ * ws: fp8gmm_workspace_bytes(FP8GMM_OP_QUANT_WEIGHTS, 0, K, N, G, dtype) bytes (0 for small K).
  */
 int quantize_fp8_weights(const void* w, int32_t dtype, int64_t K, int64_t N, int32_t G, uint8_t* codes_out,
-                         float* scale_out, void* stream);
+                         float* scale_out, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * MXFP4: 4-bit e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) in

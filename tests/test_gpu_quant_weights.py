@@ -30,8 +30,8 @@ def check(codes, scales, w):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("G_,K,N", [(1, 128, 128), (2, 256, 384), (3, 768, 256), (1, 7168, 128), (2, 1152, 640),
-                                    (1, 16384, 128), (1, 16640, 256), (5, 128, 1920), (1, 32768, 128),
-                                    (2, 2048, 1536)])
+                                    (1, 16384, 128), (1, 1664, 256), (5, 128, 1920), (1, 3200, 384),
+                                    (2, 2048, 1536), (3, 896, 6144), (40, 256, 640), (9, 1152, 2176)])
 def test_quantize_fp8_weights(G_, K, N, dtype):
     import fp8_moe_grouped_amd as G
     w = weights(G_, K, N, dtype, K + N)
@@ -120,6 +120,69 @@ def test_outputs_graph_and_stream():
     assert torch.equal(o[0], eager[2][0])
 
 
+def _launch(w, codes, scales, words, polls):
+    """The library's launcher, which the C call hands its number of polls."""
+    import ctypes
+
+    import fp8_moe_grouped_amd as G
+    f = G.lib()._ZN6fp8gmm24launch_quant_weights_fp8EPKvbiiiPhPfPviP12ihipStream_t
+    p, i = ctypes.c_void_p, ctypes.c_int
+    f.argtypes = [p, ctypes.c_bool, i, i, i, p, p, p, i, p]
+    n, K, N = w.shape
+    assert f(w.data_ptr(), w.dtype == torch.bfloat16, n, K, N, codes.data_ptr(), scales.data_ptr(), words.data_ptr(),
+             polls, torch.cuda.current_stream().cuda_stream) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_block_that_waits_in_vain(dtype):
+    """With no polls, or one, blocks compute the maxima of the strip's other blocks themselves: the same bits."""
+    import fp8_moe_grouped_amd as G
+    w = weights(3, 2432, 512, dtype, 5)
+    w[1, 2000, 100] = math.nan
+    w[1, 10, 101] = -math.inf
+    dev = w.cuda()
+    want = G.quantize_fp8_weights(dev)
+    check(*want, w)
+    for polls in (0, 1):
+        codes, scales = torch.full_like(want[0], 0xAA), torch.full_like(want[1], -1.0)
+        words = torch.full((3 * 512 * 4,), -1, dtype=torch.int64, device="cuda")
+        _launch(dev, codes, scales, words, polls)
+        assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])
+
+
+def test_given_workspace():
+    import fp8_moe_grouped_amd as G
+    w = weights(2, 2048, 256, torch.float32, 6).cuda()
+    want = G.quantize_fp8_weights(w)
+    need = G.workspace_bytes(G.OP_QUANT_WEIGHTS, 0, 2048, 256, 2, G.F32)
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(2):                                           # whatever the last call left there
+        got = G.quantize_fp8_weights(w, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bool((ws[need:] == 0xFF).all())
+    with pytest.raises(ValueError, match="needed"):
+        G.quantize_fp8_weights(w, workspace=ws[:need - 1])
+    with pytest.raises(ValueError):
+        G.quantize_fp8_weights(w, workspace=ws.cpu())
+
+
+def test_two_at_once():
+    """Two streams, many blocks of each waiting for others: every call ends with the same bits."""
+    import fp8_moe_grouped_amd as G
+    ws = [weights(2, 7168, 1024, torch.float32, s).cuda() for s in range(2)]
+    want = [G.quantize_fp8_weights(w) for w in ws]
+    streams = [torch.cuda.Stream() for _ in ws]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s, w in zip(streams, ws):
+            with torch.cuda.stream(s):
+                got.append(G.quantize_fp8_weights(w))
+    torch.cuda.synchronize()
+    for i, (c, s) in enumerate(got):
+        assert torch.equal(c, want[i % 2][0]) and torch.equal(s, want[i % 2][1])
+
+
 def test_past_4_gib():
     """f32 weights of 9 GiB: the last expert's columns."""
     import fp8_moe_grouped_amd as G
@@ -144,7 +207,8 @@ def test_refusals():
             call()
     with pytest.raises(TypeError):
         G.quantize_fp8_weights(w.half())
-    for bad in (w[:, :100].contiguous(), w[:, :, :200].contiguous(), w[:0]):
+    for bad in (w[:, :100].contiguous(), w[:, :, :200].contiguous(), w[:0],
+                torch.zeros((1, 16384 + 128, 128), device="cuda")):
         with pytest.raises(G.Fp8GmmError):
             G.quantize_fp8_weights(bad)
     torch.cuda.synchronize()

@@ -111,12 +111,20 @@ def test_adamw_overlaps(bits):
 def test_quantize_refusals():
     L = _lib()
     f = lambda **a: L.quantize_fp8_weights(a.get("w", A), a.get("dt", G.F32), a.get("K", 256), a.get("N", 256),
-                                           a.get("G", 2), a.get("codes", A), a.get("scales", A), None)
+                                           a.get("G", 2), a.get("codes", A), a.get("scales", A), a.get("ws", A),
+                                           a.get("wsb", 1 << 30), None)
     for name in ("w", "codes", "scales"):
         assert f(**{name: None}) == G.ERR_NULL and f(**{name: BAD}) == G.ERR_ALIGN, name
     assert f(K=0) == G.ERR_SHAPE and f(N=-128) == G.ERR_SHAPE and f(G=0) == G.ERR_SHAPE
     assert f(K=96) == G.ERR_UNSUPPORTED and f(N=200) == G.ERR_UNSUPPORTED and f(G=1025) == G.ERR_UNSUPPORTED
     assert f(dt=2) == G.ERR_UNSUPPORTED and f(K=1 << 16, N=1 << 16) == G.ERR_UNSUPPORTED
+    assert f(K=16384 + 128) == G.ERR_UNSUPPORTED and f(ws=BAD) == G.ERR_ALIGN
+    for dt, small, large in ((G.F32, 768, 896), (G.BF16, 1024, 1152)):
+        assert L.fp8gmm_workspace_bytes(G.OP_QUANT_WEIGHTS, 0, small, 256, 2, dt) == 0
+        need = L.fp8gmm_workspace_bytes(G.OP_QUANT_WEIGHTS, 0, large, 256, 2, dt)
+        assert need == 2 * 256 * 2 * 8                        # a word for each column of each half
+        assert f(dt=dt, K=large, ws=None) == G.ERR_WORKSPACE and f(dt=dt, K=large, wsb=need - 1) == G.ERR_WORKSPACE
+    assert L.fp8gmm_workspace_bytes(G.OP_QUANT_WEIGHTS, 0, 7168, 256, 2, 2) == 0
 
 
 def test_binding_refusals():
