@@ -47,6 +47,8 @@ __device__ __forceinline__ float same_columns_max(float v) {
   return v;
 }
 
+constexpr int kTogether = 4;                        // strips side by side that one XCD takes
+
 // A block keeps M chunks a thread, a strip of LPR chunks x kRows * M rows, in its registers, so that the weights are
 // read once.  Where that is not all of K (parts > 1), the strip's blocks tell each other their columns' largest
 // magnitudes through `words` [total][parts][columns], zero at first: the magnitude's bits below a one, published and
@@ -61,10 +63,12 @@ __global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW*
   constexpr int C = 16 / (int)sizeof(TW), kRows = THREADS / LPR, kWaves = THREADS / 64, kColumns = LPR * C;
   __shared__ __attribute__((aligned(16))) float tops[kWaves][kColumns];
   const int tid = threadIdx.x, col = tid % LPR * C, wave = tid >> 6;
-  // a strip is a part of whole cache lines, whose other parts go to the same XCD at about the same time
+  // Blocks go to the 8 XCDs in turn: an XCD takes a strip's parts one after the other, and every 8th group of strips,
+  // so that all work on neighbouring columns (an XCD with an expert of its own: 270 us instead of 243).
   const long long b = linear_block();
-  const int per = (total + 7) / 8, slot = (int)(b / 8), strip = (int)(b % 8) * per + slot / parts, part = slot % parts;
-  if (slot / parts >= per || strip >= total) return;
+  const int slot = (int)(b / 8), turn = slot / parts, part = slot % parts;
+  const int strip = (turn / kTogether * 8 + (int)(b % 8)) * kTogether + turn % kTogether;
+  if (strip >= total) return;
   const int g = strip / strips, n = strip % strips * kColumns + col;
   const int first = part * (kRows * M), end = min(K, first + kRows * M);
   // A wave's rows are inside or outside together.  Its addresses are a uniform part and 32 bits of each lane
@@ -113,16 +117,20 @@ __global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW*
     if ((tid & 63) < LPR) tops[wave][col + c] = top[c];
   }
   __syncthreads();
-  if (parts > 1) {
+  constexpr int kGroups = THREADS / kColumns < kWaves ? THREADS / kColumns : kWaves;
+  if (parts > 1) {                                  // group 0 has the block's own, each group some of the others'
+    const int column = tid % kColumns, group = tid / kColumns;
     float most = 0.f;
-    if (tid < kColumns) {
+    if (group < kGroups) {
+      uint64_t* const mine = words + (size_t)strip * parts * kColumns + column;
+      if (group == 0) {
 #pragma unroll
-      for (int v = 0; v < kWaves; ++v) most = __builtin_fmaxf(most, tops[v][tid]);
-      uint64_t* const mine = words + (size_t)strip * parts * kColumns + tid;
-      __hip_atomic_store(mine + part * kColumns, 1ull << 32 | __float_as_uint(most), __ATOMIC_RELAXED,
-                         __HIP_MEMORY_SCOPE_AGENT);
-      for (int o = 1; o < parts; ++o) {
-        const int q = (part + o) % parts;
+        for (int v = 0; v < kWaves; ++v) most = __builtin_fmaxf(most, tops[v][column]);
+        __hip_atomic_store(mine + part * kColumns, 1ull << 32 | __float_as_uint(most), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+      }
+      for (int o = 1 + group; o < parts; o += kGroups) {
+        const int q = part + o < parts ? part + o : part + o - parts;
         uint64_t word = 0;
         for (int tries = 0; tries < polls && !word; ++tries) {
           word = __hip_atomic_load(mine + q * kColumns, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -131,7 +139,7 @@ __global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW*
         if (word) {
           most = __builtin_fmaxf(most, __uint_as_float((uint32_t)word));
         } else {
-          const TW* const others = w + (size_t)g * K * N + (n - col) + tid;
+          const TW* const others = w + (size_t)g * K * N + (n - col) + column;
           const int stop = min(K, (q + 1) * kRows * M);
           for (int k = q * kRows * M; k < stop; ++k) {
             float v;
@@ -143,17 +151,18 @@ __global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW*
       }
     }
     __syncthreads();
-    if (tid < kColumns) tops[0][tid] = most;
+    if (group < kGroups) tops[group][column] = most;
     __syncthreads();
   }
+  const int rows_of_tops = parts > 1 ? kGroups : kWaves;
   float scale[C], inverse[C];
   bool finite = true;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    float t = __builtin_fmaxf(kAmaxFloor, tops[0][col + c]);
-    if (parts == 1)
+    float t = kAmaxFloor;
 #pragma unroll
-      for (int v = 1; v < kWaves; ++v) t = __builtin_fmaxf(t, tops[v][col + c]);
+    for (int v = 0; v < kWaves; ++v)
+      if (v < rows_of_tops) t = __builtin_fmaxf(t, tops[v][col + c]);
     scale[c] = t / kE4M3Max;
     inverse[c] = 1.f / scale[c];
     finite = finite && __builtin_isfinite(scale[c]);
@@ -189,45 +198,66 @@ __global__ __launch_bounds__(256) void clear_words_kernel(v4i* __restrict__ word
   if (i < n) words[i] = (v4i){0, 0, 0, 0};
 }
 
-// Rows of a block, f32 or bf16: 24 or 16 chunks a thread.  16 in f32 takes 274 us for 8 x 7168 x 4096 (24: 256), 24 in
-// bf16 the same 173 as 16 there and 16.7 instead of 13.2 for 8 x 768 x 2048.
-__host__ __device__ constexpr int part_rows(bool bf16) { return bf16 ? 1024 : 768; }
 constexpr int kThreads = 512;
 
-template <typename TW, int LPR>
-void strips_of(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint64_t* words,
+// How the columns are cut into strips and the rows into parts.
+//   wide, 128 columns: whole lines of codes.  8 x 7168 x 4096 f32 243 us, with 64 columns 277; bf16 157 and 187.
+//   64 columns where a CU has fewer than 2^18 elements, whose blocks are few: 8 x 2048 x 1536 f32 32 us, wide 34; 8 x 768
+//   x 2048 bf16 12.7 and 16.6; the sides meet at 2^18 (8 x 4096 x 2048: 75 and 72, 51 and 50).
+//   32 where 64 would leave CUs without a block: 512 x 4096 f32 4.9 us, with 64 6.3.
+struct Cut {
+  int lanes, chunks, parts;
+};
+template <typename TW>
+Cut cut_of(int G, int K, int N, int cus) {
+  constexpr int kColumnLanes = 64 * (int)sizeof(TW) / 16;                // of 64 columns
+  constexpr int kChunks = sizeof(TW) == 4 ? 24 : 16;
+  const long long elements = (long long)G * K * N;
+  Cut c{2 * kColumnLanes, 24, 0};
+  if (elements < (long long)cus << 18) {
+    c = {kColumnLanes, kChunks, 0};
+    const int rows = kThreads / c.lanes * c.chunks;
+    if ((long long)G * (N / 64) * ((K + rows - 1) / rows) < cus) c = {kColumnLanes / 2, kChunks / 2, 0};
+  }
+  const int rows = kThreads / c.lanes * c.chunks;
+  c.parts = (K + rows - 1) / rows;
+  return c;
+}
+
+template <typename TW, int LPR, int M>
+hipError_t run(const TW* w, int G, int K, int N, int parts, int polls, uint8_t* codes, float* scales, uint64_t* words,
                hipStream_t stream) {
-  constexpr int kRows = part_rows(sizeof(TW) == 2);
-  const int strips = N / (LPR * 16 / (int)sizeof(TW)), total = strips * G, parts = (K + kRows - 1) / kRows;
-  hipLaunchKernelGGL((quant_weights_fp8_kernel<TW, kThreads, LPR, kRows * LPR / kThreads>),
-                     linear_grid((long long)((total + 7) / 8 * 8) * parts), dim3(kThreads), 0, stream, w, K, N, strips,
-                     total, parts, polls, words, codes, scales);
+  const int strips = N / (LPR * 16 / (int)sizeof(TW)), total = strips * G, all = 8 * kTogether;
+  const long long blocks = (long long)((total + all - 1) / all * all) * parts;
+  hipLaunchKernelGGL((quant_weights_fp8_kernel<TW, kThreads, LPR, M>), linear_grid(blocks), dim3(kThreads), 0, stream,
+                     w, K, N, strips, total, parts, polls, words, codes, scales);
+  return hipGetLastError();
 }
 
 template <typename TW>
 hipError_t quantize(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint64_t* words,
                     hipStream_t stream) {
-  constexpr int kWide = 64 * (int)sizeof(TW) / 16;  // lanes of 64 columns
-  const long long parts = (K + part_rows(sizeof(TW) == 2) - 1) / part_rows(sizeof(TW) == 2);
-  if (parts > 1) {
-    const long long n = (long long)G * N * parts / 2;
+  constexpr int kLanes = 64 * (int)sizeof(TW) / 16, kChunks = sizeof(TW) == 4 ? 24 : 16;
+  const Cut c = cut_of<TW>(G, K, N, device_cu_count());
+  if (c.parts > 1) {
+    const long long n = (long long)G * N * c.parts / 2;
     hipLaunchKernelGGL(clear_words_kernel, linear_grid((n + 255) / 256), dim3(256), 0, stream,
                        reinterpret_cast<v4i*>(words), n);
     const hipError_t st = hipGetLastError();
     if (st != hipSuccess) return st;
   }
-  // half the columns where that leaves CUs without a block: 512 x 4096 f32 5.7 us, with 64 columns 7.4
-  if ((long long)G * (N / 64) * parts < device_cu_count())
-    strips_of<TW, kWide / 2>(w, G, K, N, polls, codes, scales, words, stream);
-  else
-    strips_of<TW, kWide>(w, G, K, N, polls, codes, scales, words, stream);
-  return hipGetLastError();
+#define RUN(L, M) run<TW, L, M>(w, G, K, N, c.parts, polls, codes, scales, words, stream)
+  if (c.lanes == 2 * kLanes) return RUN(2 * kLanes, 24);
+  if (c.lanes == kLanes) return RUN(kLanes, kChunks);
+  return RUN(kLanes / 2, kChunks / 2);
+#undef RUN
 }
 
 }  // namespace
 
 size_t quant_weights_workspace_bytes(bool bf16, int G, int K, int N) {
-  const size_t parts = (K + part_rows(bf16) - 1) / part_rows(bf16);
+  // the most that any cut needs: a device with another number of CUs gives the same answer
+  const size_t rows = bf16 ? 768 : 384, parts = (K + rows - 1) / rows;
   return parts > 1 ? 8 * (size_t)G * N * parts : 0;
 }
 

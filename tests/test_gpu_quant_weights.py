@@ -150,6 +150,30 @@ def test_a_block_that_waits_in_vain(dtype):
         assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("G_,K,N", [(8, 4096, 2048), (1, 16384, 4224), (61, 1152, 1024), (520, 128, 1024)])
+def test_large(G_, K, N, dtype):
+    """Enough elements for strips of 128 columns, against the definition on the GPU: 64-bit quotients of f32 numbers
+    round to f32's own."""
+    import fp8_moe_grouped_amd as G
+    g = torch.Generator(device="cuda").manual_seed(K)
+    w = torch.randn((G_, K, N), generator=g, device="cuda") * torch.exp2(torch.randint(-9, 9, (N,), generator=g,
+                                                                                      device="cuda").float())
+    w = w.to(dtype)
+    w[0, K - 1, 5], w[G_ - 1, 0, N - 1], w[G_ // 2, K // 2, 77] = math.nan, math.inf, 1e4
+    codes, scales = G.quantize_fp8_weights(w)
+    for e in range(G_):
+        x = w[e].float()
+        top = torch.where(torch.isnan(x), 0.0, x.abs()).amax(0).clamp(min=1e-12)
+        scale = (top.double() / 448).float()
+        assert torch.equal(scales[e], scale)
+        q = (x.double() / scale.double()).float().double()
+        d = torch.exp2(torch.floor(torch.log2(q.abs().clamp(min=2.0 ** -6))).clamp(max=8) - 3)
+        want = torch.where(torch.isnan(q), 500.0, torch.round(q / d) * d)
+        got = codes[e].view(torch.float8_e4m3fn).double()
+        assert torch.equal(torch.where(torch.isnan(got), 500.0, got), want)
+
+
 def test_given_workspace():
     import fp8_moe_grouped_amd as G
     w = weights(2, 2048, 256, torch.float32, 6).cuda()

@@ -119,7 +119,7 @@ def test_quantize_refusals():
     assert f(K=96) == G.ERR_UNSUPPORTED and f(N=200) == G.ERR_UNSUPPORTED and f(G=1025) == G.ERR_UNSUPPORTED
     assert f(dt=2) == G.ERR_UNSUPPORTED and f(K=1 << 16, N=1 << 16) == G.ERR_UNSUPPORTED
     assert f(K=16384 + 128) == G.ERR_UNSUPPORTED and f(ws=BAD) == G.ERR_ALIGN
-    for dt, small, large in ((G.F32, 768, 896), (G.BF16, 1024, 1152)):
+    for dt, small, large in ((G.F32, 384, 640), (G.BF16, 768, 1152)):
         assert L.fp8gmm_workspace_bytes(G.OP_QUANT_WEIGHTS, 0, small, 256, 2, dt) == 0
         need = L.fp8gmm_workspace_bytes(G.OP_QUANT_WEIGHTS, 0, large, 256, 2, dt)
         assert need == 2 * 256 * 2 * 8                        # a word for each column of each half
