@@ -25,107 +25,154 @@ constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMaxBlocks = 256;                     // of the forward, a partial sum each
 constexpr int kOneBlock = 64;                       // tokens that one block takes by itself
+constexpr int kBackwardBlocks = 2;                  // of the gradient, a CU
+constexpr int kJoin = 32;                           // experts that a block of the join takes
 
 __host__ __device__ constexpr int padded(int E) { return (E + 63) & ~63; }
 
-// A token's exponentials in x (0 outside), their sum, and what was taken off the logits.  The sum is 0
-// only where all logits are -inf: a finite maximum adds 1, NaN and +inf make it NaN.
-template <int L, int V, typename TX>
-__device__ __forceinline__ void exponentials(float (&x)[V], int E, int at, float& top, float& total) {
-  constexpr int C = 16 / (int)sizeof(TX);
-  top = -__builtin_inff();
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+
+// A token's logits x become 2^(x log2(e) - below) with below = log2(e) max x; `total` is their sum: 0 only where all
+// logits are -inf, as a finite maximum adds 1 and NaN or +inf make it NaN.  The product and the difference round once
+// together, and what `below` was rounded by is the same in all terms, so a term is as exact as exp(x - max x).
+template <int L, int V>
+__device__ __forceinline__ void exponentials(float (&x)[V], float& total, float& lse) {
+  float top = x[0];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (expert_of<L, C>(at, i) >= E) x[i] = -__builtin_inff();
-    top = __builtin_fmaxf(top, x[i]);
-  }
+  for (int i = 1; i < V; ++i) top = __builtin_fmaxf(top, x[i]);
   top = lanes_max<L>(top);
   top = top == -__builtin_inff() ? 0.f : top;
+  const float below = top * kLog2e;
+  if (__builtin_amdgcn_ballot_w64(__builtin_fabsf(below) > 0x1p16f)) {   // `below` is 2^-8 off or more: from distances
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = __builtin_amdgcn_exp2f((x[i] - top) * kLog2e);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], kLog2e, -below));
+  }
   total = 0.f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    x[i] = expf(x[i] - top);
-    total += x[i];
-  }
+  for (int i = 0; i < V; ++i) total += x[i];
   total = lanes_sum<L>(total);
+  lse = top + kLn2 * __builtin_amdgcn_logf(total);
 }
 
-// What the losses come from: one thread an expert (E <= kThreads) with its sums over all tokens.
-__device__ __forceinline__ void write_losses(int tid, int E, float prob, int count, float z, int n,
-                                             float* __restrict__ losses, int* __restrict__ counts,
-                                             float* __restrict__ probs, int* __restrict__ tokens, bool counted) {
-  __shared__ double joint[2][kWaves];
+// Sum over the wave's four rows of 16 lanes: a lane keeps V / 4 of its V values, the columns from kept(lane), and adds
+// the other rows' of those.  An exchange of rows brings two registers' halves together, so each level halves them.
+template <int V>
+__device__ __forceinline__ void rows_sum(const float (&v)[V], float (&out)[V / 4]) {
+  float half[V / 2];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + V / 2]), false, false);
+    half[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(half[i]), __float_as_uint(half[i + V / 4]), false, false);
+    out[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+}
+template <int V>
+__device__ __forceinline__ int kept(int lane) { return (lane & 16 ? V / 2 : 0) + (lane & 32 ? V / 4 : 0); }
+
+// What a part of the experts gives the losses, one thread an expert (`inside`) of a whole wave: counts times mean
+// probabilities and counts, summed over the wave.
+struct Share {
+  double dot, slots;
+};
+__device__ __forceinline__ Share write_expert(bool inside, int e, float prob, int count, int n,
+                                              int* __restrict__ counts, float* __restrict__ probs, bool counted) {
   const float mean = n > 0 ? prob / (float)n : 0.f;
-  if (tid < E) {
-    probs[tid] = mean;
-    if (counted) counts[tid] = count;
+  if (inside) {
+    probs[e] = mean;
+    if (counted) counts[e] = count;
   }
-  const double c = tid < E ? (double)max(count, 0) : 0.0;
+  const double c = inside ? (double)max(count, 0) : 0.0;
   const auto plus = [](double a, double b) { return a + b; };
-  const double dot = reduce<64>(tid < E ? c * (double)mean : 0.0, plus), slots = reduce<64>(c, plus);
-  if ((tid & 63) == 0) {
-    joint[0][tid >> 6] = dot;
-    joint[1][tid >> 6] = slots;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    double d = 0.0, s = 0.0;
-    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) {
-      d += joint[0][w];
-      s += joint[1][w];
-    }
-    losses[0] = s > 0.0 && n > 0 ? (float)((double)E * d / s) : 0.f;
-    losses[1] = n > 0 ? z / (float)n : 0.f;
-    tokens[0] = n;
-  }
+  return {reduce<64>(inside ? c * (double)mean : 0.0, plus), reduce<64>(c, plus)};
+}
+__device__ __forceinline__ void write_losses(int E, const Share& s, float z, int n, float* __restrict__ losses,
+                                             int* __restrict__ tokens) {
+  losses[0] = s.slots > 0.0 && n > 0 ? (float)((double)E * s.dot / s.slots) : 0.f;
+  losses[1] = n > 0 ? z / (float)n : 0.f;
+  tokens[0] = n;
 }
 
-// ONE: the grid is one block, which writes the results itself.  Otherwise partial sums: probs f32 [blocks][Ep],
-// counts i32 [blocks][Ep], then z f32 [blocks] and n i32 [blocks].
-template <int L, int V, typename TX, bool ONE>
+// The workspace of a grid of several blocks: each block's sums, then the join's.
+struct Partial {
+  float* probs;                                     // [blocks][Ep]
+  int* counts;                                      // [blocks][Ep]
+  float* z;                                         // [blocks]
+  int* n;                                           // [blocks]
+  double* shares;                                   // [Ep / kJoin][2]
+  unsigned* done;
+};
+__host__ __device__ inline Partial partial_of(void* ws, int blocks, int E) {
+  Partial p;
+  const size_t Ep = padded(E);
+  p.shares = static_cast<double*>(ws);
+  p.probs = reinterpret_cast<float*>(p.shares + 2 * (Ep / kJoin));
+  p.counts = reinterpret_cast<int*>(p.probs + blocks * Ep);
+  p.z = reinterpret_cast<float*>(p.counts + blocks * Ep);
+  p.n = reinterpret_cast<int*>(p.z + blocks);
+  p.done = reinterpret_cast<unsigned*>(p.n + blocks);
+  return p;
+}
+
+// ONE: the grid is one block, which writes the results itself.
+template <int L, int V, typename TX, bool WIDE, bool ONE>
 __global__ __launch_bounds__(kThreads) void balance_kernel(const TX* __restrict__ logits, const int* __restrict__ ids,
                                                            int T, int E, int slots, float* __restrict__ losses,
                                                            int* __restrict__ counts, float* __restrict__ probs,
-                                                           int* __restrict__ tokens, float* __restrict__ part) {
+                                                           int* __restrict__ tokens, void* __restrict__ ws) {
   constexpr int C = 16 / (int)sizeof(TX);
   __shared__ __attribute__((aligned(16))) float sums[kWaves][L * V];
   __shared__ int hist[1024];
   __shared__ float zs[kWaves];
   __shared__ int ns[kWaves];
+  __shared__ Share shares[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, at = lane % L, sub = lane / L;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), blocks = gridDim.x, b = blockIdx.x;
-  const bool wide = E % C == 0;
+  // the first tokens' logits and slots are on their way while the histogram is cleared
+  const int step = blocks * kWaves * (64 / L);
+  int t = (b * kWaves + wave) * (64 / L) + sub;
+  const int each = (slots + blocks - 1) / blocks, end = min((b + 1) * each, slots);
+  int s = b * each + tid;
+  int id = ids && s < end ? ids[s] : -1;
+  Chunks<V, TX> next;
+  load_chunks<L, V, true>(logits + (size_t)t * E, E, at, t < T, WIDE, next);
   hist[tid] = 0;
   __syncthreads();
-  if (ids) {
-    const int each = (slots + blocks - 1) / blocks, end = min((b + 1) * each, slots);
-    for (int s = b * each + tid; s < end; s += kThreads) {
-      const int id = ids[s];
-      if (id >= 0 && id < E) atomicAdd(hist + id, 1);   // integers: the order does not matter
-    }
+  while (s < end && ids) {
+    const int now = id;
+    s += kThreads;
+    id = s < end ? ids[s] : -1;
+    if (now >= 0 && now < E) atomicAdd(hist + now, 1);   // integers: the order does not matter
   }
   float acc[V] = {}, z = 0.f;
   int n = 0;
-  for (int t0 = (b * kWaves + wave) * (64 / L); t0 < T; t0 += blocks * kWaves * (64 / L)) {
-    const int t = t0 + sub;
-    const bool here = t < T;
-    float x[V], top, total;
-    load_logits<L, V>(logits + (size_t)t * E, E, at, here, wide, x);
-    exponentials<L, V, TX>(x, E, at, top, total);
-    const bool some = here && total != 0.f;
-    const float share = some ? 1.f / total : 0.f, lse = some ? top + logf(total) : 0.f;
+  while (t - sub < T) {
+    float x[V], total, lse;
+    unpack<V>(next, x);
+    t += step;
+    load_chunks<L, V, true>(logits + (size_t)t * E, E, at, t < T, WIDE, next);
+    exponentials<L, V>(x, total, lse);
+    const bool some = total != 0.f;                 // 0 past the last token too
+    const float share = some ? 1.f / total : 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] += x[i] * share;
-    z += lse * lse;
+    z += some ? lse * lse : 0.f;
     n += some;
   }
+  if constexpr (L == 16) {
+    float mine[V / 4];
+    rows_sum<V>(acc, mine);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (L == 16) {                                  // the wave's four rows of lanes
-      acc[i] += other_rows<16>(acc[i], (lane & 16) != 0);
-      acc[i] += other_rows<32>(acc[i], (lane & 32) != 0);
-    }
-    if (sub == 0) sums[wave][expert_of<L, C>(at, i)] = acc[i];
+    for (int i = 0; i < V / 4; ++i) sums[wave][expert_of<L, C>(at, kept<V>(lane) + i)] = mine[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) sums[wave][expert_of<L, C>(at, i)] = acc[i];
   }
   z = lanes_sum<64>(at == 0 ? z : 0.f);
   n = reduce<64>((uint32_t)(at == 0 ? n : 0), [](uint32_t u, uint32_t v) { return u + v; });
@@ -144,71 +191,119 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const TX* __restrict_
     n += ns[w];
   }
   if (ONE) {
-    write_losses(tid, E, prob, ids ? hist[tid] : tid < E ? counts[tid] : 0, z, n, losses, counts, probs, tokens,
-                 ids != nullptr);
+    const bool inside = tid < E;
+    const Share one = write_expert(inside, tid, prob, ids || !inside ? hist[tid] : counts[tid], n, counts, probs,
+                                   ids != nullptr);
+    if (lane == 0) shares[wave] = one;
+    __syncthreads();
+    if (tid == 0) {
+      Share all = shares[0];
+      for (int w = 1; w < kWaves; ++w) {
+        all.dot += shares[w].dot;
+        all.slots += shares[w].slots;
+      }
+      write_losses(E, all, z, n, losses, tokens);
+    }
     return;
   }
   const int Ep = padded(E);
-  int* const part_c = reinterpret_cast<int*>(part + (size_t)blocks * Ep);
-  float* const part_z = reinterpret_cast<float*>(part_c + (size_t)blocks * Ep);
+  const Partial part = partial_of(ws, blocks, E);
   if (tid < Ep) {
-    part[(size_t)b * Ep + tid] = prob;
-    part_c[(size_t)b * Ep + tid] = hist[tid];
+    part.probs[(size_t)b * Ep + tid] = prob;
+    part.counts[(size_t)b * Ep + tid] = hist[tid];
   }
   if (tid == 0) {
-    part_z[b] = z;
-    reinterpret_cast<int*>(part_z + blocks)[b] = n;
+    part.z[b] = z;
+    part.n[b] = n;
+    if (b == 0) *part.done = 0;                     // the join's, which runs after this grid
   }
 }
 
-// Joins the blocks' partial sums: one block, groups of Ep threads take every group-th partial.
-__global__ __launch_bounds__(kThreads) void balance_join_kernel(const float* __restrict__ part, int blocks, int E,
+// Joins the blocks' sums for kJoin experts a block; the block that is done last writes the losses.  A chain of
+// latencies: every thread's loads go out at once, sums stay in registers but for one step through LDS.
+__global__ __launch_bounds__(kThreads) void balance_join_kernel(void* __restrict__ ws, int blocks, int E,
                                                                 float* __restrict__ losses, int* __restrict__ counts,
                                                                 float* __restrict__ probs, int* __restrict__ tokens,
                                                                 bool counted) {
-  __shared__ float sums[kThreads];
-  __shared__ int hist[kThreads];
-  __shared__ float zs[kWaves];
-  __shared__ int ns[kWaves];
-  const int tid = threadIdx.x, Ep = padded(E), groups = kThreads / Ep, group = tid / Ep, e = tid % Ep;
-  const int* const part_c = reinterpret_cast<const int*>(part + (size_t)blocks * Ep);
-  const float* const part_z = reinterpret_cast<const float*>(part_c + (size_t)blocks * Ep);
-  float prob = 0.f;
-  int count = 0;
-  if (group < groups)
-    for (int b = group; b < blocks; b += groups) {
-      prob += part[(size_t)b * Ep + e];
-      count += part_c[(size_t)b * Ep + e];
+  constexpr int kGroups = kThreads / kJoin, kEach = kMaxBlocks / kGroups;
+  static_assert(kJoin == 32, "two groups a wave");
+  __shared__ float sums[kWaves][kJoin];
+  __shared__ int hist[kWaves][kJoin];
+  __shared__ float zs[kMaxBlocks / 64];
+  __shared__ int ns[kMaxBlocks / 64];
+  const Partial part = partial_of(ws, blocks, E);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, Ep = padded(E), group = tid / kJoin, col = tid % kJoin;
+  const int e = blockIdx.x * kJoin + col;
+  const bool upper = (lane & 32) != 0;
+  float p[kEach], z = 0.f;
+  int c[kEach], n = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int b = group + i * kGroups;
+    p[i] = b < blocks ? part.probs[(size_t)b * Ep + e] : 0.f;
+    c[i] = b < blocks ? part.counts[(size_t)b * Ep + e] : 0;
+  }
+  if (tid < blocks) {
+    z = part.z[tid];
+    n = part.n[tid];
+  }
+  const int given = !counted && tid < kJoin && e < E ? counts[e] : 0;
+#pragma unroll
+  for (int i = 1; i < kEach; ++i) {
+    p[0] += p[i];
+    c[0] += c[i];
+  }
+  sums[wave][col] = p[0] + other_rows<32>(p[0], upper);
+  hist[wave][col] = c[0] + (int)other_rows<32>((uint32_t)c[0], upper);
+  if (wave < kMaxBlocks / 64) {
+    z = lanes_sum<64>(z);
+    n = reduce<64>((uint32_t)n, [](uint32_t u, uint32_t v) { return u + v; });
+    if (lane == 0) {
+      zs[wave] = z;
+      ns[wave] = n;
     }
-  sums[tid] = prob;
-  hist[tid] = count;
-  float z = tid < blocks ? part_z[tid] : 0.f;       // blocks <= kMaxBlocks <= kThreads
-  int n = tid < blocks ? reinterpret_cast<const int*>(part_z + blocks)[tid] : 0;
-  z = lanes_sum<64>(z);
-  n = reduce<64>((uint32_t)n, [](uint32_t u, uint32_t v) { return u + v; });
-  if ((tid & 63) == 0) {
-    zs[tid >> 6] = z;
-    ns[tid >> 6] = n;
   }
   __syncthreads();
-  prob = 0.f;
-  count = 0;
-  if (tid < E)
-    for (int g = 0; g < groups; ++g) {
-      prob += sums[g * Ep + tid];
-      count += hist[g * Ep + tid];
-    }
+  if (tid >= 64) return;
+  float prob = 0.f;
+  int count = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves / 2; ++w) {            // a half of the waves' sums for each half of this wave
+    prob += sums[w + (upper ? kWaves / 2 : 0)][col];
+    count += hist[w + (upper ? kWaves / 2 : 0)][col];
+  }
+  prob += other_rows<32>(prob, upper);
+  count += (int)other_rows<32>((uint32_t)count, upper);
   z = 0.f;
   n = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
+  for (int w = 0; w < kMaxBlocks / 64; ++w) {
     z += zs[w];
     n += ns[w];
   }
-  write_losses(tid, E, prob, counted ? count : tid < E ? counts[tid] : 0, z, n, losses, counts, probs, tokens, counted);
+  const Share one = write_expert(tid < kJoin && e < E, e, prob, counted ? count : given, n, counts, probs, counted);
+  unsigned before = 0;
+  if (tid == 0) {
+    __hip_atomic_store(part.shares + 2 * blockIdx.x, one.dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(part.shares + 2 * blockIdx.x + 1, one.slots, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // The device's other blocks read the shares with atomic loads alone, so that the stores have arrived is all that
+    // the count needs: a release of the agent's scope would write the whole L2 back.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    before = __hip_atomic_fetch_add(part.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if ((unsigned)__builtin_amdgcn_readfirstlane((int)before) + 1 != gridDim.x) return;
+  const int joins = gridDim.x;                      // at most 32
+  const auto plus = [](double a, double b) { return a + b; };
+  const auto of = [&](int k) {
+    const double* s = part.shares + 2 * min(tid, joins - 1) + k;
+    const double v = __hip_atomic_load(s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return reduce<64>(tid < joins ? v : 0.0, plus);
+  };
+  const Share all{of(0), of(1)};
+  if (tid == 0) write_losses(E, all, z, n, losses, tokens);
 }
 
-template <int L, int V, typename TX>
+template <int L, int V, typename TX, bool WIDE>
 __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* __restrict__ dlosses,
                                                           const TX* __restrict__ logits,
                                                           const int* __restrict__ counts,
@@ -217,92 +312,108 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* __restric
   constexpr int C = 16 / (int)sizeof(TX);
   const int lane = threadIdx.x & 63, at = lane % L, sub = lane / L;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t = (blockIdx.x * 4 + wave) * (64 / L) + sub;
-  const bool here = t < T, wide = E % C == 0;
-  float x[V], old[V], c[V], top, total;
-  load_logits<L, V>(logits + (size_t)t * E, E, at, here, wide, x);
-  if (add) load_logits<L, V>(add + (size_t)t * E, E, at, here, wide, old);
-  double slots = 0.0;
+  const int step = gridDim.x * 4 * (64 / L);
+  int t = (blockIdx.x * 4 + wave) * (64 / L) + sub;
+  Chunks<V, TX> next, next_add;
+  load_chunks<L, V, true>(logits + (size_t)t * E, E, at, t < T, WIDE, next);
+  if (add) load_chunks<L, V, false>(add + (size_t)t * E, E, at, t < T, WIDE, next_add);
+  float c[V];
+  uint64_t slots = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = expert_of<L, C>(at, i);
-    c[i] = e < E ? (float)max(counts[e], 0) : 0.f;
-    slots += (double)c[i];
+    const int e = expert_of<L, C>(at, i), count = e < E ? max(counts[e], 0) : 0;
+    slots += (uint32_t)count;
+    c[i] = (float)count;
   }
-  slots = reduce<L>(slots, [](double a, double b) { return a + b; });
-  const float mean = (float)(slots / E);
-  const int n = tokens[0];
-  const float a = n > 0 && slots > 0.0 ? (float)((double)dlosses[0] * E / ((double)n * slots)) : 0.f;
-  const float b = n > 0 ? dlosses[1] * 2.f / (float)n : 0.f;
-  exponentials<L, V, TX>(x, E, at, top, total);
-  const bool some = total != 0.f;
-  const float share = 1.f / total, lse = top + logf(total);
-  float dot = 0.f;
+  const float S = (float)reduce<L>((double)slots, [](double a, double b) { return a + b; });
+  const float mean = S / (float)E, n = (float)tokens[0];
+  const float a = n > 0.f && S > 0.f ? dlosses[0] * (float)E / n / S : 0.f;
+  const float b = n > 0.f ? dlosses[1] * 2.f / n : 0.f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    c[i] -= mean;
-    x[i] *= share;
-    dot += x[i] * c[i];
-  }
-  dot = lanes_sum<L>(dot);
+  for (int i = 0; i < V; ++i) c[i] -= mean;
+  while (t - sub < T) {
+    const int now = t;
+    float x[V], old[V], total, lse, dot = 0.f;
+    unpack<V>(next, x);
+    if (add) unpack<V>(next_add, old);
+    t += step;
+    load_chunks<L, V, true>(logits + (size_t)t * E, E, at, t < T, WIDE, next);
+    if (add) load_chunks<L, V, false>(add + (size_t)t * E, E, at, t < T, WIDE, next_add);
+    exponentials<L, V>(x, total, lse);
+    const bool some = total != 0.f;
+    const float share = 1.f / total;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    x[i] = some ? x[i] * (a * (c[i] - dot) + b * lse) : 0.f;
-    if (add) x[i] += old[i];
+    for (int i = 0; i < V; ++i) {
+      x[i] *= share;
+      dot += x[i] * c[i];
+    }
+    dot = b * lse - a * lanes_sum<L>(dot);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      x[i] = some ? x[i] * __builtin_fmaf(a, c[i], dot) : 0.f;
+      if (add) x[i] += old[i];
+    }
+    if (now < T) store_logits<L, V>(dlogits + (size_t)now * E, E, at, WIDE, x);
   }
-  if (here) store_logits<L, V>(dlogits + (size_t)t * E, E, at, wide, x);
 }
 
 int balance_blocks(int T) { return T <= kOneBlock ? 1 : std::min((T + 63) / 64, kMaxBlocks); }
 
-template <int L, int V, typename TX>
+template <int L, int V, typename TX, bool WIDE>
 hipError_t balance_impl(const TX* logits, const int* ids, int T, int E, int k, float* losses, int* counts, float* probs,
-                        int* tokens, float* part, hipStream_t stream) {
+                        int* tokens, void* ws, hipStream_t stream) {
   const int blocks = balance_blocks(T), slots = T * k;
   if (blocks == 1) {
-    hipLaunchKernelGGL((balance_kernel<L, V, TX, true>), dim3(1), dim3(kThreads), 0, stream, logits, ids, T, E, slots,
-                       losses, counts, probs, tokens, part);
+    hipLaunchKernelGGL((balance_kernel<L, V, TX, WIDE, true>), dim3(1), dim3(kThreads), 0, stream, logits, ids, T, E, slots,
+                       losses, counts, probs, tokens, ws);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((balance_kernel<L, V, TX, false>), dim3(blocks), dim3(kThreads), 0, stream, logits, ids, T, E,
-                     slots, losses, counts, probs, tokens, part);
+  hipLaunchKernelGGL((balance_kernel<L, V, TX, WIDE, false>), dim3(blocks), dim3(kThreads), 0, stream, logits, ids, T, E,
+                     slots, losses, counts, probs, tokens, ws);
   const hipError_t st = hipGetLastError();
   if (st != hipSuccess) return st;
-  hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(kThreads), 0, stream, part, blocks, E, losses, counts, probs,
-                     tokens, ids != nullptr);
+  hipLaunchKernelGGL(balance_join_kernel, dim3((E + kJoin - 1) / kJoin), dim3(kThreads), 0, stream, ws, blocks, E,
+                     losses, counts, probs, tokens, ids != nullptr);
   return hipGetLastError();
 }
 
-// The lanes of a token, from its experts; a lane holds whole 16-byte chunks (4 logits in f32, 8 in bf16).
-#define BY_EXPERTS(RUN)                                   \
-  constexpr int C = 16 / (int)sizeof(TX);                 \
-  if (E <= 16 * C) return RUN(16, C);                     \
-  if (E <= 128) return RUN(16, 8); /* f32 alone */        \
-  if (E <= 256) return RUN(16, 16);                       \
-  if (E <= 64 * C) return RUN(64, C);                     \
-  if (E <= 512) return RUN(64, 8); /* f32 alone */        \
-  return RUN(64, 16);
+// The lanes of a token, from its experts; a lane holds whole 16-byte chunks (4 logits in f32, 8 in bf16), which rows
+// of other sizes do not keep together.
+#define BY_EXPERTS(RUN)                                                       \
+  constexpr int C = 16 / (int)sizeof(TX);                                     \
+  if (E % C == 0) {                                                           \
+    BY_LANES(RUN, true)                                                       \
+  }                                                                           \
+  BY_LANES(RUN, false)
+#define BY_LANES(RUN, WIDE)                             \
+  if (E <= 16 * C) return RUN(16, C, WIDE);             \
+  if (E <= 128) return RUN(16, 8, WIDE); /* f32 alone */ \
+  if (E <= 256) return RUN(16, 16, WIDE);               \
+  if (E <= 64 * C) return RUN(64, C, WIDE);             \
+  if (E <= 512) return RUN(64, 8, WIDE); /* f32 alone */ \
+  return RUN(64, 16, WIDE);
 
 template <typename TX>
 hipError_t balance_pick(const TX* logits, const int* ids, int T, int E, int k, float* losses, int* counts, float* probs,
-                        int* tokens, float* part, hipStream_t stream) {
-#define RUN(L, V) (balance_impl<L, V, TX>(logits, ids, T, E, k, losses, counts, probs, tokens, part, stream))
+                        int* tokens, void* ws, hipStream_t stream) {
+#define RUN(L, V, WIDE) (balance_impl<L, V, TX, WIDE>(logits, ids, T, E, k, losses, counts, probs, tokens, ws, stream))
   BY_EXPERTS(RUN)
 #undef RUN
 }
 
-template <int L, int V, typename TX>
+template <int L, int V, typename TX, bool WIDE>
 hipError_t balance_bwd_impl(const float* dlosses, const TX* logits, const int* counts, const int* tokens, int T, int E,
                             const TX* add, TX* dlogits, hipStream_t stream) {
-  hipLaunchKernelGGL((balance_bwd_kernel<L, V, TX>), dim3((T + 256 / L - 1) / (256 / L)), dim3(256), 0, stream,
-                     dlosses, logits, counts, tokens, T, E, add, dlogits);
+  const int blocks = std::min((T + 256 / L - 1) / (256 / L), kBackwardBlocks * device_cu_count());
+  hipLaunchKernelGGL((balance_bwd_kernel<L, V, TX, WIDE>), dim3(blocks), dim3(256), 0, stream, dlosses, logits, counts,
+                     tokens, T, E, add, dlogits);
   return hipGetLastError();
 }
 
 template <typename TX>
 hipError_t balance_bwd_pick(const float* dlosses, const TX* logits, const int* counts, const int* tokens, int T, int E,
                             const TX* add, TX* dlogits, hipStream_t stream) {
-#define RUN(L, V) (balance_bwd_impl<L, V, TX>(dlosses, logits, counts, tokens, T, E, add, dlogits, stream))
+#define RUN(L, V, WIDE) (balance_bwd_impl<L, V, TX, WIDE>(dlosses, logits, counts, tokens, T, E, add, dlogits, stream))
   BY_EXPERTS(RUN)
 #undef RUN
 }
@@ -311,15 +422,14 @@ hipError_t balance_bwd_pick(const float* dlosses, const TX* logits, const int* c
 
 size_t balance_workspace_bytes(int T, int E) {
   const size_t blocks = balance_blocks(T);
-  return blocks == 1 ? 0 : 8 * blocks * (padded(E) + 1);
+  return blocks == 1 ? 0 : 16 * (size_t)(padded(E) / kJoin) + 8 * blocks * (padded(E) + 1) + 8;
 }
 
 hipError_t launch_balance(const void* logits, bool bf16, const int* ids, int T, int E, int k, float* losses,
                           int* counts, float* probs, int* tokens, void* ws, hipStream_t stream) {
-  float* const part = static_cast<float*>(ws);
   if (bf16)
-    return balance_pick(static_cast<const uint16_t*>(logits), ids, T, E, k, losses, counts, probs, tokens, part, stream);
-  return balance_pick(static_cast<const float*>(logits), ids, T, E, k, losses, counts, probs, tokens, part, stream);
+    return balance_pick(static_cast<const uint16_t*>(logits), ids, T, E, k, losses, counts, probs, tokens, ws, stream);
+  return balance_pick(static_cast<const float*>(logits), ids, T, E, k, losses, counts, probs, tokens, ws, stream);
 }
 
 hipError_t launch_balance_bwd(const float* dlosses, const void* logits, bool bf16, const int* counts,
