@@ -291,6 +291,15 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END
 }
 
+// n numbers of 4 bytes of a tensor's storage, from the at-th, as a tensor of their own
+Tensor piece(const Tensor& whole, int64_t at, int64_t n, at::ScalarType type) {
+  auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                   c10::scalarTypeToTypeMeta(type));
+  impl->set_storage_offset(at);
+  impl->set_sizes_contiguous({n});
+  return Tensor(std::move(impl));
+}
+
 bool logits_type(const Tensor& t) { return t.scalar_type() == kF32 || t.scalar_type() == kBf16; }
 int32_t type_of(const Tensor& t) { return t.scalar_type() == kBf16 ? FP8GMM_BF16 : FP8GMM_F32; }
 
@@ -303,8 +312,11 @@ PyObject* balance(PyObject*, PyObject* const* a, Py_ssize_t n) {
   PLAIN(in.ok && logits_type(*x) && !ids != !given)
   const int64_t T = x->size(0), E = x->size(1), k = ids ? ids->size(1) : 1;
   PLAIN(T > 0 && E < (1 << 30) && k < (1 << 30) && (!ids || ids->size(0) == T) && (!given || given->size(0) == E))
-  const Tensor losses = in.make({2}, kF32), probs = in.make({E}, kF32), tokens = in.make({1}, kI32);
-  const Tensor counts = given ? *given : in.make({E}, kI32);
+  // one allocation for the small outputs: a tensor in it costs the host a fifth of one by itself
+  const int64_t row = (E + 3) / 4 * 4;
+  const Tensor all = in.make({4 + 2 * row}, kI32);
+  const Tensor losses = piece(all, 0, 2, kF32), tokens = piece(all, 2, 1, kI32), probs = piece(all, 4, E, kF32);
+  const Tensor counts = given ? *given : piece(all, 4 + row, E, kI32);
   const size_t need = lib.fp8gmm_workspace_bytes(FP8GMM_OP_BALANCE, T, E, k, 1, 0);
   Tensor ws;
   if (need) ws = in.make({(int64_t)need}, kU8);
