@@ -26,9 +26,9 @@ namespace {
 constexpr int kBlock = 256;                         // elements that share a scale
 constexpr int kThreads = 256;
 constexpr int kMost = 48;                           // tensors a launch
-constexpr int kVec = 4;                             // elements a lane at a time
-constexpr int kPer = 4;                             // times
-constexpr int kChunk = kThreads * kVec * kPer;      // elements a block
+constexpr long long kMostBlocks = 1LL << 30;        // blocks a launch; a tensor has at most 2^25
+constexpr int kVec = 4;                             // elements a lane, f32 states
+constexpr int kVec8 = 8;                            // 8-bit states
 
 struct State32 {
   float* m;
@@ -72,74 +72,126 @@ __device__ __forceinline__ Rates rates(const AdamW& a, int64_t& step) {
   return r;
 }
 
-__device__ __forceinline__ v4f load4(const float* p) { return *reinterpret_cast<const v4f*>(p); }
-__device__ __forceinline__ v4f load4(const uint16_t* p) {
-  const v2i w = *reinterpret_cast<const v2i*>(p);
-  return (v4f){bf16_lo((uint32_t)w[0]), bf16_hi((uint32_t)w[0]), bf16_lo((uint32_t)w[1]), bf16_hi((uint32_t)w[1])};
-}
-__device__ __forceinline__ void store4(float* p, v4f v) { *reinterpret_cast<v4f*>(p) = v; }
-__device__ __forceinline__ void store4(uint16_t* p, v4f v) {
-  *reinterpret_cast<v2i*>(p) = (v2i){(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
-}
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)pack_bf16x2(v, 0.f); }
-
-// Up to 4 elements at j of n; those past the end are 0 and not written.
-template <typename T>
-__device__ __forceinline__ v4f load_some(const T* p, int64_t j, int64_t n) {
-  if (j + 4 <= n) return load4(p + j);
-  v4f v = {0.f, 0.f, 0.f, 0.f};
+// N = 4 or 8 elements at j of n, streamed; those past the end are 0 and not written.
+template <int N>
+__device__ __forceinline__ void load(const float* p, int64_t j, int64_t n, float (&x)[N]) {
+  if (j + N <= n) {
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (j + i < n) v[i] = load1(p + j + i);
-  return v;
-}
-template <typename T>
-__device__ __forceinline__ void store_some(T* p, int64_t j, int64_t n, v4f v) {
-  if (j + 4 <= n) return store4(p + j, v);
+    for (int i = 0; i < N; i += 4) {
+      const v4f w = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(p + j + i));
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (j + i < n) store1(p + j + i, v[i]);
-}
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t j, int64_t n) {
-  if (j + 4 <= n) return *reinterpret_cast<const uint32_t*>(p + j);
-  uint32_t w = 0;
+      for (int c = 0; c < 4; ++c) x[i + c] = w[c];
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (j + i < n) w |= (uint32_t)p[j + i] << (8 * i);
+    for (int i = 0; i < N; ++i) x[i] = j + i < n ? p[j + i] : 0.f;
+  }
+}
+template <int N>
+__device__ __forceinline__ void load(const uint16_t* p, int64_t j, int64_t n, float (&x)[N]) {
+  if (j + N <= n) {
+    typedef int vec __attribute__((ext_vector_type(N / 2)));
+    const vec w = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p + j));
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = i & 1 ? bf16_hi((uint32_t)w[i / 2]) : bf16_lo((uint32_t)w[i / 2]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = j + i < n ? __uint_as_float((uint32_t)p[j + i] << 16) : 0.f;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store(float* p, int64_t j, int64_t n, const float (&x)[N]) {
+  if (j + N <= n) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      __builtin_nontemporal_store((v4f){x[i], x[i + 1], x[i + 2], x[i + 3]}, reinterpret_cast<v4f*>(p + j + i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (j + i < n) p[j + i] = x[i];
+  }
+}
+template <int N>
+__device__ __forceinline__ void store(uint16_t* p, int64_t j, int64_t n, const float (&x)[N]) {
+  if (j + N <= n) {
+    typedef int vec __attribute__((ext_vector_type(N / 2)));
+    vec w;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) w[i] = (int)pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    __builtin_nontemporal_store(w, reinterpret_cast<vec*>(p + j));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (j + i < n) p[j + i] = (uint16_t)pack_bf16x2(x[i], 0.f);
+  }
+}
+// 8 codes.
+__device__ __forceinline__ v2i load_codes(const uint8_t* p, int64_t j, int64_t n) {
+  if (j + 8 <= n) return __builtin_nontemporal_load(reinterpret_cast<const v2i*>(p + j));
+  v2i w = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (j + i < n) w[i / 4] |= (int)((uint32_t)p[j + i] << (8 * (i & 3)));
   return w;
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t j, int64_t n, uint32_t w) {
-  if (j + 4 <= n) {
-    *reinterpret_cast<uint32_t*>(p + j) = w;
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t j, int64_t n, v2i w) {
+  if (j + 8 <= n) {
+    __builtin_nontemporal_store(w, reinterpret_cast<v2i*>(p + j));
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (j + i < n) p[j + i] = (uint8_t)(w >> (8 * i));
+  for (int i = 0; i < 7; ++i)
+    if (j + i < n) p[j + i] = (uint8_t)((uint32_t)w[i / 4] >> (8 * (i & 3)));
 }
 
-// One element: p, m, v become their next values.  old_v is b2 * v.  Every product
-// and sum rounds by itself: a step of another program in f32 then chooses the same codes, which would otherwise part
-// by a whole step of theirs wherever a sum's last bit decides.
-__device__ __forceinline__ void update(const Rates& a, float g, float old_v, float& p, float& m, float& v, float& r) {
-#pragma clang fp contract(off)
-  g = g * a.scale;
-  m = a.b1 * m + a.c1 * g;
-  v = old_v + a.c2 * g * g;
-  r = sqrtf(v);
-  p = p - (a.decay * p + a.up * m / (r * a.root + a.eps));
+// sqrt(x), correctly rounded, for 2^-96 <= x < inf: from the reciprocal root, root and half its reciprocal are refined
+// together, the root once more with its remainder.
+__device__ __forceinline__ float usual_root(float x) {
+  const float r = __builtin_amdgcn_rsqf(x);
+  float s = x * r, h = 0.5f * r;
+  const float e = __builtin_fmaf(-h, s, 0.5f);
+  s = __builtin_fmaf(s, e, s);
+  h = __builtin_fmaf(h, e, h);
+  return __builtin_fmaf(__builtin_fmaf(-s, s, x), h, s);
 }
-__device__ __forceinline__ float square(float b2, float r) {
-#pragma clang fp contract(off)
-  return b2 * r * r;
+template <int N>
+__device__ __forceinline__ void roots(const float (&x)[N], float (&r)[N]) {
+  constexpr uint32_t kLeast = 0x0F800000u;          // 2^-96
+  bool usual = true;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    usual = usual && __float_as_uint(x[i]) - kLeast < 0x7F800000u - kLeast;
+    r[i] = usual_root(x[i]);
+  }
+  if (!usual)                                       // zeros, tiny ones, infinities
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = sqrtf(x[i]);
 }
 
-// The tensor of a block and the block's place in it.
+// N elements: p, m, v become their next values and r the roots of v; v comes as b2 times its old value.  Every product
+// and sum rounds by itself: a step of another program in f32 then chooses the same codes, which would otherwise part by
+// a whole step of theirs wherever a sum's last bit decides.  p's quotient alone is a product with a reciprocal (2^-23).
+template <int N>
+__device__ __forceinline__ void update(const Rates& a, float (&g)[N], float (&p)[N], float (&m)[N], float (&v)[N],
+                                       float (&r)[N]) {
+#pragma clang fp contract(off)
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    g[i] = g[i] * a.scale;
+    m[i] = a.b1 * m[i] + a.c1 * g[i];
+    v[i] = v[i] + a.c2 * g[i] * g[i];
+  }
+  roots<N>(v, r);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    p[i] = p[i] - (a.decay * p[i] + a.up * m[i] * __builtin_amdgcn_rcpf(r[i] * a.root + a.eps));
+}
+
+// The tensor of this block and the block's place in it; -1 for a block past the last one.
 template <typename S>
 __device__ __forceinline__ int tensor_of(const Tensors<S>& all, uint32_t& block) {
+  block = (uint32_t)linear_block();
+  if (block >= all.blocks[all.count - 1]) return -1;
   int lo = 0, hi = all.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -150,33 +202,30 @@ __device__ __forceinline__ int tensor_of(const Tensors<S>& all, uint32_t& block)
   return lo;
 }
 
+// Bound by HBM: 28 bytes an element in f32, at 6 TB/s with streaming accesses (8 x 2048 x 1536 and 8 x 768 x 2048 in
+// 177 us, with ordinary ones 203; four times 4 elements a thread instead of one 187).
 template <typename TP, typename TG>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const Tensors<State32> all, const AdamW how) {
-  uint32_t block = blockIdx.x;
+  uint32_t block;
   const int i = tensor_of(all, block);
-  const int64_t n = all.size[i];
+  if (i < 0) return;
+  const int64_t n = all.size[i], j = ((int64_t)block * kThreads + threadIdx.x) * kVec;
+  if (j >= n) return;
   TP* const p = static_cast<TP*>(all.p[i]);
-  const TG* const g = static_cast<const TG*>(all.g[i]);
   float *const m = all.state[i].m, *const v = all.state[i].v;
+  float pv[kVec], gv[kVec], mv[kVec], vv[kVec], rv[kVec];
+  load(p, j, n, pv);
+  load(static_cast<const TG*>(all.g[i]), j, n, gv);
+  load(m, j, n, mv);
+  load(v, j, n, vv);
   int64_t step;
   const Rates a = rates(how, step);
 #pragma unroll
-  for (int u = 0; u < kPer; ++u) {
-    const int64_t j = (int64_t)block * kChunk + (u * kThreads + (int)threadIdx.x) * kVec;
-    if (j >= n) return;
-    v4f pv = load_some(p, j, n), gv = load_some(g, j, n), mv = load_some(m, j, n), vv = load_some(v, j, n);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float pe = pv[c], me = mv[c], ve, re;
-      update(a, gv[c], a.b2 * vv[c], pe, me, ve, re);
-      pv[c] = pe;
-      mv[c] = me;
-      vv[c] = ve;
-    }
-    store_some(p, j, n, pv);
-    store_some(m, j, n, mv);
-    store_some(v, j, n, vv);
-  }
+  for (int c = 0; c < kVec; ++c) vv[c] *= a.b2;
+  update<kVec>(a, gv, pv, mv, vv, rv);
+  store(p, j, n, pv);
+  store(m, j, n, mv);
+  store(v, j, n, vv);
 }
 
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
@@ -187,88 +236,103 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// |q| up to 448 to e4m3's grid, up or down by chance: floor(|q| / d + u) d, u = (bits + 1/2) / 2^16.  For a
-// normal number the 20 mantissa bits that e4m3 lacks are |q| / d's fraction, so u is added to them and they are
-// cut off.  Below 2^-6 the distance is 2^-9, which 2^-6 added to |q| makes that of the first normal numbers.
-__device__ __forceinline__ float by_chance(float q, uint32_t bits) {
-  const float low = q < 0x1p-6f ? 0x1p-6f : 0.f;
-  const uint32_t w = (__float_as_uint(q + low) + (bits << 4 | 8)) & ~0xFFFFFu;
-  return __builtin_fminf(__uint_as_float(w) - low, kE4M3Max);
+// The e4m3 code of q in [0, 448], up or down by chance: floor(q / d + u) d, u = (b + 1/2) / 2^16, noise = 16 b + 8.  For
+// a normal number the 20 mantissa bits that e4m3 lacks are q / d's fraction, so the noise is added to them and the
+// bits above are the code, but for the exponents' bias.  Below 2^-6 the distance is 2^-9, which 2^-6 added to q makes
+// that of the first normal numbers, 8 codes further on.
+__device__ __forceinline__ uint32_t by_chance(float q, uint32_t noise) {
+  const bool low = q < 0x1p-6f;
+  const uint32_t w = __float_as_uint(q + (low ? 0x1p-6f : 0.f)) + noise;
+  return min((w - ((low ? 968u : 960u) << 20)) >> 20, 126u);
 }
 
-// New codes and the scale of the wave's block of x.  bits: the element's 16 random ones.
+// New codes and the scale of x's block, which 32 lanes hold.
 template <bool POSITIVE>
-__device__ __forceinline__ uint32_t hold(const v4f x, const uint32_t (&bits)[4], float& scale) {
+__device__ __forceinline__ v2i hold(const float (&x)[kVec8], const uint32_t (&noise)[kVec8], float& scale) {
+  const auto larger = [](uint32_t a, uint32_t b) { return max(a, b); };
   uint32_t top = 0;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) top = max(top, __float_as_uint(x[c]) & 0x7FFFFFFFu);
-  top = reduce<64>(top, [](uint32_t a, uint32_t b) { return max(a, b); });
+  for (int c = 0; c < kVec8; ++c) top = max(top, __float_as_uint(x[c]) & 0x7FFFFFFFu);
+  top = reduce<16>(top, larger);
+  top = max(top, other_rows<16>(top, (threadIdx.x & 16) != 0));
   scale = top < 0x7F800000u ? __uint_as_float(top) * (1.f / kE4M3Max) : __builtin_nanf("");
-  const bool some = scale > 0.f;
   const float inverse = 1.f / scale;
-  const bool normal = inverse < __builtin_inff();   // of a scale below 2^-128 it is not
-  float q[4];
+  float q[kVec8];
+  uint32_t least = 1;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    q[c] = some ? by_chance(__builtin_fminf(normal ? __builtin_fabsf(x[c]) * inverse : __builtin_fabsf(x[c]) / scale, kE4M3Max), bits[c]) : 0.f;
-    if (POSITIVE) q[c] = some && x[c] > 0.f ? __builtin_fmaxf(q[c], 0x1p-9f) : q[c];
-    else q[c] = __builtin_copysignf(q[c], x[c]);
+  for (int c = 0; c < kVec8; ++c) q[c] = __builtin_fabsf(x[c]) * inverse;
+  if (!(scale > 0x1p-120f)) {                       // zeros, scales whose reciprocal is past f32, NaN
+#pragma unroll
+    for (int c = 0; c < kVec8; ++c) q[c] = scale > 0.f ? __builtin_fminf(__builtin_fabsf(x[c]) / scale, kE4M3Max) : 0.f;
+    least = scale > 0.f;
   }
-  return cvt_e4m3x4(q[0], q[1], q[2], q[3]);
+  v2i out = {0, 0};
+#pragma unroll
+  for (int c = 0; c < kVec8; ++c) {
+    uint32_t code = by_chance(q[c], noise[c]);
+    if (POSITIVE) code = max(code, min(__float_as_uint(x[c]), least));
+    else code |= __float_as_uint(x[c]) >> 24 & 0x80u;
+    out[c / 4] |= (int)(code << (8 * (c & 3)));
+  }
+  return out;
 }
 
+// Bound by HBM with f32 parameters and gradients (16 bytes an element, 5.3 TB/s: 8 x 7168 x 4096 and 8 x 2048 x 7168 in
+// HBMTIME) and by its some 90 instructions an element with bf16 ones (10 bytes, BF16TIME).
 template <typename TP, typename TG>
 __global__ __launch_bounds__(kThreads) void adamw8_kernel(const Tensors<State8> all, const uint64_t seed,
                                                           const AdamW how) {
-  uint32_t block = blockIdx.x;
+  static_assert(kBlock == 32 * kVec8, "32 lanes hold a block");
+  uint32_t block;
   const int i = tensor_of(all, block);
-  const int64_t n = all.size[i];
+  if (i < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t n = all.size[i], b = (int64_t)block * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t j = b * kBlock + lane * kVec8;
+  if (b * kBlock >= n) return;                      // all 32 lanes
   TP* const p = static_cast<TP*>(all.p[i]);
-  const TG* const g = static_cast<const TG*>(all.g[i]);
   const State8 s = all.state[i];
+  float pv[kVec8], gv[kVec8], mv[kVec8], rv[kVec8], vv[kVec8];
+  load(p, j, n, pv);
+  load(static_cast<const TG*>(all.g[i]), j, n, gv);
+  const v2i mw = load_codes(s.m, j, n), rw = load_codes(s.r, j, n);
+  const float ms = s.ms[b], rs = s.rs[b];
   int64_t step;
   const Rates a = rates(how, step);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int c = 0; c < kVec8; c += 4) {
+    const v2f m0 = dec_e4m3x2<false>(mw[c / 4]), m1 = dec_e4m3x2<true>(mw[c / 4]);
+    const v2f r0 = dec_e4m3x2<false>(rw[c / 4]), r1 = dec_e4m3x2<true>(rw[c / 4]);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      mv[c + d] = (d < 2 ? m0[d & 1] : m1[d & 1]) * ms;
+      const float r = (d < 2 ? r0[d & 1] : r1[d & 1]) * rs;
+      vv[c + d] = a.b2 * r * r;
+    }
+  }
+  update<kVec8>(a, gv, pv, mv, vv, rv);
+  store(p, j, n, pv);
   const uint32_t key = mix(mix((uint32_t)seed + mix((uint32_t)(seed >> 32) + mix((uint32_t)step))) +
                            (uint32_t)(all.first + i));
-  static_assert(kBlock == 64 * kVec, "a wave holds a block");
+  const uint32_t of_block = mix(key + (uint32_t)b) + 0x9E3779B9u * (uint32_t)(lane * kVec8);
+  uint32_t low[kVec8], high[kVec8];
 #pragma unroll
-  for (int u = 0; u < kPer; ++u) {
-    const int64_t b = (int64_t)block * (kChunk / kBlock) + u * (kThreads / 64) + wave, j = b * kBlock + lane * kVec;
-    if (b * kBlock >= n) return;                    // the whole wave
-    v4f pv = load_some(p, j, n), gv = load_some(g, j, n);
-    const uint32_t mw = load_codes(s.m, j, n), rw = load_codes(s.r, j, n);
-    const float ms = s.ms[b], rs = s.rs[b];
-    const v2f m0 = dec_e4m3x2<false>(mw), m1 = dec_e4m3x2<true>(mw);
-    const v2f r0 = dec_e4m3x2<false>(rw), r1 = dec_e4m3x2<true>(rw);
-    v4f mv = {m0[0] * ms, m0[1] * ms, m1[0] * ms, m1[1] * ms};
-    v4f rv = {r0[0] * rs, r0[1] * rs, r1[0] * rs, r1[1] * rs};
-    const uint32_t kb = mix(key + (uint32_t)b);
-    uint32_t low[4], high[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t h = mix(kb + 0x9E3779B9u * (uint32_t)(lane * kVec + c));
-      low[c] = h & 0xFFFFu;
-      high[c] = h >> 16;
-      float pe = pv[c], me = mv[c], ve, re;
-      update(a, gv[c], square(a.b2, rv[c]), pe, me, ve, re);
-      pv[c] = pe;
-      mv[c] = me;
-      rv[c] = re;
-    }
-    store_some(p, j, n, pv);
-    float mscale, rscale;
-    store_codes(s.m, j, n, hold<false>(mv, low, mscale));
-    store_codes(s.r, j, n, hold<true>(rv, high, rscale));
-    if (lane == 0) {
-      s.ms[b] = mscale;
-      s.rs[b] = rscale;
-    }
+  for (int c = 0; c < kVec8; ++c) {
+    const uint32_t h = mix(of_block + 0x9E3779B9u * (uint32_t)c);
+    low[c] = (h << 4 & 0xFFFF0u) | 8u;
+    high[c] = (h >> 12 & 0xFFFF0u) | 8u;
+  }
+  float mscale, rscale;
+  store_codes(s.m, j, n, hold<false>(mv, low, mscale));
+  store_codes(s.r, j, n, hold<true>(rv, high, rscale));
+  if (lane == 0) {
+    s.ms[b] = mscale;
+    s.rs[b] = rscale;
   }
 }
 
 // Launches of up to kMost tensors: state(i) is a tensor's, run(tensors, grid) launches.
-template <typename S, typename F, typename R>
+template <typename S, int kChunk, typename F, typename R>
 hipError_t in_turns(int tensors, const int64_t* sizes, void* const* params, const void* const* grads, F state, R run) {
   Tensors<S> all;
   long long blocks = 0;
@@ -283,11 +347,10 @@ hipError_t in_turns(int tensors, const int64_t* sizes, void* const* params, cons
     all.p[c] = params[i];
     all.g[c] = grads[i];
     all.state[c] = state(i);
-    // a launch has fewer than 2^32 threads, a tensor at most 2^23 blocks
     const bool last = i + 1 == tensors;
-    if (last || all.count == kMost || blocks + (sizes[i + 1] + kChunk - 1) / kChunk >= (1LL << 24)) {
+    if (last || all.count == kMost || blocks + (sizes[i + 1] + kChunk - 1) / kChunk >= kMostBlocks) {
       if (blocks > 0) {
-        const hipError_t st = run(all, dim3((unsigned)blocks));
+        const hipError_t st = run(all, linear_grid(blocks));
         if (st != hipSuccess) return st;
       }
       all.count = 0;
@@ -311,7 +374,7 @@ hipError_t in_turns(int tensors, const int64_t* sizes, void* const* params, cons
 hipError_t launch_adamw(int tensors, const int64_t* sizes, void* const* params, bool param_bf16,
                         const void* const* grads, bool grad_bf16, float* const* m, float* const* v, const AdamW& how,
                         hipStream_t stream) {
-  return in_turns<State32>(
+  return in_turns<State32, kThreads * kVec>(
       tensors, sizes, params, grads, [&](int i) { return State32{m[i], v[i]}; },
       [&](const Tensors<State32>& all, dim3 grid) {
 #define RUN(P, G) hipLaunchKernelGGL((adamw_kernel<P, G>), grid, dim3(kThreads), 0, stream, all, how)
@@ -325,7 +388,7 @@ hipError_t launch_adamw8(int tensors, const int64_t* sizes, void* const* params,
                          const void* const* grads, bool grad_bf16, uint8_t* const* m_codes, float* const* m_scales,
                          uint8_t* const* r_codes, float* const* r_scales, uint64_t seed, const AdamW& how,
                          hipStream_t stream) {
-  return in_turns<State8>(
+  return in_turns<State8, kThreads * kVec8>(
       tensors, sizes, params, grads,
       [&](int i) { return State8{m_codes[i], r_codes[i], m_scales[i], r_scales[i]}; },
       [&](const Tensors<State8>& all, dim3 grid) {
