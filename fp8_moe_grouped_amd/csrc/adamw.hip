@@ -18,7 +18,7 @@
 #include "moe_common.hpp"
 #include "moe_launch.hpp"
 
-#include <algorithm>
+#include <type_traits>
 
 namespace fp8gmm {
 namespace {
@@ -39,13 +39,17 @@ struct State8 {
   float *ms, *rs;
 };
 template <typename S>
+struct Tensor {
+  int64_t size;
+  void* p;
+  const void* g;
+  S state;
+};
+template <typename S>
 struct Tensors {
   int count, first;                                 // the first one's place in the list
   uint32_t blocks[kMost];                           // before the next tensor's first block
-  int64_t size[kMost];
-  void* p[kMost];
-  const void* g[kMost];
-  S state[kMost];
+  Tensor<S> at[kMost];
 };
 static_assert(sizeof(Tensors<State8>) + sizeof(AdamW) <= 4096, "kernel arguments");
 
@@ -59,23 +63,24 @@ __device__ __forceinline__ double power(double b, int64_t n) {
 }
 // The step's coefficients.  Those of a step on the device are computed here, by every block: some 20 rounds of
 // three f64 products.
-__device__ __forceinline__ Rates rates(const AdamW& a, int64_t& step) {
-  step = a.step_dev ? max((int64_t)1, *a.step_dev) : a.step;
-  Rates r{(float)a.beta1, (float)(1.0 - a.beta1), (float)a.beta2, (float)(1.0 - a.beta2), (float)a.eps,
-          (float)a.decay, (float)a.up, (float)a.root, a.grad_scale ? *a.grad_scale : 1.f};
+__device__ __forceinline__ Rates rates(const AdamW& a, uint32_t& step) {
+  Rates r{a.b1, a.c1, a.b2, a.c2, a.eps, a.decay, a.up, a.root, a.grad_scale ? *a.grad_scale : 1.f};
+  int64_t t = a.step;
   if (a.step_dev || a.lr_dev) {
+    if (a.step_dev) t = max((int64_t)1, *a.step_dev);
     const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
     r.decay = (float)(lr * a.weight_decay);
-    r.up = (float)(lr / (1.0 - power(a.beta1, step)));
-    r.root = 1.f / sqrtf((float)(1.0 - power(a.beta2, step)));
+    r.up = (float)(lr / (1.0 - power(a.beta1, t)));
+    r.root = 1.f / sqrtf((float)(1.0 - power(a.beta2, t)));
   }
+  step = (uint32_t)__builtin_amdgcn_readfirstlane((int)t);
   return r;
 }
 
-// N = 4 or 8 elements at j of n, streamed; those past the end are 0 and not written.
-template <int N>
+// N = 4 or 8 elements at j of n, streamed.  Without FULL those past the end are 0 and not written.
+template <bool FULL, int N>
 __device__ __forceinline__ void load(const float* p, int64_t j, int64_t n, float (&x)[N]) {
-  if (j + N <= n) {
+  if constexpr (FULL) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
       const v4f w = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(p + j + i));
@@ -87,9 +92,9 @@ __device__ __forceinline__ void load(const float* p, int64_t j, int64_t n, float
     for (int i = 0; i < N; ++i) x[i] = j + i < n ? p[j + i] : 0.f;
   }
 }
-template <int N>
+template <bool FULL, int N>
 __device__ __forceinline__ void load(const uint16_t* p, int64_t j, int64_t n, float (&x)[N]) {
-  if (j + N <= n) {
+  if constexpr (FULL) {
     typedef int vec __attribute__((ext_vector_type(N / 2)));
     const vec w = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p + j));
 #pragma unroll
@@ -99,9 +104,9 @@ __device__ __forceinline__ void load(const uint16_t* p, int64_t j, int64_t n, fl
     for (int i = 0; i < N; ++i) x[i] = j + i < n ? __uint_as_float((uint32_t)p[j + i] << 16) : 0.f;
   }
 }
-template <int N>
+template <bool FULL, int N>
 __device__ __forceinline__ void store(float* p, int64_t j, int64_t n, const float (&x)[N]) {
-  if (j + N <= n) {
+  if constexpr (FULL) {
 #pragma unroll
     for (int i = 0; i < N; i += 4)
       __builtin_nontemporal_store((v4f){x[i], x[i + 1], x[i + 2], x[i + 3]}, reinterpret_cast<v4f*>(p + j + i));
@@ -111,9 +116,9 @@ __device__ __forceinline__ void store(float* p, int64_t j, int64_t n, const floa
       if (j + i < n) p[j + i] = x[i];
   }
 }
-template <int N>
+template <bool FULL, int N>
 __device__ __forceinline__ void store(uint16_t* p, int64_t j, int64_t n, const float (&x)[N]) {
-  if (j + N <= n) {
+  if constexpr (FULL) {
     typedef int vec __attribute__((ext_vector_type(N / 2)));
     vec w;
 #pragma unroll
@@ -126,16 +131,18 @@ __device__ __forceinline__ void store(uint16_t* p, int64_t j, int64_t n, const f
   }
 }
 // 8 codes.
+template <bool FULL>
 __device__ __forceinline__ v2i load_codes(const uint8_t* p, int64_t j, int64_t n) {
-  if (j + 8 <= n) return __builtin_nontemporal_load(reinterpret_cast<const v2i*>(p + j));
+  if constexpr (FULL) return __builtin_nontemporal_load(reinterpret_cast<const v2i*>(p + j));
   v2i w = {0, 0};
 #pragma unroll
   for (int i = 0; i < 7; ++i)
     if (j + i < n) w[i / 4] |= (int)((uint32_t)p[j + i] << (8 * (i & 3)));
   return w;
 }
+template <bool FULL>
 __device__ __forceinline__ void store_codes(uint8_t* p, int64_t j, int64_t n, v2i w) {
-  if (j + 8 <= n) {
+  if constexpr (FULL) {
     __builtin_nontemporal_store(w, reinterpret_cast<v2i*>(p + j));
     return;
   }
@@ -156,14 +163,14 @@ __device__ __forceinline__ float usual_root(float x) {
 }
 template <int N>
 __device__ __forceinline__ void roots(const float (&x)[N], float (&r)[N]) {
-  constexpr uint32_t kLeast = 0x0F800000u;          // 2^-96
-  bool usual = true;
+  constexpr uint32_t kLeast = 0x0F800000u, kPast = 0x7F800000u;   // 2^-96, inf
+  uint32_t furthest = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    usual = usual && __float_as_uint(x[i]) - kLeast < 0x7F800000u - kLeast;
+    furthest = max(furthest, __float_as_uint(x[i]) - kLeast);
     r[i] = usual_root(x[i]);
   }
-  if (!usual)                                       // zeros, tiny ones, infinities
+  if (furthest >= kPast - kLeast)                   // zeros, tiny ones, infinities, NaN
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = sqrtf(x[i]);
 }
@@ -187,19 +194,18 @@ __device__ __forceinline__ void update(const Rates& a, float (&g)[N], float (&p)
     p[i] = p[i] - (a.decay * p[i] + a.up * m[i] * __builtin_amdgcn_rcpf(r[i] * a.root + a.eps));
 }
 
-// The tensor of this block and the block's place in it; -1 for a block past the last one.
+// The tensor of this block and the block's place in it; -1 for a block past the last one.  Arguments come from far on
+// their first use, so that a search would wait for each step: every lane looks at one tensor.
+static_assert(kMost <= 64, "a lane a tensor");
 template <typename S>
 __device__ __forceinline__ int tensor_of(const Tensors<S>& all, uint32_t& block) {
+  const int lane = threadIdx.x & 63;
   block = (uint32_t)linear_block();
-  if (block >= all.blocks[all.count - 1]) return -1;
-  int lo = 0, hi = all.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (block < all.blocks[mid]) hi = mid;
-    else lo = mid + 1;
-  }
-  if (lo > 0) block -= all.blocks[lo - 1];
-  return lo;
+  const uint32_t end = all.blocks[min(lane, kMost - 1)];
+  const int i = __builtin_popcountll(__builtin_amdgcn_ballot_w64(lane < all.count && block >= end));
+  if (i == all.count) return -1;
+  if (i > 0) block -= (uint32_t)__builtin_amdgcn_readlane((int)end, i - 1);
+  return i;
 }
 
 // Bound by HBM: 28 bytes an element in f32, at 6 TB/s with streaming accesses (8 x 2048 x 1536 and 8 x 768 x 2048 in
@@ -209,23 +215,29 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Tensors<State32> 
   uint32_t block;
   const int i = tensor_of(all, block);
   if (i < 0) return;
-  const int64_t n = all.size[i], j = ((int64_t)block * kThreads + threadIdx.x) * kVec;
+  const int64_t n = all.at[i].size, j = ((int64_t)block * kThreads + threadIdx.x) * kVec;
   if (j >= n) return;
-  TP* const p = static_cast<TP*>(all.p[i]);
-  float *const m = all.state[i].m, *const v = all.state[i].v;
-  float pv[kVec], gv[kVec], mv[kVec], vv[kVec], rv[kVec];
-  load(p, j, n, pv);
-  load(static_cast<const TG*>(all.g[i]), j, n, gv);
-  load(m, j, n, mv);
-  load(v, j, n, vv);
-  int64_t step;
-  const Rates a = rates(how, step);
+  const Tensor<State32> to = all.at[i];
+  TP* const p = static_cast<TP*>(to.p);
+  // one branch for all accesses: behind one for each, a load waits for the last one
+  const auto run = [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    float pv[kVec], gv[kVec], mv[kVec], vv[kVec], rv[kVec];
+    load<FULL>(p, j, n, pv);
+    load<FULL>(static_cast<const TG*>(to.g), j, n, gv);
+    load<FULL>(to.state.m, j, n, mv);
+    load<FULL>(to.state.v, j, n, vv);
+    uint32_t step;
+    const Rates a = rates(how, step);               // while the loads are on their way
 #pragma unroll
-  for (int c = 0; c < kVec; ++c) vv[c] *= a.b2;
-  update<kVec>(a, gv, pv, mv, vv, rv);
-  store(p, j, n, pv);
-  store(m, j, n, mv);
-  store(v, j, n, vv);
+    for (int c = 0; c < kVec; ++c) vv[c] *= a.b2;
+    update<kVec>(a, gv, pv, mv, vv, rv);
+    store<FULL>(p, j, n, pv);
+    store<FULL>(to.state.m, j, n, mv);
+    store<FULL>(to.state.v, j, n, vv);
+  };
+  if (j + kVec <= n) run(std::true_type{});
+  else run(std::false_type{});
 }
 
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
@@ -236,19 +248,11 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// The e4m3 code of q in [0, 448], up or down by chance: floor(q / d + u) d, u = (b + 1/2) / 2^16, noise = 16 b + 8.  For
-// a normal number the 20 mantissa bits that e4m3 lacks are q / d's fraction, so the noise is added to them and the
-// bits above are the code, but for the exponents' bias.  Below 2^-6 the distance is 2^-9, which 2^-6 added to q makes
-// that of the first normal numbers, 8 codes further on.
-__device__ __forceinline__ uint32_t by_chance(float q, uint32_t noise) {
-  const bool low = q < 0x1p-6f;
-  const uint32_t w = __float_as_uint(q + (low ? 0x1p-6f : 0.f)) + noise;
-  return min((w - ((low ? 968u : 960u) << 20)) >> 20, 126u);
-}
-
-// New codes and the scale of x's block, which 32 lanes hold.
+// New codes and the scale of x's block, which 32 lanes hold.  The conversion adds the upper 20 of its random bits to the
+// mantissa's 20 that e4m3 lacks (below 2^-6, to the distance's fraction) and cuts them off: floor(|q| / d + u) d.  The
+// bits are 16 b + 8, so u = (b + 1/2) / 2^16 and 448, a few roundings off, does not leave its code.
 template <bool POSITIVE>
-__device__ __forceinline__ v2i hold(const float (&x)[kVec8], const uint32_t (&noise)[kVec8], float& scale) {
+__device__ __forceinline__ v2i hold(const float (&x)[kVec8], const uint32_t (&random)[kVec8], float& scale) {
   const auto larger = [](uint32_t a, uint32_t b) { return max(a, b); };
   uint32_t top = 0;
 #pragma unroll
@@ -258,21 +262,24 @@ __device__ __forceinline__ v2i hold(const float (&x)[kVec8], const uint32_t (&no
   scale = top < 0x7F800000u ? __uint_as_float(top) * (1.f / kE4M3Max) : __builtin_nanf("");
   const float inverse = 1.f / scale;
   float q[kVec8];
-  uint32_t least = 1;
+  // a number above 0 counts as the smallest code's at least, which is then its code
 #pragma unroll
-  for (int c = 0; c < kVec8; ++c) q[c] = __builtin_fabsf(x[c]) * inverse;
+  for (int c = 0; c < kVec8; ++c)
+    q[c] = POSITIVE && x[c] > 0.f ? __builtin_fmaxf(x[c] * inverse, 0x1p-9f) : x[c] * inverse;
   if (!(scale > 0x1p-120f)) {                       // zeros, scales whose reciprocal is past f32, NaN
 #pragma unroll
-    for (int c = 0; c < kVec8; ++c) q[c] = scale > 0.f ? __builtin_fminf(__builtin_fabsf(x[c]) / scale, kE4M3Max) : 0.f;
-    least = scale > 0.f;
+    for (int c = 0; c < kVec8; ++c) {
+      q[c] = scale > 0.f ? __builtin_fmaxf(__builtin_fminf(x[c] / scale, kE4M3Max), -kE4M3Max) : 0.f;
+      if (POSITIVE && q[c] > 0.f) q[c] = __builtin_fmaxf(q[c], 0x1p-9f);
+    }
   }
-  v2i out = {0, 0};
+  v2i out;
 #pragma unroll
-  for (int c = 0; c < kVec8; ++c) {
-    uint32_t code = by_chance(q[c], noise[c]);
-    if (POSITIVE) code = max(code, min(__float_as_uint(x[c]), least));
-    else code |= __float_as_uint(x[c]) >> 24 & 0x80u;
-    out[c / 4] |= (int)(code << (8 * (c & 3)));
+  for (int c = 0; c < kVec8; c += 4) {
+    int w = __builtin_amdgcn_cvt_sr_fp8_f32(q[c], (int)random[c], 0, 0);
+    w = __builtin_amdgcn_cvt_sr_fp8_f32(q[c + 1], (int)random[c + 1], w, 1);
+    w = __builtin_amdgcn_cvt_sr_fp8_f32(q[c + 2], (int)random[c + 2], w, 2);
+    out[c / 4] = __builtin_amdgcn_cvt_sr_fp8_f32(q[c + 3], (int)random[c + 3], w, 3);
   }
   return out;
 }
@@ -287,44 +294,56 @@ __global__ __launch_bounds__(kThreads) void adamw8_kernel(const Tensors<State8> 
   const int i = tensor_of(all, block);
   if (i < 0) return;
   const int lane = threadIdx.x & 31;
-  const int64_t n = all.size[i], b = (int64_t)block * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t n = all.at[i].size, b = (int64_t)block * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t j = b * kBlock + lane * kVec8;
   if (b * kBlock >= n) return;                      // all 32 lanes
-  TP* const p = static_cast<TP*>(all.p[i]);
-  const State8 s = all.state[i];
+  const Tensor<State8> to = all.at[i];
+  const State8 s = to.state;
+  TP* const p = static_cast<TP*>(to.p);
+  uint32_t step = 0;
   float pv[kVec8], gv[kVec8], mv[kVec8], rv[kVec8], vv[kVec8];
-  load(p, j, n, pv);
-  load(static_cast<const TG*>(all.g[i]), j, n, gv);
-  const v2i mw = load_codes(s.m, j, n), rw = load_codes(s.r, j, n);
-  const float ms = s.ms[b], rs = s.rs[b];
-  int64_t step;
-  const Rates a = rates(how, step);
+  const auto begin = [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    load<FULL>(p, j, n, pv);
+    load<FULL>(static_cast<const TG*>(to.g), j, n, gv);
+    const v2i mw = load_codes<FULL>(s.m, j, n), rw = load_codes<FULL>(s.r, j, n);
+    const float ms = s.ms[b], rs = s.rs[b];
+    const Rates a = rates(how, step);
 #pragma unroll
-  for (int c = 0; c < kVec8; c += 4) {
-    const v2f m0 = dec_e4m3x2<false>(mw[c / 4]), m1 = dec_e4m3x2<true>(mw[c / 4]);
-    const v2f r0 = dec_e4m3x2<false>(rw[c / 4]), r1 = dec_e4m3x2<true>(rw[c / 4]);
+    for (int c = 0; c < kVec8; c += 4) {
+      const v2f m0 = dec_e4m3x2<false>(mw[c / 4]), m1 = dec_e4m3x2<true>(mw[c / 4]);
+      const v2f r0 = dec_e4m3x2<false>(rw[c / 4]), r1 = dec_e4m3x2<true>(rw[c / 4]);
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      mv[c + d] = (d < 2 ? m0[d & 1] : m1[d & 1]) * ms;
-      const float r = (d < 2 ? r0[d & 1] : r1[d & 1]) * rs;
-      vv[c + d] = a.b2 * r * r;
+      for (int d = 0; d < 4; ++d) {
+        mv[c + d] = (d < 2 ? m0[d & 1] : m1[d & 1]) * ms;
+        const float r = (d < 2 ? r0[d & 1] : r1[d & 1]) * rs;
+        vv[c + d] = a.b2 * r * r;
+      }
     }
-  }
-  update<kVec8>(a, gv, pv, mv, vv, rv);
-  store(p, j, n, pv);
-  const uint32_t key = mix(mix((uint32_t)seed + mix((uint32_t)(seed >> 32) + mix((uint32_t)step))) +
-                           (uint32_t)(all.first + i));
+    update<kVec8>(a, gv, pv, mv, vv, rv);
+    store<FULL>(p, j, n, pv);
+  };
+  const bool whole = j + kVec8 <= n;
+  if (whole) begin(std::true_type{});
+  else begin(std::false_type{});
+  const uint32_t key = mix(mix((uint32_t)seed + mix((uint32_t)(seed >> 32) + mix(step))) + (uint32_t)(all.first + i));
   const uint32_t of_block = mix(key + (uint32_t)b) + 0x9E3779B9u * (uint32_t)(lane * kVec8);
   uint32_t low[kVec8], high[kVec8];
 #pragma unroll
   for (int c = 0; c < kVec8; ++c) {
     const uint32_t h = mix(of_block + 0x9E3779B9u * (uint32_t)c);
-    low[c] = (h << 4 & 0xFFFF0u) | 8u;
-    high[c] = (h >> 12 & 0xFFFF0u) | 8u;
+    low[c] = h << 16 | 0x8000u;
+    high[c] = (h & 0xFFFF0000u) | 0x8000u;
   }
   float mscale, rscale;
-  store_codes(s.m, j, n, hold<false>(mv, low, mscale));
-  store_codes(s.r, j, n, hold<true>(rv, high, rscale));
+  const v2i mw = hold<false>(mv, low, mscale), rw = hold<true>(rv, high, rscale);
+  if (whole) {
+    store_codes<true>(s.m, j, n, mw);
+    store_codes<true>(s.r, j, n, rw);
+  } else {
+    store_codes<false>(s.m, j, n, mw);
+    store_codes<false>(s.r, j, n, rw);
+  }
   if (lane == 0) {
     s.ms[b] = mscale;
     s.rs[b] = rscale;
@@ -343,10 +362,7 @@ hipError_t in_turns(int tensors, const int64_t* sizes, void* const* params, cons
     const int c = all.count++;
     blocks += more;
     all.blocks[c] = (uint32_t)blocks;
-    all.size[c] = sizes[i];
-    all.p[c] = params[i];
-    all.g[c] = grads[i];
-    all.state[c] = state(i);
+    all.at[c] = {sizes[i], params[i], grads[i], state(i)};
     const bool last = i + 1 == tensors;
     if (last || all.count == kMost || blocks + (sizes[i + 1] + kChunk - 1) / kChunk >= kMostBlocks) {
       if (blocks > 0) {

@@ -101,23 +101,41 @@ constexpr int64_t kMaxElements = 1LL << 35;         // of an AdamW tensor: 2^23 
 // A buffer of an AdamW call.
 struct Range {
   uintptr_t begin, end;
-  bool written;
+};
+// The buffers of one list; all but the gradients are written.
+struct Column {
+  std::vector<Range> all;
+  bool written = true;
 };
 
-// Whether a written buffer overlaps another one.
-bool overlap(std::vector<Range>& all) {
-  std::sort(all.begin(), all.end(), [](const Range& a, const Range& b) { return a.begin < b.begin; });
-  uintptr_t any = 0, written = 0;                   // where the buffers so far end
-  for (const Range& r : all) {
-    if (r.begin < (r.written ? any : written)) return true;
-    any = std::max(any, r.end);
-    if (r.written) written = std::max(written, r.end);
+// Whether a written buffer overlaps another one.  A program's lists mostly are in the order of their addresses, so each
+// is sorted where it is not and then all are merged (48 tensors of 4 lists: 1 us; sorted together 3).
+template <size_t N>
+bool overlap(Column (&columns)[N]) {
+  const auto before = [](const Range& a, const Range& b) { return a.begin < b.begin; };
+  const Range* at[N];
+  const Range* end[N];
+  for (size_t c = 0; c < N; ++c) {
+    std::vector<Range>& v = columns[c].all;
+    if (!std::is_sorted(v.begin(), v.end(), before)) std::sort(v.begin(), v.end(), before);
+    at[c] = v.data();
+    end[c] = v.data() + v.size();
   }
-  return false;
+  uintptr_t any = 0, written = 0;                   // where the buffers so far end
+  for (;;) {
+    size_t next = N;
+    for (size_t c = 0; c < N; ++c)
+      if (at[c] != end[c] && (next == N || at[c]->begin < at[next]->begin)) next = c;
+    if (next == N) return false;
+    const Range r = *at[next]++;
+    if (r.begin < (columns[next].written ? any : written)) return true;
+    any = std::max(any, r.end);
+    if (columns[next].written) written = std::max(written, r.end);
+  }
 }
 
-// What both AdamW calls check; buffers(i, size, put) names a tensor's state as put(pointer, bytes).
-template <typename F>
+// What both AdamW calls check; buffers(i, size, put) names a tensor's N - 2 states as put(list, pointer, bytes, align).
+template <size_t N, typename F>
 int check_adamw(int32_t tensors, const int64_t* sizes, void* const* params, int32_t param_dtype,
                 const void* const* grads, int32_t grad_dtype, bool states, const fp8gmm_adamw* how, F buffers) {
   if (tensors < 0) return FP8GMM_ERR_SHAPE;
@@ -130,35 +148,50 @@ int check_adamw(int32_t tensors, const int64_t* sizes, void* const* params, int3
       !beta(how->beta2) || (!how->step_dev && how->step < 1))
     return FP8GMM_ERR_UNSUPPORTED;
   try {
-    std::vector<Range> all;
-    all.reserve((size_t)tensors * 6);
+    Column columns[N];
+    columns[1].written = false;
+    for (Column& c : columns) c.all.reserve((size_t)tensors);
     int st = FP8GMM_OK;
+    const auto put = [&](size_t list, const void* p, int64_t bytes, uintptr_t align) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+      if (!p) st = FP8GMM_ERR_NULL;
+      else if (at % align != 0 && st == FP8GMM_OK) st = FP8GMM_ERR_ALIGN;
+      columns[list].all.push_back({at, at + (uintptr_t)bytes});
+    };
     for (int32_t i = 0; i < tensors && st == FP8GMM_OK; ++i) {
       const int64_t n = sizes[i];
       if (n < 0 || n > kMaxElements) return FP8GMM_ERR_SHAPE;
       if (n == 0) continue;
-      const auto put = [&](const void* p, int64_t bytes, uintptr_t align = 16, bool written = true) {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-        if (!p) st = FP8GMM_ERR_NULL;
-        else if (at % align != 0 && st == FP8GMM_OK) st = FP8GMM_ERR_ALIGN;
-        all.push_back({at, at + (uintptr_t)bytes, written});
-      };
-      put(params[i], n * (param_dtype == FP8GMM_F32 ? 4 : 2));
-      put(grads[i], n * (grad_dtype == FP8GMM_F32 ? 4 : 2), 16, false);
+      put(0, params[i], n * (param_dtype == FP8GMM_F32 ? 4 : 2), 16);
+      put(1, grads[i], n * (grad_dtype == FP8GMM_F32 ? 4 : 2), 16);
       buffers(i, n, put);
     }
     if (st != FP8GMM_OK) return st;
-    return overlap(all) ? FP8GMM_ERR_OVERLAP : FP8GMM_OK;
+    return overlap(columns) ? FP8GMM_ERR_OVERLAP : FP8GMM_OK;
   } catch (...) {                                   // host memory: nothing passes the C boundary
     return FP8GMM_ERR_UNSUPPORTED;
   }
 }
 
 AdamW adamw_of(const fp8gmm_adamw& h) {
-  AdamW a{h.lr, h.beta1, h.beta2, h.eps, h.weight_decay, h.lr * h.weight_decay, 0.0, 0.0, h.step,
-          h.lr_dev, h.step_dev, h.grad_scale};
-  a.up = h.lr / (1.0 - std::pow(h.beta1, (double)h.step));
-  a.root = 1.0 / std::sqrt(1.0 - std::pow(h.beta2, (double)h.step));
+  const double t = (double)h.step;
+  AdamW a = {};
+  a.b1 = (float)h.beta1;
+  a.c1 = (float)(1.0 - h.beta1);
+  a.b2 = (float)h.beta2;
+  a.c2 = (float)(1.0 - h.beta2);
+  a.eps = (float)h.eps;
+  a.decay = (float)(h.lr * h.weight_decay);
+  a.up = (float)(h.lr / (1.0 - std::pow(h.beta1, t)));
+  a.root = (float)(1.0 / std::sqrt(1.0 - std::pow(h.beta2, t)));
+  a.lr = h.lr;
+  a.beta1 = h.beta1;
+  a.beta2 = h.beta2;
+  a.weight_decay = h.weight_decay;
+  a.step = h.step;
+  a.lr_dev = h.lr_dev;
+  a.step_dev = h.step_dev;
+  a.grad_scale = h.grad_scale;
   return a;
 }
 
@@ -641,11 +674,11 @@ int quantize_fp8_weights(const void* w, int32_t dtype, int64_t K, int64_t N, int
 int adamw_step(int32_t tensors, const int64_t* sizes, void* const* params, int32_t param_dtype,
                const void* const* grads, int32_t grad_dtype, float* const* exp_avgs, float* const* exp_avg_sqs,
                const fp8gmm_adamw* how, void* stream) {
-  const int st = check_adamw(tensors, sizes, params, param_dtype, grads, grad_dtype, exp_avgs && exp_avg_sqs, how,
-                             [&](int32_t i, int64_t n, const auto& put) {
-                               put(exp_avgs[i], 4 * n);
-                               put(exp_avg_sqs[i], 4 * n);
-                             });
+  const int st = check_adamw<4>(tensors, sizes, params, param_dtype, grads, grad_dtype, exp_avgs && exp_avg_sqs, how,
+                                [&](int32_t i, int64_t n, const auto& put) {
+                                  put(2, exp_avgs[i], 4 * n, 16);
+                                  put(3, exp_avg_sqs[i], 4 * n, 16);
+                                });
   if (st != FP8GMM_OK) return st;
   if (launch_adamw(tensors, sizes, params, param_dtype == FP8GMM_BF16, grads, grad_dtype == FP8GMM_BF16, exp_avgs,
                    exp_avg_sqs, adamw_of(*how), reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
@@ -657,14 +690,15 @@ int adamw_step_8bit(int32_t tensors, const int64_t* sizes, void* const* params, 
                     const void* const* grads, int32_t grad_dtype, uint8_t* const* m_codes, float* const* m_scales,
                     uint8_t* const* r_codes, float* const* r_scales, uint64_t seed, const fp8gmm_adamw* how,
                     void* stream) {
-  const int st = check_adamw(tensors, sizes, params, param_dtype, grads, grad_dtype,
-                             m_codes && m_scales && r_codes && r_scales, how,
-                             [&](int32_t i, int64_t n, const auto& put) {
-                               put(m_codes[i], n);
-                               put(r_codes[i], n);
-                               put(m_scales[i], (n + 255) / 256 * 4, 4);
-                               put(r_scales[i], (n + 255) / 256 * 4, 4);
-                             });
+  const int st = check_adamw<6>(tensors, sizes, params, param_dtype, grads, grad_dtype,
+                                m_codes && m_scales && r_codes && r_scales, how,
+                                [&](int32_t i, int64_t n, const auto& put) {
+                                  const int64_t scales = (n + 255) / 256 * 4;
+                                  put(2, m_codes[i], n, 16);
+                                  put(3, m_scales[i], scales, 4);
+                                  put(4, r_codes[i], n, 16);
+                                  put(5, r_scales[i], scales, 4);
+                                });
   if (st != FP8GMM_OK) return st;
   if (launch_adamw8(tensors, sizes, params, param_dtype == FP8GMM_BF16, grads, grad_dtype == FP8GMM_BF16, m_codes,
                     m_scales, r_codes, r_scales, seed, adamw_of(*how), reinterpret_cast<hipStream_t>(stream)) !=

@@ -52,10 +52,11 @@ size_t quant_weights_workspace_bytes(bool bf16, int G, int K, int N);
 hipError_t launch_quant_weights_fp8(const void* w, bool bf16, int G, int K, int N, uint8_t* codes, float* scales,
                                     void* ws, int polls, hipStream_t stream);
 
-// AdamW.  decay, up and root are lr * weight_decay, lr / (1 - beta1^step) and 1 / sqrt(1 - beta2^step); lr_dev and
-// step_dev replace lr and step.
+// AdamW's coefficients: c1 and c2 are 1 - beta, decay, up and root lr * weight_decay, lr / (1 - beta1^step) and
+// 1 / sqrt(1 - beta2^step).  lr_dev and step_dev replace lr and step.
 struct AdamW {
-  double lr, beta1, beta2, eps, weight_decay, decay, up, root;
+  float b1, c1, b2, c2, eps, decay, up, root;
+  double lr, beta1, beta2, weight_decay;
   int64_t step;
   const float* lr_dev;
   const int64_t* step_dev;

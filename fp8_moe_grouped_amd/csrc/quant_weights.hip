@@ -179,7 +179,9 @@ __global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW*
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           const float v = element<TW>(x[i], c + d);
-          e[d] = decltype(fast)::value ? quotient(v, scale[c + d], inverse[c + d]) : v / scale[c + d];
+          if constexpr (!decltype(fast)::value) e[d] = v / scale[c + d];
+          else if constexpr (C == 4) e[d] = quotient(v, scale[c + d], inverse[c + d]);
+          else e[d] = div_by_scale(v, scale[c + d], inverse[c + d]);   // enough for bf16 values and their scales
         }
         const int low = __builtin_amdgcn_cvt_pk_fp8_f32(e[0], e[1], 0, false);
         q[c / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(e[2], e[3], low, true);
