@@ -14,6 +14,15 @@ Training (forward, then backward):
     dy, dweights = moe_combine_bwd(dout, ...);  dxp, dwi, dwo = moe_ffn_fp8_bwd(dy, ...)
     dlogits = moe_route_bwd(dweights, ...);     dx = moe_combine(dxp) + dlogits @ router^T
 
+with the router's auxiliary losses, where they are asked for, between the two (their gradient joins the router's own):
+
+    losses, counts, probs, tokens = moe_balance_loss(logits, counts=group_sizes)
+    dlogits = moe_balance_loss_bwd(coefficients, logits, counts, tokens, add=dlogits)
+
+and then the update of the f32 master weights, whose new codes the next step reads:
+
+    adamw_step([router, wi, wo], gradients, ...)  or  adamw_step_8bit;   quantize_fp8_weights(wi), (wo)
+
 Decoding has no dispatch of its own: the first product gathers its rows.
 
     h = gmm_silu_mxfp4(x, ..., slot_of_row, topk);  y = gmm_mxfp4_fwd(h, ...);  out = moe_combine(y, ...)
@@ -31,20 +40,31 @@ if __name__ == "__main__":
 import fp8_moe_grouped_amd as lib
 
 
-def quantize_fp8_weights(w):
-    """e4m3 codes [G, K, N] and f32 scales [G, N] of bf16 weights [G, K, N]."""
-    scale = w.float().abs().amax(1).clamp(min=1e-12) / 448
-    return (w.float() / scale.unsqueeze(1)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8), scale
-
-
 class MoeLayer:
-    """SwiGLU experts behind a top-k softmax router.  Master weights: router
-    f32 [H, E], wi bf16 [E, H, 2I] ([gate | up]), wo bf16 [E, I, H]."""
+    """SwiGLU experts behind a top-k softmax router: router f32 [H, E], wi
+    bf16 [E, H, 2I] ([gate | up]), wo bf16 [E, I, H].  Training keeps f32 masters
+    of the experts' weights, whose e4m3 codes the products read."""
 
     def __init__(self, router, wi, wo, topk):
         self.router, self.topk = router, topk
-        self.wi, self.wo = quantize_fp8_weights(wi), quantize_fp8_weights(wo)
+        self.wi, self.wo = lib.quantize_fp8_weights(wi), lib.quantize_fp8_weights(wo)
         self.wi4, self.wo4 = lib.quantize_mxfp4_weights(wi), lib.quantize_mxfp4_weights(wo)
+
+    def start_training(self, bits=32):
+        """Masters and AdamW's states, in 32 bits or 8."""
+        values = lambda w: lib.dequantize_fp8_codes(*w).float()
+        self.masters = [self.router, values(self.wi), values(self.wo)]
+        self.bits, self.step = bits, 0
+        self.states = (lib.adamw_8bit_states(self.masters) if bits == 8 else
+                       [[torch.zeros_like(w) for w in self.masters] for _ in range(2)])
+
+    def update(self, gradients, lr, **how):
+        """One AdamW step on (drouter, dwi, dwo), and the experts' new codes."""
+        self.step += 1
+        step = lib.adamw_step_8bit if self.bits == 8 else lib.adamw_step
+        step(self.masters, list(gradients), *self.states, lr=lr, step=self.step, **how)
+        for (codes, scales), w in zip((self.wi, self.wo), self.masters[1:]):
+            lib.quantize_fp8_weights(w, codes=codes, scales=scales)
 
     def route(self, x):
         logits = x.float() @ self.router
@@ -58,12 +78,20 @@ class MoeLayer:
         out = lib.moe_combine(y, r.row_of_slot, r.weights)
         return out, (x, logits, r, xp, y, h, preact)
 
-    def backward(self, dout, saved):
-        """(dx bf16 [T, H], drouter f32 [H, E], dwi f32 [E, H, 2I], dwo f32 [E, I, H])."""
+    def balance(self, saved):
+        """The router's auxiliary losses of a forward pass."""
+        _, logits, r, *_ = saved
+        return lib.moe_balance_loss(logits, counts=r.group_sizes)
+
+    def backward(self, dout, saved, balance=None, coefficients=None):
+        """(dx bf16 [T, H], drouter f32 [H, E], dwi f32 [E, H, 2I], dwo f32 [E, I, H]), with balance's losses
+        weighted by coefficients f32 [2]."""
         x, logits, r, xp, y, h, preact = saved
         dy, dweights = lib.moe_combine_bwd(dout, y, r.row_of_slot, r.weights)
         dxp, dwi, dwo, _ = lib.moe_ffn_fp8_bwd(xp, h, preact, dy, *self.wi, *self.wo, r.group_sizes)
         dlogits = lib.moe_route_bwd(dweights, logits, r.ids, r.weights)
+        if balance is not None:
+            lib.moe_balance_loss_bwd(coefficients, logits, balance.counts, balance.tokens, add=dlogits, out=dlogits)
         dx = (lib.moe_combine(dxp, r.row_of_slot).float() + dlogits @ self.router.t()).to(torch.bfloat16)
         return dx, x.float().t() @ dlogits, dwi, dwo
 
@@ -104,13 +132,19 @@ def main():
     x = torch.randn((a.tokens, a.hidden), device="cuda").to(torch.bfloat16)
     dout = (1e-3 * torch.randn((a.tokens, a.hidden), device="cuda")).to(torch.bfloat16)
 
+    coefficients = torch.tensor([1e-2, 1e-3], device="cuda")
+    layer.start_training()
+
     def step():
         out, saved = layer.forward(x)
-        return layer.backward(dout, saved)
+        return layer.backward(dout, saved, layer.balance(saved), coefficients)
+
+    gradients = step()[1:]
 
     print(f"{a.tokens} tokens, {a.experts} experts of {a.hidden} x {a.inner}, top {a.topk}")
     print(f"  forward            {_milliseconds(lambda: layer.forward(x)):8.3f} ms")
     print(f"  forward + backward {_milliseconds(step):8.3f} ms")
+    print(f"  update             {_milliseconds(lambda: layer.update(gradients, 1e-4)):8.3f} ms")
     for n in (1, 32, a.tokens):
         print(f"  decode {n:6d}      {_milliseconds(lambda: layer.decode(x[:n])):8.3f} ms")
 
