@@ -5,6 +5,9 @@
 
 namespace fp8gmm {
 
+__device__ __forceinline__ float load_logit(const float* x) { return *x; }
+__device__ __forceinline__ float load_logit(const uint16_t* x) { return __uint_as_float((uint32_t)*x << 16); }
+
 // Lane `at` of the L that share a token holds the experts of chunks at, at + L, ..: C logits each (16 bytes).
 template <int L, int C>
 __device__ __forceinline__ int expert_of(int at, int i) { return (i / C * L + at) * C + i % C; }
@@ -55,11 +58,27 @@ __device__ __forceinline__ void unpack(const Chunks<V, TX>& y, float (&x)[V]) {
     x[i] = C == 4 ? __uint_as_float(w) : i & 1 ? bf16_hi(w) : bf16_lo(w);
   }
 }
+// The same as values at once, 0 for none.
 template <int L, int V, typename TX>
 __device__ __forceinline__ void load_logits(const TX* row, int E, int at, bool here, bool wide, float (&x)[V]) {
-  Chunks<V, TX> y;
-  load_chunks<L, V, false>(row, E, at, here, wide, y);
-  unpack<V>(y, x);
+  constexpr int C = 16 / (int)sizeof(TX);
+  if (wide) {                                       // E is a multiple of C: a chunk is inside or outside
+#pragma unroll
+    for (int i = 0; i < V; i += C) {
+      const int e = expert_of<L, C>(at, i);
+      const v4i w = here && e < E ? *reinterpret_cast<const v4i*>(row + e) : (v4i){0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        x[i + c] = C == 4 ? __uint_as_float((uint32_t)w[c % 4])
+                          : (c & 1 ? bf16_hi((uint32_t)w[c / 2 % 4]) : bf16_lo((uint32_t)w[c / 2 % 4]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = expert_of<L, C>(at, i);
+      x[i] = here && e < E ? load_logit(row + e) : 0.f;
+    }
+  }
 }
 
 // A row of the lanes' values, rounded once to the logits' type.

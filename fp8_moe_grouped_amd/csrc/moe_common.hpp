@@ -19,10 +19,10 @@ __device__ __forceinline__ void copy4(const void* src, void* lds_wave_base) {
 
 // ----------------------------------------------------------------- long grids
 
-// A launch dimension holds fewer than 2^32 threads: longer grids of 256-thread blocks continue in y.  Blocks past
-// the last one exist, so a kernel checks its index.
-inline dim3 linear_grid(long long blocks) {
-  constexpr long long kWide = 1 << 23;
+// A launch dimension holds fewer than 2^32 threads: longer grids continue in y.  Blocks past the last one exist, so a
+// kernel checks its index.
+inline dim3 linear_grid(long long blocks, int threads = 256) {
+  const long long kWide = (1LL << 31) / threads;
   if (blocks <= kWide) return dim3((unsigned)blocks);
   return dim3((unsigned)kWide, (unsigned)((blocks + kWide - 1) / kWide));
 }

@@ -5,11 +5,11 @@
 // The quotient never passes 448 by more than a rounding, which the conversion brings back,
 // so nothing is clamped and a NaN stays one.
 //
-// Bound by HBM: 5 bytes an element in f32.  A strip of 64 columns keeps reads and codes in
+// Bound by HBM: 5 bytes an element in f32.  A strip of 64 columns or more keeps reads and codes in
 // whole half-lines or more: with 16 columns the codes' 16-byte pieces took as long as half of
-// the reads (8 x 7168 x 4096 f32: 357 us, 228 without the stores).  64 columns of 7168 rows are
-// 1.8 MB, four times a CU's registers, so a strip's rows are shared by blocks that exchange
-// their maxima (250 us, 4.7 TB/s; two passes over the weights 960).
+// the reads (8 x 7168 x 4096 f32: 357 us, 228 without the stores).  128 columns of 7168 rows are
+// 3.7 MB, eight times a CU's registers, so a strip's rows are shared by blocks that exchange
+// their maxima (235 us, 5 TB/s; two passes over the weights 960).
 #include "moe_common.hpp"
 #include "moe_launch.hpp"
 
@@ -19,12 +19,12 @@ namespace fp8gmm {
 namespace {
 
 // x / s, correctly rounded, from r = 1/s: two corrections, each with the exact remainder (the first brings the
-// quotient within a step of the truth, where the second rounds it as a division would).  s is finite and at least
-// 1e-12 / 448; remainders are subnormal only where the code is 0 whatever they are.
+// quotient within a step of the truth, where the second rounds it as a division would).  The remainder comes negated,
+// which keeps the sign of a zero.  s is finite and at least 1e-12 / 448; remainders are subnormal only where the code is
+// 0 whatever they are.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
-  float q = x * r;
-  q = __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
-  return __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
+  const float q = div_by_scale(x, s, r);
+  return __builtin_fmaf(-__builtin_fmaf(q, s, -x), r, q);
 }
 
 typedef uint16_t v8u __attribute__((ext_vector_type(8)));
@@ -200,58 +200,48 @@ __global__ __launch_bounds__(256) void clear_words_kernel(v4i* __restrict__ word
   if (i < n) words[i] = (v4i){0, 0, 0, 0};
 }
 
+// A strip's lanes and a thread's chunks, by how many elements a CU has: wide strips for whole lines of codes, narrow
+// ones for enough blocks.  Both sides in us:
+//   f32   128 columns or 64: 8 x 7168 x 3840 240, 257; 8 x 3200 x 3328 92, 86
+//         64 or 32: 2 x 3840 x 2304 24.1, 27.4; 8 x 768 x 2048 15.6, 15.1;   32 or 16: 4 x 4992 x 256 10.6, 12.6;
+//         1 x 1024 x 1024 6.9, 4.4
+//   bf16  128 or 64: 8 x 7168 x 3840 149, 169; 2 x 8192 x 4096 50, 56;   64 or 32: 8 x 768 x 2048 12.0, 13.3;
+//         1 x 6912 x 640 14.6, 11.3
+// A block of 512 threads keeps 384 rows of 128 columns in f32, 768 of them in bf16 and of 64 or 32 in f32, 1024 otherwise.
 constexpr int kThreads = 512;
-
-// How the columns are cut into strips and the rows into parts.
-//   wide, 128 columns: whole lines of codes.  8 x 7168 x 4096 f32 243 us, with 64 columns 277; bf16 157 and 187.
-//   64 columns where a CU has fewer than 2^18 elements, whose blocks are few: 8 x 2048 x 1536 f32 32 us, wide 34; 8 x 768
-//   x 2048 bf16 12.7 and 16.6; the sides meet at 2^18 (8 x 4096 x 2048: 75 and 72, 51 and 50).
-//   32 where 64 would leave CUs without a block: 512 x 4096 f32 4.9 us, with 64 6.3.
-struct Cut {
-  int lanes, chunks, parts;
-};
-template <typename TW>
-Cut cut_of(int G, int K, int N, int cus) {
-  constexpr int kColumnLanes = 64 * (int)sizeof(TW) / 16;                // of 64 columns
-  constexpr int kChunks = sizeof(TW) == 4 ? 24 : 16;
-  const long long elements = (long long)G * K * N;
-  Cut c{2 * kColumnLanes, 24, 0};
-  if (elements < (long long)cus << 18) {
-    c = {kColumnLanes, kChunks, 0};
-    const int rows = kThreads / c.lanes * c.chunks;
-    if ((long long)G * (N / 64) * ((K + rows - 1) / rows) < cus) c = {kColumnLanes / 2, kChunks / 2, 0};
-  }
-  const int rows = kThreads / c.lanes * c.chunks;
-  c.parts = (K + rows - 1) / rows;
-  return c;
-}
-
 template <typename TW, int LPR, int M>
-hipError_t run(const TW* w, int G, int K, int N, int parts, int polls, uint8_t* codes, float* scales, uint64_t* words,
+hipError_t run(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint64_t* words,
                hipStream_t stream) {
-  const int strips = N / (LPR * 16 / (int)sizeof(TW)), total = strips * G, all = 8 * kTogether;
-  const long long blocks = (long long)((total + all - 1) / all * all) * parts;
-  hipLaunchKernelGGL((quant_weights_fp8_kernel<TW, kThreads, LPR, M>), linear_grid(blocks), dim3(kThreads), 0, stream,
-                     w, K, N, strips, total, parts, polls, words, codes, scales);
+  constexpr int kRows = kThreads / LPR * M;
+  const int strips = N / (LPR * 16 / (int)sizeof(TW)), total = strips * G, parts = (K + kRows - 1) / kRows;
+  if (parts > 1) {
+    const long long n = (long long)G * N * parts / 2;
+    hipLaunchKernelGGL(clear_words_kernel, linear_grid((n + 255) / 256), dim3(256), 0, stream,
+                       reinterpret_cast<v4i*>(words), n);
+    const hipError_t st = hipGetLastError();
+    if (st != hipSuccess) return st;
+  }
+  constexpr int kAll = 8 * kTogether;
+  hipLaunchKernelGGL((quant_weights_fp8_kernel<TW, kThreads, LPR, M>),
+                     linear_grid((long long)((total + kAll - 1) / kAll * kAll) * parts, kThreads), dim3(kThreads), 0, stream, w,
+                     K, N, strips, total, parts, polls, words, codes, scales);
   return hipGetLastError();
 }
 
 template <typename TW>
 hipError_t quantize(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint64_t* words,
                     hipStream_t stream) {
-  constexpr int kLanes = 64 * (int)sizeof(TW) / 16, kChunks = sizeof(TW) == 4 ? 24 : 16;
-  const Cut c = cut_of<TW>(G, K, N, device_cu_count());
-  if (c.parts > 1) {
-    const long long n = (long long)G * N * c.parts / 2;
-    hipLaunchKernelGGL(clear_words_kernel, linear_grid((n + 255) / 256), dim3(256), 0, stream,
-                       reinterpret_cast<v4i*>(words), n);
-    const hipError_t st = hipGetLastError();
-    if (st != hipSuccess) return st;
+  const long long each = (long long)G * K * N / device_cu_count();
+#define RUN(L, M) run<TW, L, M>(w, G, K, N, polls, codes, scales, words, stream)
+  if constexpr (sizeof(TW) == 4) {
+    if (each >= 1 << 19) return RUN(32, 24);
+    if (each >= 1 << 16) return RUN(16, 24);
+    if (each >= 1 << 13) return RUN(8, 12);
+  } else {
+    if (each >= 1 << 18) return RUN(16, 24);
+    if (each >= 24 << 10) return RUN(8, 16);
   }
-#define RUN(L, M) run<TW, L, M>(w, G, K, N, c.parts, polls, codes, scales, words, stream)
-  if (c.lanes == 2 * kLanes) return RUN(2 * kLanes, 24);
-  if (c.lanes == kLanes) return RUN(kLanes, kChunks);
-  return RUN(kLanes / 2, kChunks / 2);
+  return RUN(4, 8);
 #undef RUN
 }
 

@@ -15,6 +15,7 @@ def weights(G, K, N, dtype, seed):
     w = 0.02 * torch.randn((G, K, N), generator=g) * torch.exp2(torch.randint(-20, 20, (N,), generator=g).float())
     w[:, :, 3] = 0
     w[:, :, 5] *= 1e-20
+    w[:, 1::3, ::7] = -0.0
     return w.to(dtype)
 
 
@@ -151,9 +152,10 @@ def test_a_block_that_waits_in_vain(dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("G_,K,N", [(8, 4096, 2048), (1, 16384, 4224), (61, 1152, 1024), (520, 128, 1024)])
+@pytest.mark.parametrize("G_,K,N", [(8, 4096, 2048), (2, 16384, 4224), (122, 1152, 1024), (1024, 128, 1152), (1, 6912, 640),
+                                    (3, 2176, 2816)])
 def test_large(G_, K, N, dtype):
-    """Enough elements for strips of 128 columns, against the definition on the GPU: 64-bit quotients of f32 numbers
+    """Strips of 16 to 128 columns, one part to forty-three, against the definition on the GPU: 64-bit quotients of f32 numbers
     round to f32's own."""
     import fp8_moe_grouped_amd as G
     g = torch.Generator(device="cuda").manual_seed(K)
