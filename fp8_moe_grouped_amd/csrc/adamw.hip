@@ -5,12 +5,11 @@
 //   p' = p - (lr wd p + lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps))
 //
 // The tensors' pointers travel in the kernel's arguments, kMost of them a launch, so that a
-// call copies nothing and can be captured.  A block finds its tensor among the prefix sums
-// of their blocks.
+// call copies nothing and can be captured.
 //
 // 8-bit states: m and r = sqrt(v) as e4m3 codes, a scale for each 256 consecutive elements.
-// A wave holds such a block, 4 elements a lane, so its new scale is a reduction over the
-// wave's registers.  Codes are rounded up or down by chance: at beta2 = 0.999 a step changes
+// 32 lanes hold such a block, 8 elements each, so its new scale is a reduction over their
+// registers.  Codes are rounded up or down by chance: at beta2 = 0.999 a step changes
 // r by 0.05 % and m by 10 %, half a step of e4m3 is 3 to 6 %, so the nearest code would
 // keep r where it started.  r and not v is held because e4m3's 2^18 between its largest and
 // smallest number would be 2^9 in r.  An r' above 0 gets the smallest code at least: the
@@ -284,8 +283,10 @@ __device__ __forceinline__ v2i hold(const float (&x)[kVec8], const uint32_t (&ra
   return out;
 }
 
-// Bound by HBM with f32 parameters and gradients (16 bytes an element, 5.3 TB/s: 8 x 7168 x 4096 and 8 x 2048 x 7168 in
-// HBMTIME) and by its some 90 instructions an element with bf16 ones (10 bytes, BF16TIME).
+// Bound by HBM: 16 bytes an element with f32 parameters and gradients, 5.3 TB/s (8 x 7168 x 4096 and 8 x 2048 x 7168 in
+// 1060 us).  With bf16 ones, 10 bytes, its 67 instructions an element count as much: 38M elements in 73 us, 5.2 TB/s.  It
+// had 87 and took 80 to 85 when codes were made with integers (11 instructions a state; the conversion is one), the key's
+// mixing was not scalar and the coefficients came in f64; with 4 elements a lane and divisions 104.
 template <typename TP, typename TG>
 __global__ __launch_bounds__(kThreads) void adamw8_kernel(const Tensors<State8> all, const uint64_t seed,
                                                           const AdamW how) {

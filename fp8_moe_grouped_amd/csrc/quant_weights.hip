@@ -51,13 +51,13 @@ constexpr int kTogether = 4;                        // strips side by side that 
 
 // A block keeps M chunks a thread, a strip of LPR chunks x kRows * M rows, in its registers, so that the weights are
 // read once.  Where that is not all of K (parts > 1), the strip's blocks tell each other their columns' largest
-// magnitudes through `words` [total][parts][columns], zero at first: the magnitude's bits below a one, published and
-// read as one 64-bit word, so that no other order matters.  The blocks of a strip follow each other on one XCD and
+// magnitudes through `words` [total][parts][columns], zero at first: the magnitude's bits and one, published and read as
+// one word, so that no other order matters.  The blocks of a strip follow each other on one XCD and
 // run at the same time; one that waits longer than `polls` reads the rows of the others instead, so every wait ends.
 template <typename TW, int THREADS, int LPR, int M>
 __global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW* __restrict__ w, int K, int N, int strips,
                                                                        int total, int parts, int polls,
-                                                                       uint64_t* __restrict__ words,
+                                                                       uint32_t* __restrict__ words,
                                                                        uint8_t* __restrict__ codes,
                                                                        float* __restrict__ scales) {
   constexpr int C = 16 / (int)sizeof(TW), kRows = THREADS / LPR, kWaves = THREADS / 64, kColumns = LPR * C;
@@ -122,22 +122,22 @@ __global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW*
     const int column = tid % kColumns, group = tid / kColumns;
     float most = 0.f;
     if (group < kGroups) {
-      uint64_t* const mine = words + (size_t)strip * parts * kColumns + column;
+      uint32_t* const mine = words + (size_t)strip * parts * kColumns + column;
       if (group == 0) {
 #pragma unroll
         for (int v = 0; v < kWaves; ++v) most = __builtin_fmaxf(most, tops[v][column]);
-        __hip_atomic_store(mine + part * kColumns, 1ull << 32 | __float_as_uint(most), __ATOMIC_RELAXED,
+        __hip_atomic_store(mine + part * kColumns, __float_as_uint(most) + 1, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
       }
       for (int o = 1 + group; o < parts; o += kGroups) {
         const int q = part + o < parts ? part + o : part + o - parts;
-        uint64_t word = 0;
+        uint32_t word = 0;
         for (int tries = 0; tries < polls && !word; ++tries) {
           word = __hip_atomic_load(mine + q * kColumns, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
           if (!word) __builtin_amdgcn_s_sleep(4);
         }
         if (word) {
-          most = __builtin_fmaxf(most, __uint_as_float((uint32_t)word));
+          most = __builtin_fmaxf(most, __uint_as_float(word - 1));
         } else {
           const TW* const others = w + (size_t)g * K * N + (n - col) + column;
           const int stop = min(K, (q + 1) * kRows * M);
@@ -210,12 +210,12 @@ __global__ __launch_bounds__(256) void clear_words_kernel(v4i* __restrict__ word
 // A block of 512 threads keeps 384 rows of 128 columns in f32, 768 of them in bf16 and of 64 or 32 in f32, 1024 otherwise.
 constexpr int kThreads = 512;
 template <typename TW, int LPR, int M>
-hipError_t run(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint64_t* words,
+hipError_t run(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint32_t* words,
                hipStream_t stream) {
   constexpr int kRows = kThreads / LPR * M;
   const int strips = N / (LPR * 16 / (int)sizeof(TW)), total = strips * G, parts = (K + kRows - 1) / kRows;
   if (parts > 1) {
-    const long long n = (long long)G * N * parts / 2;
+    const long long n = (long long)G * N * parts / 4;
     hipLaunchKernelGGL(clear_words_kernel, linear_grid((n + 255) / 256), dim3(256), 0, stream,
                        reinterpret_cast<v4i*>(words), n);
     const hipError_t st = hipGetLastError();
@@ -229,7 +229,7 @@ hipError_t run(const TW* w, int G, int K, int N, int polls, uint8_t* codes, floa
 }
 
 template <typename TW>
-hipError_t quantize(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint64_t* words,
+hipError_t quantize(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint32_t* words,
                     hipStream_t stream) {
   const long long each = (long long)G * K * N / device_cu_count();
 #define RUN(L, M) run<TW, L, M>(w, G, K, N, polls, codes, scales, words, stream)
@@ -250,12 +250,12 @@ hipError_t quantize(const TW* w, int G, int K, int N, int polls, uint8_t* codes,
 size_t quant_weights_workspace_bytes(bool bf16, int G, int K, int N) {
   // the most that any cut needs: a device with another number of CUs gives the same answer
   const size_t rows = bf16 ? 768 : 384, parts = (K + rows - 1) / rows;
-  return parts > 1 ? 8 * (size_t)G * N * parts : 0;
+  return parts > 1 ? 4 * (size_t)G * N * parts : 0;
 }
 
 hipError_t launch_quant_weights_fp8(const void* w, bool bf16, int G, int K, int N, uint8_t* codes, float* scales,
                                     void* ws, int polls, hipStream_t stream) {
-  uint64_t* const words = static_cast<uint64_t*>(ws);
+  uint32_t* const words = static_cast<uint32_t*>(ws);
   if (bf16) return quantize(static_cast<const uint16_t*>(w), G, K, N, polls, codes, scales, words, stream);
   return quantize(static_cast<const float*>(w), G, K, N, polls, codes, scales, words, stream);
 }

@@ -146,7 +146,7 @@ def test_a_block_that_waits_in_vain(dtype):
     check(*want, w)
     for polls in (0, 1):
         codes, scales = torch.full_like(want[0], 0xAA), torch.full_like(want[1], -1.0)
-        words = torch.full((3 * 512 * 4,), -1, dtype=torch.int64, device="cuda")
+        words = torch.full((3 * 512 * 7,), -1, dtype=torch.int32, device="cuda")
         _launch(dev, codes, scales, words, polls)
         assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])
 

@@ -122,7 +122,7 @@ def test_quantize_refusals():
     for dt, small, large in ((G.F32, 384, 640), (G.BF16, 768, 1152)):
         assert L.fp8gmm_workspace_bytes(G.OP_QUANT_WEIGHTS, 0, small, 256, 2, dt) == 0
         need = L.fp8gmm_workspace_bytes(G.OP_QUANT_WEIGHTS, 0, large, 256, 2, dt)
-        assert need == 2 * 256 * 2 * 8                        # a word for each column of each half
+        assert need == 2 * 256 * 2 * 4                        # a word for each column of each half
         assert f(dt=dt, K=large, ws=None) == G.ERR_WORKSPACE and f(dt=dt, K=large, wsb=need - 1) == G.ERR_WORKSPACE
     assert L.fp8gmm_workspace_bytes(G.OP_QUANT_WEIGHTS, 0, 7168, 256, 2, 2) == 0
 
