@@ -955,6 +955,8 @@ def _adamw(name, params, grads, states, held, lr, step, betas, eps, weight_decay
     rates = [how.lr, how.eps, how.weight_decay]
     if not all(0 <= v < float("inf") for v in rates) or not all(0 <= b < 1 for b in (how.beta1, how.beta2)):
         raise ValueError(f"lr, eps and weight_decay must be finite and not negative, betas in [0, 1): got {rates}, {betas}")
+    if 0 < how.eps < 2.0 ** -126:
+        raise ValueError(f"eps must be 0 or at least 2^-126, got {eps}")
     if held and not 0 <= seed < 1 << 64:
         raise ValueError(f"seed must fit 64 bits without a sign, got {seed}")
     pointers = [(_P * n)(*(t.data_ptr() for t in l)) for l in columns]

@@ -96,13 +96,13 @@ int current_scratch(void** out) {
 
 namespace {
 
-constexpr int64_t kMaxElements = 1LL << 35;         // of an AdamW tensor: 2^23 blocks
+constexpr int64_t kMaxElements = 1LL << 35;         // of an AdamW tensor: 2^25 blocks
 
 // A buffer of an AdamW call.
 struct Range {
   uintptr_t begin, end;
 };
-// The buffers of one list; all but the gradients are written.
+// The buffers of one list; all but the gradients and the numbers on the device are written.
 struct Column {
   std::vector<Range> all;
   bool written = true;
@@ -134,7 +134,7 @@ bool overlap(Column (&columns)[N]) {
   }
 }
 
-// What both AdamW calls check; buffers(i, size, put) names a tensor's N - 2 states as put(list, pointer, bytes, align).
+// What both AdamW calls check; buffers(i, size, put) names a tensor's N - 3 states as put(list, pointer, bytes, align).
 template <size_t N, typename F>
 int check_adamw(int32_t tensors, const int64_t* sizes, void* const* params, int32_t param_dtype,
                 const void* const* grads, int32_t grad_dtype, bool states, const fp8gmm_adamw* how, F buffers) {
@@ -147,9 +147,10 @@ int check_adamw(int32_t tensors, const int64_t* sizes, void* const* params, int3
   if ((!how->lr_dev && !rate(how->lr)) || !rate(how->eps) || !rate(how->weight_decay) || !beta(how->beta1) ||
       !beta(how->beta2) || (!how->step_dev && how->step < 1))
     return FP8GMM_ERR_UNSUPPORTED;
+  if (how->eps > 0.0 && how->eps < 0x1p-126) return FP8GMM_ERR_UNSUPPORTED;   // its reciprocal passes f32
   try {
     Column columns[N];
-    columns[1].written = false;
+    columns[1].written = columns[N - 1].written = false;
     for (Column& c : columns) c.all.reserve((size_t)tensors);
     int st = FP8GMM_OK;
     const auto put = [&](size_t list, const void* p, int64_t bytes, uintptr_t align) {
@@ -166,6 +167,9 @@ int check_adamw(int32_t tensors, const int64_t* sizes, void* const* params, int3
       put(1, grads[i], n * (grad_dtype == FP8GMM_F32 ? 4 : 2), 16);
       buffers(i, n, put);
     }
+    if (how->lr_dev) put(N - 1, how->lr_dev, 4, 4);
+    if (how->step_dev) put(N - 1, how->step_dev, 8, 8);
+    if (how->grad_scale) put(N - 1, how->grad_scale, 4, 4);
     if (st != FP8GMM_OK) return st;
     return overlap(columns) ? FP8GMM_ERR_OVERLAP : FP8GMM_OK;
   } catch (...) {                                   // host memory: nothing passes the C boundary
@@ -674,7 +678,7 @@ int quantize_fp8_weights(const void* w, int32_t dtype, int64_t K, int64_t N, int
 int adamw_step(int32_t tensors, const int64_t* sizes, void* const* params, int32_t param_dtype,
                const void* const* grads, int32_t grad_dtype, float* const* exp_avgs, float* const* exp_avg_sqs,
                const fp8gmm_adamw* how, void* stream) {
-  const int st = check_adamw<4>(tensors, sizes, params, param_dtype, grads, grad_dtype, exp_avgs && exp_avg_sqs, how,
+  const int st = check_adamw<5>(tensors, sizes, params, param_dtype, grads, grad_dtype, exp_avgs && exp_avg_sqs, how,
                                 [&](int32_t i, int64_t n, const auto& put) {
                                   put(2, exp_avgs[i], 4 * n, 16);
                                   put(3, exp_avg_sqs[i], 4 * n, 16);
@@ -690,7 +694,7 @@ int adamw_step_8bit(int32_t tensors, const int64_t* sizes, void* const* params, 
                     const void* const* grads, int32_t grad_dtype, uint8_t* const* m_codes, float* const* m_scales,
                     uint8_t* const* r_codes, float* const* r_scales, uint64_t seed, const fp8gmm_adamw* how,
                     void* stream) {
-  const int st = check_adamw<6>(tensors, sizes, params, param_dtype, grads, grad_dtype,
+  const int st = check_adamw<7>(tensors, sizes, params, param_dtype, grads, grad_dtype,
                                 m_codes && m_scales && r_codes && r_scales, how,
                                 [&](int32_t i, int64_t n, const auto& put) {
                                   const int64_t scales = (n + 255) / 256 * 4;

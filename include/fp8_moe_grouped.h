@@ -453,8 +453,9 @@ int moe_balance_loss_bwd(const float* dlosses, const void* logits, int32_t dtype
  * bf16 each (FP8GMM_F32 / FP8GMM_BF16, one type for all of a call's tensors).  The
  * coefficients are computed in f64 and rounded to f32.  lr_dev (f32 [1]) and step_dev
  * (i64 [1], values below 1 count as 1) replace lr and step where they are not NULL, for
- * captured graphs; they and grad_scale are device memory.  lr, wd and eps are finite
- * and not negative, the betas in [0, 1), step at least 1.  No buffer that the call
+ * captured graphs; they and grad_scale are device memory, and lr_dev's value is taken as
+ * it is.  lr, wd and eps are finite and not negative, eps 0 or at least 2^-126, the
+ * betas in [0, 1), step at least 1.  No buffer that the call
  * writes may overlap another of its buffers (FP8GMM_ERR_OVERLAP): a tensor is listed
  * once.  Buffers of empty tensors may be NULL.
  *

@@ -87,8 +87,10 @@ def test_adamw_refusals(bits):
     assert f(n=-1) == G.ERR_SHAPE and f(size=-1) == G.ERR_SHAPE and f(size=(1 << 35) + 1) == G.ERR_SHAPE
     for bad in (dict(pd=2), dict(gd=-1), dict(lr=-1.0), dict(lr=math.nan), dict(lr=math.inf), dict(eps=-1e-9),
                 dict(weight_decay=math.inf), dict(beta1=1.0), dict(beta2=-0.1), dict(beta1=math.nan), dict(step=0),
-                dict(step=-5)):
+                dict(step=-5), dict(eps=1e-39), dict(eps=5e-324)):
         assert f(**bad) == G.ERR_UNSUPPORTED, bad
+    for name, bad in (("lr_dev", 0x900002), ("step_dev", 0x900004), ("grad_scale", 0x900001)):
+        assert f(**{name: bad}) == G.ERR_ALIGN, name
     # nothing to do: no launch
     assert f(n=0) == G.OK and f(size=0, p=None, g=None, m=None, v=None, ms=None, vs=None) == G.OK
 
@@ -106,6 +108,9 @@ def test_adamw_overlaps(bits):
     if bits == 8:
         assert f(n=2, second={**other, "ms": 0x500000 + 8}) == G.ERR_OVERLAP
         assert f(vs=0x500000 + 12) == G.ERR_OVERLAP          # four scales a tensor of 1000
+    # numbers on the device are read while the buffers are written
+    for name in ("lr_dev", "step_dev", "grad_scale"):
+        assert f(**{name: 0x100000 + 80}) == G.ERR_OVERLAP and f(**{name: 0x400000}) == G.ERR_OVERLAP, name
 
 
 def test_quantize_refusals():
