@@ -46,8 +46,10 @@ hipError_t launch_gmm_mxfp4(const uint8_t* aq, const uint8_t* ascale, const uint
                             int N, bool swiglu, uint16_t* out, int* status, hipStream_t stream);
 
 // Master weights to e4m3 codes and a scale per output channel.  polls: how often a block looks for another one's
-// maxima before it computes them itself, some microsecond each.
-constexpr int kQuantPolls = 20000;
+// maxima before it computes them itself, a third of a microsecond each.  By itself a call is as fast with 100 to 20000
+// and a tenth to a third slower with 30; four of 8 x 16384 x 4096 f32 at once take 18 ms with 300, 26 with
+// 1000 and 280 with 20000.
+constexpr int kQuantPolls = 300;
 size_t quant_weights_workspace_bytes(bool bf16, int G, int K, int N);
 hipError_t launch_quant_weights_fp8(const void* w, bool bf16, int G, int K, int N, uint8_t* codes, float* scales,
                                     void* ws, int polls, hipStream_t stream);

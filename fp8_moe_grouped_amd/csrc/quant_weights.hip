@@ -9,7 +9,7 @@
 // whole half-lines or more: with 16 columns the codes' 16-byte pieces took as long as half of
 // the reads (8 x 7168 x 4096 f32: 357 us, 228 without the stores).  128 columns of 7168 rows are
 // 3.7 MB, eight times a CU's registers, so a strip's rows are shared by blocks that exchange
-// their maxima (235 us, 5 TB/s; two passes over the weights 960).
+// their maxima (229 us in a row of calls, 5.1 TB/s; two passes over the weights 960).
 #include "moe_common.hpp"
 #include "moe_launch.hpp"
 
@@ -53,7 +53,8 @@ constexpr int kTogether = 4;                        // strips side by side that 
 // read once.  Where that is not all of K (parts > 1), the strip's blocks tell each other their columns' largest
 // magnitudes through `words` [total][parts][columns], zero at first: the magnitude's bits and one, published and read as
 // one word, so that no other order matters.  The blocks of a strip follow each other on one XCD and
-// run at the same time; one that waits longer than `polls` reads the rows of the others instead, so every wait ends.
+// run at the same time; where a thread waited in vain for `polls` looks, it reads the rows of that block instead and looks
+// once for each of the rest, so every wait ends.
 template <typename TW, int THREADS, int LPR, int M>
 __global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW* __restrict__ w, int K, int N, int strips,
                                                                        int total, int parts, int polls,
@@ -123,30 +124,38 @@ __global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW*
     float most = 0.f;
     if (group < kGroups) {
       uint32_t* const mine = words + (size_t)strip * parts * kColumns + column;
+      const auto publish = [&](int q, float top) {
+        __hip_atomic_store(mine + q * kColumns, __float_as_uint(top) + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      };
       if (group == 0) {
 #pragma unroll
         for (int v = 0; v < kWaves; ++v) most = __builtin_fmaxf(most, tops[v][column]);
-        __hip_atomic_store(mine + part * kColumns, __float_as_uint(most) + 1, __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
+        publish(part, most);
       }
+      int looks = polls;
       for (int o = 1 + group; o < parts; o += kGroups) {
         const int q = part + o < parts ? part + o : part + o - parts;
         uint32_t word = 0;
-        for (int tries = 0; tries < polls && !word; ++tries) {
+        for (int tries = 0; tries < looks && !word; ++tries) {
           word = __hip_atomic_load(mine + q * kColumns, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
           if (!word) __builtin_amdgcn_s_sleep(4);
         }
         if (word) {
           most = __builtin_fmaxf(most, __uint_as_float(word - 1));
         } else {
+          looks = min(looks, 1);
           const TW* const others = w + (size_t)g * K * N + (n - col) + column;
           const int stop = min(K, (q + 1) * kRows * M);
+          float there = 0.f;
+#pragma unroll 2                                    // 4 or 8: their registers cost every call 5 or 8 %
           for (int k = q * kRows * M; k < stop; ++k) {
             float v;
             if constexpr (C == 4) v = others[(size_t)k * N];
             else v = __uint_as_float((uint32_t)others[(size_t)k * N] << 16);
-            most = __builtin_fmaxf(most, __builtin_fabsf(v));
+            there = __builtin_fmaxf(there, __builtin_fabsf(v));
           }
+          most = __builtin_fmaxf(most, there);
+          publish(q, there);
         }
       }
     }
@@ -208,6 +217,9 @@ __global__ __launch_bounds__(256) void clear_words_kernel(v4i* __restrict__ word
 //   bf16  128 or 64: 8 x 7168 x 3840 149, 169; 2 x 8192 x 4096 50, 56;   64 or 32: 8 x 768 x 2048 12.0, 13.3;
 //         1 x 6912 x 640 14.6, 11.3
 // A block of 512 threads keeps 384 rows of 128 columns in f32, 768 of them in bf16 and of 64 or 32 in f32, 1024 otherwise.
+// An XCD has room for 64 blocks.  Calls on several streams each fill it with what is ready and may leave each other's
+// strips half in: strips of at most kMostParts leave room for two (two of 8 x 16384 x 4096 at once 1.4 ms; in strips of
+// 43 parts 150 and more, every block waiting and reading for the others).
 constexpr int kThreads = 512;
 template <typename TW, int LPR, int M>
 hipError_t run(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint32_t* words,
@@ -228,13 +240,14 @@ hipError_t run(const TW* w, int G, int K, int N, int polls, uint8_t* codes, floa
   return hipGetLastError();
 }
 
+constexpr int kMostParts = 24;                      // 128 columns or 64: 8 x 16384 x 4096 656, 665
 template <typename TW>
 hipError_t quantize(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint32_t* words,
                     hipStream_t stream) {
   const long long each = (long long)G * K * N / device_cu_count();
 #define RUN(L, M) run<TW, L, M>(w, G, K, N, polls, codes, scales, words, stream)
   if constexpr (sizeof(TW) == 4) {
-    if (each >= 1 << 19) return RUN(32, 24);
+    if (each >= 1 << 19 && K <= kMostParts * 384) return RUN(32, 24);
     if (each >= 1 << 16) return RUN(16, 24);
     if (each >= 1 << 13) return RUN(8, 12);
   } else {

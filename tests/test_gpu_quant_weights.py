@@ -209,6 +209,26 @@ def test_two_at_once():
         assert torch.equal(c, want[i % 2][0]) and torch.equal(s, want[i % 2][1])
 
 
+@pytest.mark.parametrize("n", [2, 4])
+def test_several_at_once_of_the_longest_columns(n):
+    """Strips in 22 parts from several streams, which together ask for more blocks than fit: what waits in vain reads for
+    itself and for the others."""
+    import fp8_moe_grouped_amd as G
+    g = torch.Generator(device="cuda").manual_seed(n)
+    ws = [torch.randn((2, 16384, 2048), generator=g, device="cuda") for _ in range(n)]
+    want = [G.quantize_fp8_weights(w) for w in ws]
+    streams = [torch.cuda.Stream() for _ in ws]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for s, w in zip(streams, ws):
+            with torch.cuda.stream(s):
+                got.append(G.quantize_fp8_weights(w))
+        torch.cuda.synchronize()
+        for (c, s), (wc, ws_) in zip(got, want):
+            assert torch.equal(c, wc) and torch.equal(s, ws_)
+
+
 def test_past_4_gib():
     """f32 weights of 9 GiB: the last expert's columns."""
     import fp8_moe_grouped_amd as G
