@@ -57,7 +57,7 @@ constexpr int kTogether = 4;                        // strips side by side that 
 // once for each of the rest, so every wait ends.
 template <typename TW, int THREADS, int LPR, int M>
 __global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW* __restrict__ w, int K, int N, int strips,
-                                                                       int total, int parts, int polls,
+                                                                       int total, int parts, int each, int polls,
                                                                        uint32_t* __restrict__ words,
                                                                        uint8_t* __restrict__ codes,
                                                                        float* __restrict__ scales) {
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW*
   const int strip = (turn / kTogether * 8 + (int)(b % 8)) * kTogether + turn % kTogether;
   if (strip >= total) return;
   const int g = strip / strips, n = strip % strips * kColumns + col;
-  const int first = part * (kRows * M), end = min(K, first + kRows * M);
+  const int first = part * each, end = min(K, first + each);
   // A wave's rows are inside or outside together.  Its addresses are a uniform part and 32 bits of each lane
   // (at most 16 rows of N < 2^24), so that M of them need no registers.
   const int row = first + tid / LPR, wave_row = __builtin_amdgcn_readfirstlane(row);
@@ -145,10 +145,10 @@ __global__ __launch_bounds__(THREADS, 4) void quant_weights_fp8_kernel(const TW*
         } else {
           looks = min(looks, 1);
           const TW* const others = w + (size_t)g * K * N + (n - col) + column;
-          const int stop = min(K, (q + 1) * kRows * M);
+          const int stop = min(K, (q + 1) * each);
           float there = 0.f;
 #pragma unroll 2                                    // 4 or 8: their registers cost every call 5 or 8 %
-          for (int k = q * kRows * M; k < stop; ++k) {
+          for (int k = q * each; k < stop; ++k) {
             float v;
             if constexpr (C == 4) v = others[(size_t)k * N];
             else v = __uint_as_float((uint32_t)others[(size_t)k * N] << 16);
@@ -210,13 +210,17 @@ __global__ __launch_bounds__(256) void clear_words_kernel(v4i* __restrict__ word
 }
 
 // A strip's lanes and a thread's chunks, by how many elements a CU has: wide strips for whole lines of codes, narrow
-// ones for enough blocks.  Both sides in us:
+// ones for enough blocks; more chunks where one part less, of one or two, is left to wait for.  Both sides in us:
 //   f32   128 columns or 64: 8 x 7168 x 3840 240, 257; 8 x 3200 x 3328 92, 86
-//         64 or 32: 2 x 3840 x 2304 24.1, 27.4; 8 x 768 x 2048 15.6, 15.1;   32 or 16: 4 x 4992 x 256 10.6, 12.6;
-//         1 x 1024 x 1024 6.9, 4.4
-//   bf16  128 or 64: 8 x 7168 x 3840 149, 169; 2 x 8192 x 4096 50, 56;   64 or 32: 8 x 768 x 2048 12.0, 13.3;
-//         1 x 6912 x 640 14.6, 11.3
-// A block of 512 threads keeps 384 rows of 128 columns in f32, 768 of them in bf16 and of 64 or 32 in f32, 1024 otherwise.
+//         64 or 32: 2 x 2304 x 896 12.6, 9.9; 4 x 2176 x 1792 21.9, 22.2;   32 or 16: 2 x 768 x 1664 6.7, 5.8;
+//         1 x 2048 x 768 10.2, 8.4
+//   bf16  128 or 64: 8 x 7168 x 3840 149, 169; 4 x 4096 x 3584 44.6, 42.6;   64 or 32: 8 x 768 x 2048 12.2, 13.4;
+//         4 x 6656 x 256 15.4, 11.2
+//   16 chunks or 24: 7 x 1280 x 1536 bf16 18.1, 14.9; 4 x 2432 x 2688 29.6, 25.0; but 6 x 3968 x 1920 33.7, 41.7
+//   8 or 16: 2 x 1408 x 1408 f32 11.1, 8.5; 1 x 1536 x 2048 bf16 8.7, 7.8; but 1 x 6144 x 768 11.4, 14.6
+// A block of 512 threads keeps 384 rows of 128 columns in f32; of 64 and 32 columns there 768 and 1024, of 128 and 64 in
+// bf16 768 and 1024 or 1536, of the narrowest 1024 or 2048.  A strip's parts get the same number of rows, within a
+// block's step (7 x 4864 x 1920 bf16 51.9 -> 49.1).
 // An XCD has room for 64 blocks.  Calls on several streams each fill it with what is ready and may leave each other's
 // strips half in: strips of at most kMostParts leave room for two (two of 8 x 16384 x 4096 at once 1.4 ms; in strips of
 // 43 parts 150 and more, every block waiting and reading for the others).
@@ -224,8 +228,9 @@ constexpr int kThreads = 512;
 template <typename TW, int LPR, int M>
 hipError_t run(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint32_t* words,
                hipStream_t stream) {
-  constexpr int kRows = kThreads / LPR * M;
-  const int strips = N / (LPR * 16 / (int)sizeof(TW)), total = strips * G, parts = (K + kRows - 1) / kRows;
+  constexpr int kRows = kThreads / LPR, kMost = kRows * M;
+  const int strips = N / (LPR * 16 / (int)sizeof(TW)), total = strips * G, parts = (K + kMost - 1) / kMost;
+  const int each = ((K + parts - 1) / parts + kRows - 1) / kRows * kRows;   // rows of a part
   if (parts > 1) {
     const long long n = (long long)G * N * parts / 4;
     hipLaunchKernelGGL(clear_words_kernel, linear_grid((n + 255) / 256), dim3(256), 0, stream,
@@ -236,7 +241,7 @@ hipError_t run(const TW* w, int G, int K, int N, int polls, uint8_t* codes, floa
   constexpr int kAll = 8 * kTogether;
   hipLaunchKernelGGL((quant_weights_fp8_kernel<TW, kThreads, LPR, M>),
                      linear_grid((long long)((total + kAll - 1) / kAll * kAll) * parts, kThreads), dim3(kThreads), 0, stream, w,
-                     K, N, strips, total, parts, polls, words, codes, scales);
+                     K, N, strips, total, parts, each, polls, words, codes, scales);
   return hipGetLastError();
 }
 
@@ -245,16 +250,17 @@ template <typename TW>
 hipError_t quantize(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint32_t* words,
                     hipStream_t stream) {
   const long long each = (long long)G * K * N / device_cu_count();
+  const auto parts = [K](int rows) { return (K + rows - 1) / rows; };
 #define RUN(L, M) run<TW, L, M>(w, G, K, N, polls, codes, scales, words, stream)
   if constexpr (sizeof(TW) == 4) {
     if (each >= 1 << 19 && K <= kMostParts * 384) return RUN(32, 24);
     if (each >= 1 << 16) return RUN(16, 24);
-    if (each >= 1 << 13) return RUN(8, 12);
+    if (each >= 1 << 13) return RUN(8, 16);
   } else {
     if (each >= 1 << 18) return RUN(16, 24);
-    if (each >= 24 << 10) return RUN(8, 16);
+    if (each >= 1 << 15) return parts(1536) <= 2 && parts(1536) < parts(1024) ? RUN(8, 24) : RUN(8, 16);
   }
-  return RUN(4, 8);
+  return parts(2048) == 1 && parts(1024) == 2 ? RUN(4, 16) : RUN(4, 8);
 #undef RUN
 }
 
