@@ -964,6 +964,8 @@ def _adamw(name, params, grads, states, held, lr, step, betas, eps, weight_decay
     p, g = LOGIT_DTYPES[columns[0][0].dtype], LOGIT_DTYPES[columns[1][0].dtype]
     _launch(dev, name, n, sizes, pointers[0], p, pointers[1], g, *pointers[2:], *((seed,) if held else ()),
             ctypes.byref(how))
+    # a graph that has saved a parameter notices that it changed
+    torch.autograd.graph.increment_version([t for t in columns[0] if not t.is_inference()])
 
 
 def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,

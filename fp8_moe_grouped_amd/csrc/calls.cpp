@@ -468,6 +468,10 @@ PyObject* adamw_call(PyObject* const* a, bool held) {
   }
   // not left to Python after a launch, which has changed some tensors already
   PLAIN(st == FP8GMM_OK || st == FP8GMM_ERR_HIP)
+  for (Py_ssize_t i = 0; i < p.n; ++i) {            // a graph that has saved a parameter notices that it changed
+    at::TensorImpl* const impl = THPVariable_Unpack(p[i]).unsafeGetTensorImpl();
+    if (!impl->is_inference()) impl->bump_version();
+  }
   return PyLong_FromLong(st);
   END
 }

@@ -156,3 +156,23 @@ def test_side_streams_and_other_threads(name):
     for t in threads:
         t.join()
     assert len(got) == 3 and all(torch.equal(a, b) for out in got for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("way", ["extension", "python"])
+def test_a_graph_notices_the_step(bits, way, monkeypatch):
+    """A backward pass that has saved a parameter does not go on with the next step's values."""
+    import fp8_moe_grouped_amd as G
+    p = [torch.nn.Parameter(rand(1, 300))]
+    m, v = G.adamw_8bit_states(p) if bits == 8 else [[torch.zeros(300, device="cuda")] for _ in "mv"]
+    G._plain()
+    if way == "python":
+        monkeypatch.setattr(G, "_calls", Nothing())
+    before, loss = p[0]._version, (p[0] * p[0]).sum()
+    step = G.adamw_step_8bit if bits == 8 else G.adamw_step
+    step(p, [rand(2, 300)], m, v, lr=1e-2, step=1)
+    assert p[0]._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():                                 # which counts no versions of what it makes
+        step([p[0] + 0.0], [rand(2, 300)], m, v, lr=1e-2, step=2)
