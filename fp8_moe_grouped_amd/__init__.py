@@ -974,7 +974,8 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr, step, betas=(0.9, 0.
     float32 or bfloat16, states float32.  ``step`` counts from 1.  ``lr`` and
     ``step`` may be tensors of one number on the device (float32, int64), read
     when the kernels run, for captured graphs; ``grad_scale`` is such a float32
-    tensor that multiplies the gradients.  A tensor may be listed once."""
+    tensor that multiplies the gradients.  Tensors may be pieces of one buffer,
+    at any element; one may be listed once."""
     st = (_calls or _plain()).adamw(params, grads, exp_avgs, exp_avg_sqs, lr, step, *betas, eps, weight_decay,
                                     grad_scale)
     if st is None:

@@ -76,13 +76,17 @@ __device__ __forceinline__ Rates rates(const AdamW& a, uint32_t& step) {
   return r;
 }
 
+// Pieces of a larger buffer begin anywhere; the widest accesses need an element's alignment only.
+typedef float any4f __attribute__((ext_vector_type(4), aligned(4)));
+typedef int any2i __attribute__((ext_vector_type(2), aligned(1)));
+
 // N = 4 or 8 elements at j of n, streamed.  Without FULL those past the end are 0 and not written.
 template <bool FULL, int N>
 __device__ __forceinline__ void load(const float* p, int64_t j, int64_t n, float (&x)[N]) {
   if constexpr (FULL) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const v4f w = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(p + j + i));
+      const any4f w = __builtin_nontemporal_load(reinterpret_cast<const any4f*>(p + j + i));
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[i + c] = w[c];
     }
@@ -94,7 +98,7 @@ __device__ __forceinline__ void load(const float* p, int64_t j, int64_t n, float
 template <bool FULL, int N>
 __device__ __forceinline__ void load(const uint16_t* p, int64_t j, int64_t n, float (&x)[N]) {
   if constexpr (FULL) {
-    typedef int vec __attribute__((ext_vector_type(N / 2)));
+    typedef int vec __attribute__((ext_vector_type(N / 2), aligned(2)));
     const vec w = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p + j));
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = i & 1 ? bf16_hi((uint32_t)w[i / 2]) : bf16_lo((uint32_t)w[i / 2]);
@@ -108,7 +112,7 @@ __device__ __forceinline__ void store(float* p, int64_t j, int64_t n, const floa
   if constexpr (FULL) {
 #pragma unroll
     for (int i = 0; i < N; i += 4)
-      __builtin_nontemporal_store((v4f){x[i], x[i + 1], x[i + 2], x[i + 3]}, reinterpret_cast<v4f*>(p + j + i));
+      __builtin_nontemporal_store((any4f){x[i], x[i + 1], x[i + 2], x[i + 3]}, reinterpret_cast<any4f*>(p + j + i));
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -118,7 +122,7 @@ __device__ __forceinline__ void store(float* p, int64_t j, int64_t n, const floa
 template <bool FULL, int N>
 __device__ __forceinline__ void store(uint16_t* p, int64_t j, int64_t n, const float (&x)[N]) {
   if constexpr (FULL) {
-    typedef int vec __attribute__((ext_vector_type(N / 2)));
+    typedef int vec __attribute__((ext_vector_type(N / 2), aligned(2)));
     vec w;
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) w[i] = (int)pack_bf16x2(x[2 * i], x[2 * i + 1]);
@@ -132,7 +136,7 @@ __device__ __forceinline__ void store(uint16_t* p, int64_t j, int64_t n, const f
 // 8 codes.
 template <bool FULL>
 __device__ __forceinline__ v2i load_codes(const uint8_t* p, int64_t j, int64_t n) {
-  if constexpr (FULL) return __builtin_nontemporal_load(reinterpret_cast<const v2i*>(p + j));
+  if constexpr (FULL) return __builtin_nontemporal_load(reinterpret_cast<const any2i*>(p + j));
   v2i w = {0, 0};
 #pragma unroll
   for (int i = 0; i < 7; ++i)
@@ -142,7 +146,7 @@ __device__ __forceinline__ v2i load_codes(const uint8_t* p, int64_t j, int64_t n
 template <bool FULL>
 __device__ __forceinline__ void store_codes(uint8_t* p, int64_t j, int64_t n, v2i w) {
   if constexpr (FULL) {
-    __builtin_nontemporal_store(w, reinterpret_cast<v2i*>(p + j));
+    __builtin_nontemporal_store((any2i)w, reinterpret_cast<any2i*>(p + j));
     return;
   }
 #pragma unroll

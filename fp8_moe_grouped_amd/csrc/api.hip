@@ -163,8 +163,9 @@ int check_adamw(int32_t tensors, const int64_t* sizes, void* const* params, int3
       const int64_t n = sizes[i];
       if (n < 0 || n > kMaxElements) return FP8GMM_ERR_SHAPE;
       if (n == 0) continue;
-      put(0, params[i], n * (param_dtype == FP8GMM_F32 ? 4 : 2), 16);
-      put(1, grads[i], n * (grad_dtype == FP8GMM_F32 ? 4 : 2), 16);
+      const int64_t pb = param_dtype == FP8GMM_F32 ? 4 : 2, gb = grad_dtype == FP8GMM_F32 ? 4 : 2;
+      put(0, params[i], n * pb, (uintptr_t)pb);
+      put(1, grads[i], n * gb, (uintptr_t)gb);
       buffers(i, n, put);
     }
     if (how->lr_dev) put(N - 1, how->lr_dev, 4, 4);
@@ -680,8 +681,8 @@ int adamw_step(int32_t tensors, const int64_t* sizes, void* const* params, int32
                const fp8gmm_adamw* how, void* stream) {
   const int st = check_adamw<5>(tensors, sizes, params, param_dtype, grads, grad_dtype, exp_avgs && exp_avg_sqs, how,
                                 [&](int32_t i, int64_t n, const auto& put) {
-                                  put(2, exp_avgs[i], 4 * n, 16);
-                                  put(3, exp_avg_sqs[i], 4 * n, 16);
+                                  put(2, exp_avgs[i], 4 * n, 4);
+                                  put(3, exp_avg_sqs[i], 4 * n, 4);
                                 });
   if (st != FP8GMM_OK) return st;
   if (launch_adamw(tensors, sizes, params, param_dtype == FP8GMM_BF16, grads, grad_dtype == FP8GMM_BF16, exp_avgs,
@@ -698,9 +699,9 @@ int adamw_step_8bit(int32_t tensors, const int64_t* sizes, void* const* params, 
                                 m_codes && m_scales && r_codes && r_scales, how,
                                 [&](int32_t i, int64_t n, const auto& put) {
                                   const int64_t scales = (n + 255) / 256 * 4;
-                                  put(2, m_codes[i], n, 16);
+                                  put(2, m_codes[i], n, 1);
                                   put(3, m_scales[i], scales, 4);
-                                  put(4, r_codes[i], n, 16);
+                                  put(4, r_codes[i], n, 1);
                                   put(5, r_scales[i], scales, 4);
                                 });
   if (st != FP8GMM_OK) return st;

@@ -50,7 +50,7 @@ extern "C" {
 #define FP8GMM_ERR_NULL (-1)        /* a required pointer is NULL */
 #define FP8GMM_ERR_SHAPE (-2)       /* a size is out of range */
 #define FP8GMM_ERR_UNSUPPORTED (-3) /* a valid request this build does not implement */
-#define FP8GMM_ERR_ALIGN (-4)       /* a base pointer is not 16-byte aligned */
+#define FP8GMM_ERR_ALIGN (-4)       /* a base pointer is not 16-byte aligned (adamw_step: as its elements) */
 #define FP8GMM_ERR_WORKSPACE (-5)   /* workspace NULL or smaller than fp8gmm_workspace_bytes */
 #define FP8GMM_ERR_HIP (-6)         /* a kernel launch failed */
 #define FP8GMM_ERR_SCRATCH (-7)     /* input larger than gmm_fp8_fwd_noalloc's fixed scratch */
@@ -457,12 +457,13 @@ int moe_balance_loss_bwd(const float* dlosses, const void* logits, int32_t dtype
  * it is.  lr, wd and eps are finite and not negative, eps 0 or at least 2^-126, the
  * betas in [0, 1), step at least 1.  No buffer that the call
  * writes may overlap another of its buffers (FP8GMM_ERR_OVERLAP): a tensor is listed
- * once.  Buffers of empty tensors may be NULL.
+ * once.  Buffers of empty tensors may be NULL, and all need their elements' alignment
+ * only: tensors may be pieces of one larger buffer.
  *
  * adamw_step: m and v f32, of the parameter's size.
  * adamw_step_8bit: m and r = sqrt(v) as e4m3 codes u8 of the parameter's size, one f32
- *   scale for each block of 256 consecutive elements (ceil(size / 256) scales, 4-byte
- *   aligned, the last block may be shorter): m = code * scale.  After the step a block's new scale is
+ *   scale for each block of 256 consecutive elements (ceil(size / 256) scales,
+ *   the last block may be shorter): m = code * scale.  After the step a block's new scale is
  *   max|m'| / 448, and its codes round m' / scale up or down by chance: with d the
  *   distance of e4m3's numbers at |q|,
  *     |q| -> min( d * floor( |q| / d + u ), 448 ),   u = (b + 1/2) / 2^16,

@@ -79,10 +79,9 @@ def test_adamw_refusals(bits):
     for name in names:
         assert f(**{name: None}) == G.ERR_NULL, name
         assert f(**{name: "null"}) == G.ERR_NULL, name
-        if name not in ("ms", "vs"):
-            assert f(**{name: BAD}) == G.ERR_ALIGN, name
-    if bits == 8:
-        assert f(ms=0x500002) == G.ERR_ALIGN and f(vs=0x600001) == G.ERR_ALIGN
+        if bits == 32 or name not in ("m", "v"):              # codes are bytes
+            assert f(**{name: BAD + 2}) == G.ERR_ALIGN, name
+    assert f(pd=G.BF16, p=0x100001) == G.ERR_ALIGN and f(gd=G.BF16, g=0x200001) == G.ERR_ALIGN
     assert f(how="null") == G.ERR_NULL
     assert f(n=-1) == G.ERR_SHAPE and f(size=-1) == G.ERR_SHAPE and f(size=(1 << 35) + 1) == G.ERR_SHAPE
     for bad in (dict(pd=2), dict(gd=-1), dict(lr=-1.0), dict(lr=math.nan), dict(lr=math.inf), dict(eps=-1e-9),
