@@ -43,17 +43,18 @@ import fp8_moe_grouped_amd as lib
 class MoeLayer:
     """SwiGLU experts behind a top-k softmax router: router f32 [H, E], wi
     bf16 [E, H, 2I] ([gate | up]), wo bf16 [E, I, H].  Training keeps f32 masters
-    of the experts' weights, whose e4m3 codes the products read."""
+    of the experts' weights instead, whose e4m3 codes the products read."""
 
     def __init__(self, router, wi, wo, topk):
         self.router, self.topk = router, topk
+        self.experts = [wi, wo]
         self.wi, self.wo = lib.quantize_fp8_weights(wi), lib.quantize_fp8_weights(wo)
         self.wi4, self.wo4 = lib.quantize_mxfp4_weights(wi), lib.quantize_mxfp4_weights(wo)
 
     def start_training(self, bits=32):
-        """Masters and AdamW's states, in 32 bits or 8."""
-        values = lambda w: lib.dequantize_fp8_codes(*w).float()
-        self.masters = [self.router, values(self.wi), values(self.wo)]
+        """f32 masters of the weights, or those of the training so far, and AdamW's states, in 32 bits or 8."""
+        self.experts = [w.float() for w in self.experts]
+        self.masters = [self.router, *self.experts]
         self.bits, self.step = bits, 0
         self.states = (lib.adamw_8bit_states(self.masters) if bits == 8 else
                        [[torch.zeros_like(w) for w in self.masters] for _ in range(2)])
