@@ -23,6 +23,8 @@ and then the update of the f32 master weights, whose new codes the next step rea
 
     adamw_step([router, wi, wo], gradients, ...)  or  adamw_step_8bit;   quantize_fp8_weights(wi), (wo)
 
+(and quantize_mxfp4_weights, so that decoding follows the training; a program may leave that to the end)
+
 Decoding has no dispatch of its own: the first product gathers its rows.
 
     h = gmm_silu_mxfp4(x, ..., slot_of_row, topk);  y = gmm_mxfp4_fwd(h, ...);  out = moe_combine(y, ...)
@@ -60,12 +62,13 @@ class MoeLayer:
                        [[torch.zeros_like(w) for w in self.masters] for _ in range(2)])
 
     def update(self, gradients, lr, **how):
-        """One AdamW step on (drouter, dwi, dwo), and the experts' new codes."""
+        """One AdamW step on (drouter, dwi, dwo), and the experts' new codes, those for decoding too."""
         self.step += 1
         step = lib.adamw_step_8bit if self.bits == 8 else lib.adamw_step
         step(self.masters, list(gradients), *self.states, lr=lr, step=self.step, **how)
-        for (codes, scales), w in zip((self.wi, self.wo), self.masters[1:]):
+        for w, (codes, scales), (codes4, scales4) in zip(self.experts, (self.wi, self.wo), (self.wi4, self.wo4)):
             lib.quantize_fp8_weights(w, codes=codes, scales=scales)
+            lib.quantize_mxfp4_weights(w.to(torch.bfloat16), codes=codes4, scales=scales4)
 
     def route(self, x):
         logits = x.float() @ self.router
