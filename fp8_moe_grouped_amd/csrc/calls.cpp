@@ -291,10 +291,9 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END
 }
 
-// n numbers of 4 bytes of a tensor's storage, from the at-th, as a tensor of their own
-Tensor piece(const Tensor& whole, int64_t at, int64_t n, at::ScalarType type) {
-  auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
-                                                   c10::scalarTypeToTypeMeta(type));
+// n numbers of 4 bytes of a storage, from the at-th, as a tensor with a made one's keys
+Tensor piece(const Tensor& made, const c10::Storage& of, at::ScalarType type, int64_t at, int64_t n) {
+  auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(of), made.key_set(), c10::scalarTypeToTypeMeta(type));
   impl->set_storage_offset(at);
   impl->set_sizes_contiguous({n});
   return Tensor(std::move(impl));
@@ -312,17 +311,22 @@ PyObject* balance(PyObject*, PyObject* const* a, Py_ssize_t n) {
   PLAIN(in.ok && logits_type(*x) && !ids != !given)
   const int64_t T = x->size(0), E = x->size(1), k = ids ? ids->size(1) : 1;
   PLAIN(T > 0 && E < (1 << 30) && k < (1 << 30) && (!ids || ids->size(0) == T) && (!given || given->size(0) == E))
-  // one allocation for the small outputs: a tensor in it costs the host a fifth of one by itself
-  const int64_t row = (E + 3) / 4 * 4;
-  const Tensor all = in.make({4 + 2 * row}, kI32);
-  const Tensor losses = piece(all, 0, 2, kF32), tokens = piece(all, 2, 1, kI32), probs = piece(all, 4, E, kF32);
-  const Tensor counts = given ? *given : piece(all, 4 + row, E, kI32);
+  // A storage for the small outputs of each type: a tensor in it costs the host a fifth of one by itself.  Not one for
+  // both types: tensors of two types over one storage cannot be saved together.
+  const int64_t row = (E + 3) / 4 * 4, numbers = given ? 1 : row + 1;
+  const Tensor made = in.make({4 + E}, kF32);
+  const c10::Storage& floats = made.storage();
+  c10::Allocator* const from = floats.allocator();
+  const c10::Storage integers(c10::Storage::use_byte_size_t(), 4 * (size_t)numbers, from->allocate(4 * (size_t)numbers),
+                              from, true);
+  const Tensor losses = piece(made, floats, kF32, 0, 2), probs = piece(made, floats, kF32, 4, E);
+  const Tensor counts = given ? *given : piece(made, integers, kI32, 0, E);
+  const Tensor tokens = piece(made, integers, kI32, given ? 0 : row, 1);
   const size_t need = lib.fp8gmm_workspace_bytes(FP8GMM_OP_BALANCE, T, E, k, 1, 0);
-  Tensor ws;
-  if (need) ws = in.make({(int64_t)need}, kU8);
+  const c10::DataPtr ws = need ? from->allocate(need) : c10::DataPtr();
   PLAIN(lib.moe_balance_loss(x->data_ptr(), type_of(*x), ids ? ptr<int32_t>(*ids) : nullptr, T, (int32_t)E,
                              (int32_t)k, ptr<float>(losses), ptr<int32_t>(counts), ptr<float>(probs),
-                             ptr<int32_t>(tokens), need ? ws.data_ptr() : nullptr, need, in.stream()) == FP8GMM_OK)
+                             ptr<int32_t>(tokens), ws.get(), need, in.stream()) == FP8GMM_OK)
   return pack({losses, counts, probs, tokens});
   END
 }
