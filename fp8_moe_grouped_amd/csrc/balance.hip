@@ -7,7 +7,7 @@
 //   dx[t, e]  = p[t, e] (a (c[e] - sum_f p[t, f] c[f]) + b lse[t]) + add[t, e],
 //               a = dlosses[0] E / (n S), b = dlosses[1] 2 / n
 //
-// The gradient takes c[e] = counts[e] - S / E: since sum_f p[t, f] = 1 the value is the
+// The gradient takes c[e] = counts[e] - S / E, in f64: since sum_f p[t, f] = 1 the value is the
 // same, and a nearly even load does not cancel in it.
 //
 // The forward reads the logits once.  A lane keeps its experts' sums over the tokens that
@@ -322,19 +322,20 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* __restric
   load_chunks<L, V, true>(logits + (size_t)t * E, E, at, t < T, WIDE, next);
   if (add) load_chunks<L, V, false>(add + (size_t)t * E, E, at, t < T, WIDE, next_add);
   float c[V];
+  int count[V];
   uint64_t slots = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = expert_of<L, C>(at, i), count = e < E ? max(counts[e], 0) : 0;
-    slots += (uint32_t)count;
-    c[i] = (float)count;
+    const int e = expert_of<L, C>(at, i);
+    count[i] = e < E ? max(counts[e], 0) : 0;
+    slots += (uint32_t)count[i];
   }
-  const float S = (float)reduce<L>((double)slots, [](double a, double b) { return a + b; });
-  const float mean = S / (float)E, n = (float)tokens[0];
-  const float a = n > 0.f && S > 0.f ? dlosses[0] * (float)E / n / S : 0.f;
+  const double S = reduce<L>((double)slots, [](double a, double b) { return a + b; }), mean = S / (double)E;
+  const float n = (float)tokens[0];
+  const float a = n > 0.f && S > 0.0 ? dlosses[0] * (float)E / n / (float)S : 0.f;
   const float b = n > 0.f ? dlosses[1] * 2.f / n : 0.f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) c[i] -= mean;
+  for (int i = 0; i < V; ++i) c[i] = (float)((double)count[i] - mean);   // loads past 2^24 are no f32 numbers
   while (t - sub < T) {
     const int now = t;
     float x[V], old[V], total, lse, dot = 0.f;

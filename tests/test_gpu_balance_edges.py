@@ -1,10 +1,11 @@
-"""GPU tests of what a caller may do with the balance losses' outputs."""
+"""GPU tests of the balance losses where loads are nearly alike, and of what a
+caller may do with their outputs."""
 import io
 
 import pytest
 import torch
 
-from tests.test_gpu_balance import ids_of, logits_of
+from tests.test_gpu_balance import check_grad, ids_of, logits_of
 from tests.test_gpu_calls import Nothing
 
 pytestmark = pytest.mark.gpu
@@ -28,3 +29,18 @@ def test_outputs_can_be_saved(T, given, way, monkeypatch):
         back = torch.load(f, weights_only=True)
         for n in names:
             assert back[n].dtype == getattr(b, n).dtype and torch.equal(back[n], getattr(b, n))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E", [(7, 8), (40, 24), (300, 160), (33, 1000)])
+@pytest.mark.parametrize("base", [1 << 22, (1 << 25) + 1, (1 << 28) + 5, (1 << 31) - 100])
+def test_gradient_of_a_nearly_even_load(base, T, E, dtype):
+    """Loads of many batches that differ by a few slots: their distances from the mean, not their f32 roundings.  The
+    bound is of the distances' magnitudes (see check_grad): a distance is rounded once, and a mean that is off by the
+    same for all experts drops out."""
+    import fp8_moe_grouped_amd as G
+    x = logits_of(T, E, dtype, E)
+    counts = base + torch.randint(-50, 51, (E,), generator=torch.Generator().manual_seed(T)).to(torch.int32)
+    d = torch.tensor([1.0, 0.0])
+    n = torch.tensor([T], dtype=torch.int32)
+    check_grad(G.moe_balance_loss_bwd(d.cuda(), x.cuda(), counts.cuda(), n.cuda()), d, x, counts, T)
