@@ -352,12 +352,18 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* __restric
       x[i] *= share;
       dot += x[i] * c[i];
     }
-    dot = b * lse - a * lanes_sum<L>(dot);
+    const float centre = a * lanes_sum<L>(dot), far = b * lse;
+    if (__builtin_amdgcn_ballot_w64(__builtin_fabsf(far) == __builtin_inff())) {   // logits near f32's largest: p first
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      x[i] = some ? x[i] * __builtin_fmaf(a, c[i], dot) : 0.f;
-      if (add) x[i] += old[i];
+      for (int i = 0; i < V; ++i)
+        x[i] = some ? __builtin_fmaf(x[i] * b, lse, x[i] * __builtin_fmaf(a, c[i], -centre)) : 0.f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = some ? x[i] * __builtin_fmaf(a, c[i], far - centre) : 0.f;
     }
+    if (add)
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] += old[i];
     if (now < T) store_logits<L, V>(dlogits + (size_t)now * E, E, at, WIDE, x);
   }
 }
