@@ -55,13 +55,8 @@ static_assert(sizeof(Tensors<State8>) + sizeof(AdamW) <= 4096, "kernel arguments
 struct Rates {
   float b1, c1, b2, c2, eps, decay, up, root, scale;
 };
-__device__ __forceinline__ double power(double b, int64_t n) {
-  double r = 1.0;
-  for (; n > 0; n >>= 1, b *= b) r = n & 1 ? r * b : r;
-  return r;
-}
-// The step's coefficients.  Those of a step on the device are computed here, by every block: some 20 rounds of
-// three f64 products.
+// The step's coefficients.  Those of a step or rate on the device are computed here, by every thread: they are the
+// host's, in f64 and rounded once.
 __device__ __forceinline__ Rates rates(const AdamW& a, uint32_t& step) {
   Rates r{a.b1, a.c1, a.b2, a.c2, a.eps, a.decay, a.up, a.root, a.grad_scale ? *a.grad_scale : 1.f};
   int64_t t = a.step;
@@ -69,8 +64,8 @@ __device__ __forceinline__ Rates rates(const AdamW& a, uint32_t& step) {
     if (a.step_dev) t = max((int64_t)1, *a.step_dev);
     const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
     r.decay = (float)(lr * a.weight_decay);
-    r.up = (float)(lr / (1.0 - power(a.beta1, t)));
-    r.root = 1.f / sqrtf((float)(1.0 - power(a.beta2, t)));
+    r.up = (float)(lr / one_minus_power(a.log_beta1, t));
+    r.root = (float)(1.0 / sqrt(one_minus_power(a.log_beta2, t)));
   }
   step = (uint32_t)__builtin_amdgcn_readfirstlane((int)t);
   return r;

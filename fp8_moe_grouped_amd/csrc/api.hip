@@ -179,19 +179,18 @@ int check_adamw(int32_t tensors, const int64_t* sizes, void* const* params, int3
 }
 
 AdamW adamw_of(const fp8gmm_adamw& h) {
-  const double t = (double)h.step;
   AdamW a = {};
+  a.log_beta1 = std::log(h.beta1);
+  a.log_beta2 = std::log(h.beta2);
   a.b1 = (float)h.beta1;
   a.c1 = (float)(1.0 - h.beta1);
   a.b2 = (float)h.beta2;
   a.c2 = (float)(1.0 - h.beta2);
   a.eps = (float)h.eps;
   a.decay = (float)(h.lr * h.weight_decay);
-  a.up = (float)(h.lr / (1.0 - std::pow(h.beta1, t)));
-  a.root = (float)(1.0 / std::sqrt(1.0 - std::pow(h.beta2, t)));
+  a.up = (float)(h.lr / one_minus_power(a.log_beta1, h.step));
+  a.root = (float)(1.0 / std::sqrt(one_minus_power(a.log_beta2, h.step)));
   a.lr = h.lr;
-  a.beta1 = h.beta1;
-  a.beta2 = h.beta2;
   a.weight_decay = h.weight_decay;
   a.step = h.step;
   a.lr_dev = h.lr_dev;

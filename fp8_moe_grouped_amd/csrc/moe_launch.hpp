@@ -58,12 +58,15 @@ hipError_t launch_quant_weights_fp8(const void* w, bool bf16, int G, int K, int 
 // 1 / sqrt(1 - beta2^step).  lr_dev and step_dev replace lr and step.
 struct AdamW {
   float b1, c1, b2, c2, eps, decay, up, root;
-  double lr, beta1, beta2, weight_decay;
+  double lr, log_beta1, log_beta2, weight_decay;
   int64_t step;
   const float* lr_dev;
   const int64_t* step_dev;
   const float* grad_scale;
 };
+// 1 - beta^t, on the host and on the device: nothing cancels, so both are a few 2^-53 of it off at any beta (a beta of 0
+// has the logarithm -inf, which gives 1).
+__host__ __device__ inline double one_minus_power(double log_beta, int64_t t) { return -expm1((double)t * log_beta); }
 hipError_t launch_adamw(int tensors, const int64_t* sizes, void* const* params, bool param_bf16,
                         const void* const* grads, bool grad_bf16, float* const* m, float* const* v, const AdamW& how,
                         hipStream_t stream);
