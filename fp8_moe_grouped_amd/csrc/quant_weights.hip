@@ -225,10 +225,15 @@ __global__ __launch_bounds__(256) void clear_words_kernel(v4i* __restrict__ word
 // strips half in: strips of at most kMostParts leave room for two (two of 8 x 16384 x 4096 at once 1.4 ms; in strips of
 // 43 parts 150 and more, every block waiting and reading for the others).
 constexpr int kThreads = 512;
+constexpr int kMostParts = 24;                      // 128 columns or 64: 8 x 16384 x 4096 656, 665
+constexpr int kWideRows = 384, kOtherRows = 768;    // of 128 columns in f32, and of any other cut at least
+constexpr int kWideK = kMostParts * kWideRows;      // the most that strips of 128 columns in f32 are taken for
+static_assert(kMaxK <= kMostParts * kOtherRows, "longer columns have more parts than two calls at once have room for");
 template <typename TW, int LPR, int M>
 hipError_t run(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint32_t* words,
                hipStream_t stream) {
   constexpr int kRows = kThreads / LPR, kMost = kRows * M;
+  static_assert(kMost >= (LPR == 32 ? kWideRows : kOtherRows), "the workspace is counted for these");
   const int strips = N / (LPR * 16 / (int)sizeof(TW)), total = strips * G, parts = (K + kMost - 1) / kMost;
   const int each = ((K + parts - 1) / parts + kRows - 1) / kRows * kRows;   // rows of a part
   if (parts > 1) {
@@ -245,7 +250,6 @@ hipError_t run(const TW* w, int G, int K, int N, int polls, uint8_t* codes, floa
   return hipGetLastError();
 }
 
-constexpr int kMostParts = 24;                      // 128 columns or 64: 8 x 16384 x 4096 656, 665
 template <typename TW>
 hipError_t quantize(const TW* w, int G, int K, int N, int polls, uint8_t* codes, float* scales, uint32_t* words,
                     hipStream_t stream) {
@@ -253,7 +257,7 @@ hipError_t quantize(const TW* w, int G, int K, int N, int polls, uint8_t* codes,
   const auto parts = [K](int rows) { return (K + rows - 1) / rows; };
 #define RUN(L, M) run<TW, L, M>(w, G, K, N, polls, codes, scales, words, stream)
   if constexpr (sizeof(TW) == 4) {
-    if (each >= 1 << 19 && K <= kMostParts * 384) return RUN(32, 24);
+    if (each >= 1 << 19 && K <= kWideK) return RUN(32, 24);
     if (each >= 1 << 16) return RUN(16, 24);
     if (each >= 1 << 13) return RUN(8, 16);
   } else {
@@ -267,8 +271,8 @@ hipError_t quantize(const TW* w, int G, int K, int N, int polls, uint8_t* codes,
 }  // namespace
 
 size_t quant_weights_workspace_bytes(bool bf16, int G, int K, int N) {
-  // the most that any cut needs: a device with another number of CUs gives the same answer
-  const size_t rows = bf16 ? 768 : 384, parts = (K + rows - 1) / rows;
+  // the most that any cut of these columns needs: a device with another number of CUs gives the same answer
+  const size_t rows = !bf16 && K <= kWideK ? kWideRows : kOtherRows, parts = (K + rows - 1) / rows;
   return parts > 1 ? 4 * (size_t)G * N * parts : 0;
 }
 
