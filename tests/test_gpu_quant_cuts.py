@@ -1,6 +1,11 @@
-"""GPU tests of the FP8 weight quantizer's workspace."""
+"""GPU tests of the FP8 weight quantizer's workspace, and of its widest f32
+strips, whose rows are shared by many blocks.  A strip of 128 columns is taken from 2^19 elements a CU
+(256 CUs: G K N >= 2^27) while K <= 9216; a block keeps 384 of its rows, and four
+groups of threads look for the other blocks' maxima, each for every fourth one."""
 import pytest
 import torch
+
+from tests.test_gpu_quant_weights import _launch
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +49,25 @@ def test_a_workspace_of_the_stated_size(G_, K, N, dtype):
     codes, scales = G.quantize_fp8_weights(w, workspace=ws)
     assert bool((ws[need:] == 0xFF).all())
     check(codes, scales, w)
+
+
+@pytest.mark.parametrize("G_,K,N", [(8, 7168, 2432), (5, 9216, 2944), (40, 1536, 2304), (12, 2944, 3968)])
+def test_strips_of_128_columns(G_, K, N):
+    """19 parts, 24 (the most of any cut), 4 and 8."""
+    import fp8_moe_grouped_amd as G
+    w = weights(G_, K, N)
+    check(*G.quantize_fp8_weights(w), w)
+
+
+@pytest.mark.parametrize("G_,K,N", [(8, 7168, 2432), (5, 9216, 2944)])
+def test_wide_strips_that_wait_in_vain(G_, K, N):
+    """With no polls, or one, a block reads the rows of the strip's other blocks itself, a group several of them."""
+    import fp8_moe_grouped_amd as G
+    w = weights(G_, K, N)
+    codes, scales = G.quantize_fp8_weights(w)
+    check(codes, scales, w)
+    for polls in (0, 1):
+        c, s = torch.full_like(codes, 0xAA), torch.full_like(scales, -1.0)
+        words = torch.full((G_ * N * (K // 384 + 1),), -1, dtype=torch.int32, device="cuda")
+        _launch(w, c, s, words, polls)
+        assert torch.equal(c, codes) and torch.equal(s, scales)
