@@ -955,8 +955,10 @@ def _adamw(name, params, grads, states, held, lr, step, betas, eps, weight_decay
     rates = [how.lr, how.eps, how.weight_decay]
     if not all(0 <= v < float("inf") for v in rates) or not all(0 <= b < 1 for b in (how.beta1, how.beta2)):
         raise ValueError(f"lr, eps and weight_decay must be finite and not negative, betas in [0, 1): got {rates}, {betas}")
-    if 0 < how.eps < 2.0 ** -126:
-        raise ValueError(f"eps must be 0 or at least 2^-126, got {eps}")
+    if how.eps != 0 and not 2.0 ** -126 <= how.eps <= 2.0 ** 126:
+        raise ValueError(f"eps must be 0 or from 2^-126 to 2^126, got {eps}")
+    if max(how.lr * how.weight_decay, how.lr / (1 - how.beta1)) > torch.finfo(torch.float32).max:
+        raise ValueError(f"lr * weight_decay and lr / (1 - beta1) must be float32 numbers, got lr {how.lr}")
     if held and not 0 <= seed < 1 << 64:
         raise ValueError(f"seed must fit 64 bits without a sign, got {seed}")
     pointers = [(_P * n)(*(t.data_ptr() for t in l)) for l in columns]

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <limits>
 #include <vector>
 
 #include "../../include/fp8_moe_grouped.h"
@@ -147,7 +148,12 @@ int check_adamw(int32_t tensors, const int64_t* sizes, void* const* params, int3
   if ((!how->lr_dev && !rate(how->lr)) || !rate(how->eps) || !rate(how->weight_decay) || !beta(how->beta1) ||
       !beta(how->beta2) || (!how->step_dev && how->step < 1))
     return FP8GMM_ERR_UNSUPPORTED;
-  if (how->eps > 0.0 && how->eps < 0x1p-126) return FP8GMM_ERR_UNSUPPORTED;   // its reciprocal passes f32
+  // the quotient is a product with a reciprocal, which has to be a normal number
+  if (how->eps != 0.0 && !(how->eps >= 0x1p-126 && how->eps <= 0x1p126)) return FP8GMM_ERR_UNSUPPORTED;
+  // an infinite coefficient would make NaN of a gradient of zero; lr / (1 - beta1^step) is largest at step 1
+  const auto fits = [](double v) { return v <= (double)std::numeric_limits<float>::max(); };
+  if (!how->lr_dev && !(fits(how->lr * how->weight_decay) && fits(how->lr / (1.0 - how->beta1))))
+    return FP8GMM_ERR_UNSUPPORTED;
   try {
     Column columns[N];
     columns[1].written = columns[N - 1].written = false;

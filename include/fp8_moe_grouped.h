@@ -454,8 +454,9 @@ int moe_balance_loss_bwd(const float* dlosses, const void* logits, int32_t dtype
  * coefficients are computed in f64 and rounded to f32.  lr_dev (f32 [1]) and step_dev
  * (i64 [1], values below 1 count as 1) replace lr and step where they are not NULL, for
  * captured graphs; they and grad_scale are device memory, and lr_dev's value is taken as
- * it is.  lr, wd and eps are finite and not negative, eps 0 or at least 2^-126, the
- * betas in [0, 1), step at least 1.  No buffer that the call
+ * it is.  lr, wd and eps are finite and not negative, eps 0 or from 2^-126 to 2^126, lr wd
+ * and lr / (1 - beta1) f32 numbers, the betas in [0, 1), step at least 1
+ * (FP8GMM_ERR_UNSUPPORTED).  No buffer that the call
  * writes may overlap another of its buffers (FP8GMM_ERR_OVERLAP): a tensor is listed
  * once.  Buffers of empty tensors may be NULL, and all need their elements' alignment
  * only: tensors may be pieces of one larger buffer.
