@@ -975,9 +975,10 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr, step, betas=(0.9, 0.
     """One AdamW step over lists of tensors, in place: parameters and gradients
     float32 or bfloat16, states float32.  ``step`` counts from 1.  ``lr`` and
     ``step`` may be tensors of one number on the device (float32, int64), read
-    when the kernels run, for captured graphs; ``grad_scale`` is such a float32
-    tensor that multiplies the gradients.  Tensors may be pieces of one buffer,
-    at any element; one may be listed once."""
+    when the kernels run, for captured graphs, with coefficients rounded as those
+    of the host's numbers; ``grad_scale`` is such a float32 tensor that multiplies
+    the gradients.  Tensors may be pieces of one buffer, at any element; one may be
+    listed once."""
     st = (_calls or _plain()).adamw(params, grads, exp_avgs, exp_avg_sqs, lr, step, *betas, eps, weight_decay,
                                     grad_scale)
     if st is None:
@@ -992,7 +993,8 @@ def adamw_step_8bit(params, grads, exp_avgs, exp_avg_roots, *, lr, step, betas=(
     """adamw_step with states in 8 bits: lists of (codes, scales) as
     adamw_8bit_states makes them, of the first moment and of the second one's
     square root.  Codes are rounded up or down by chance, as ``seed`` and
-    ``step`` decide: the same call on the same tensors gives the same bits."""
+    ``step`` decide: the same call on the same tensors gives the same bits.  The
+    mean of the root is kept; the second moment is held some 5 % too high."""
     seed = int(seed)
     st = (_calls or _plain()).adamw8(params, grads, exp_avgs, exp_avg_roots, lr, step, *betas, eps, weight_decay,
                                      grad_scale, seed)

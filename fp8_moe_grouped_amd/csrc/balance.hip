@@ -306,7 +306,8 @@ __global__ __launch_bounds__(kThreads) void balance_join_kernel(void* __restrict
 
 // Reads the logits (and add) once and writes the gradient: 16384 x 256 f32 with add, 50 MB, in 12.8 us, 9.5 at a copy's
 // rate; blocks that take several tokens each load the next ones' while they compute, two blocks a CU (one or three
-// 13.1 and 13.4 us a call against 12.7, four 15.4).
+// 13.1 and 13.4 us a call against 12.7, four 15.4).  Few tokens (10007 x 160 bf16, 6.8 us) wait for the counts: a lane's V
+// loads of them, behind a condition each, follow one another and hold up the logits that were asked for before them.
 template <int L, int V, typename TX, bool WIDE>
 __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* __restrict__ dlosses,
                                                           const TX* __restrict__ logits,

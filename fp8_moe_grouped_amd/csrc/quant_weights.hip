@@ -9,7 +9,9 @@
 // whole half-lines or more: with 16 columns the codes' 16-byte pieces took as long as half of
 // the reads (8 x 7168 x 4096 f32: 357 us, 228 without the stores).  128 columns of 7168 rows are
 // 3.7 MB, eight times a CU's registers, so a strip's rows are shared by blocks that exchange
-// their maxima (229 us in a row of calls, 5.1 TB/s; two passes over the weights 960).
+// their maxima (229 us in a row of calls, 5.1 TB/s; two passes over the weights 960).  Weights of
+// one round of blocks (8 x 768 x 2048 bf16, 12.3 us) wait for HBM twice: in the compiled
+// kernels a block's first two loads arrive before the rest go out.
 #include "moe_common.hpp"
 #include "moe_launch.hpp"
 

@@ -471,7 +471,10 @@ int moe_balance_loss_bwd(const float* dlosses, const void* logits, int32_t dtype
  *   b 16 bits of a 32-bit hash of (seed, t, place of the tensor in the list, place of
  *   the element): the low half for m, the high half for r.  The mean of the code is the
  *   value, so that changes far below d (0.05 % of r a step with beta2 = 0.999) are not
- *   lost.  An r' above 0 gets the smallest code at least: it divides the next update.
+ *   lost.  That is r's mean: v = r^2 gains the variance of the rounding at each step.  With
+ *   beta2 = 0.999 and gradients of a steady size v is held 5 % too high on average, and
+ *   at 0.47 to 2.1 times its value in 98 of 100 elements, where r is at least 10^-4 of its
+ *   block's largest; 7 % at 10^-5 of it and more, 1.7 times down to 10^-6.  An r' above 0 gets the smallest code at least: it divides the next update.
  *   Blocks with an Inf or NaN get a NaN scale.  Zero states are zero codes and scales.
  *   The hash, modulo 2^32, with mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15;
  *   x *= 0xBB67AE85; x ^= x >> 16, lo and hi the halves of seed, t modulo 2^32:
